@@ -415,6 +415,98 @@ PA_API pa_status pa_decode_noalloc(void* out, const void* q, const void* k_cache
                                    int64_t num_blocks, float scale, int partition_size,
                                    pa_dtype dtype, void* stream);
 
+/*
+ * A K/V cache held in 4 bits ("Reading vLLM's PagedAttention kernel", §3.2 gives the
+ * write a cache dtype and scales; the 4-bit format is this library's choice).
+ *
+ * Format.  A token's row of head_size dims in one kv head is head_size / 16 groups
+ * of 16 consecutive dims.  A group is 16 E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) and one E4M3 scale sf; with the tensor's scale s (k_scale or
+ * v_scale) an element reads back as code * sf * s.  The write computes, every fp32
+ * operation rounded to nearest (even):
+ *     u = max|x| / s,  sf = E4M3(u / 6) clamped to 448,  F = sf * s,
+ *     code = E2M1(x / F), to nearest with ties to even, clamped to +-6
+ * (codes of zero where F is 0).  So a group whose largest element is above 2688 s
+ * saturates there, infinities included; a group with a NaN reads back as NaN; a
+ * group whose largest element is at most 6 * 2^-10 s reads back as zero.  s near
+ * (largest |x| of the tensor) / 2688 uses the scales' full range.
+ *
+ * Pools.  k_cache and v_cache are bytes [num_blocks, num_kv_heads,
+ * pa_fp4_tile_bytes(head_size, block_size)]: 9 / 16 byte per element.  A tile's
+ * bytes are in the order the decode kernel reads; pa_gather_cache_fp4 and
+ * pa_expand_blocks_fp4 are the ways to read one.  Pools need no initialisation:
+ * a slot never written is never read into a result.
+ *
+ * For every call: head_size is 64 or 128 and block_size 16 or 32
+ * (PA_ERR_UNSUPPORTED otherwise); k_scale and v_scale lie in [2^-64, 2^64]
+ * (PA_ERR_INVALID_ARG otherwise); slots, block tables, alignment, errors and
+ * streams as in the calls above.
+ */
+
+/* Bytes of one (block, kv head) tile of an FP4 pool; 0 for unsupported sizes. */
+PA_API size_t pa_fp4_tile_bytes(int head_size, int block_size);
+
+/*
+ * pa_reshape_and_cache into FP4 pools: token t's key and value rows (key_dtype
+ * PA_F32, PA_F16 or PA_BF16) are quantised into slot slot_mapping[t]; nothing else
+ * in the pools changes.  Two tokens of one call must not share a slot (it would then
+ * hold codes and scales of either).
+ */
+PA_API pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, void* k_cache, void* v_cache,
+                                          const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads,
+                                          int head_size, int block_size, int64_t num_blocks, pa_dtype key_dtype,
+                                          float k_scale, float v_scale, void* stream);
+
+/*
+ * The write's inverse: row t of key and value [num_tokens, num_kv_heads, head_size]
+ * (out_dtype PA_F32, PA_F16 or PA_BF16) becomes the rows of slot slot_mapping[t],
+ * code * sf (exact) * s rounded in fp32 and once more to out_dtype.  A slot may
+ * appear any number of times.  The rows of a negative slot, and of one beyond the
+ * pool (recorded as PA_DEVERR_SLOT), are left as they are.
+ */
+PA_API pa_status pa_gather_cache_fp4(void* key, void* value, const void* k_cache, const void* v_cache,
+                                     const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads,
+                                     int head_size, int block_size, int64_t num_blocks, pa_dtype out_dtype,
+                                     float k_scale, float v_scale, void* stream);
+
+/*
+ * Whole blocks read back into a 16-bit pool: for each pair i, block src_dst[2i] of the
+ * FP4 pools (num_blocks of them) becomes block src_dst[2i + 1] of k_out and v_out
+ * (num_out_blocks, the layouts of k_cache and v_cache above, out_dtype PA_F16 or
+ * PA_BF16), every kv head, each element as pa_gather_cache_fp4 gives it.  All slots
+ * of a block are converted, written or not.  This is how pa_prefill attends to a
+ * context held in 4 bits.  A source may repeat, a destination may not.
+ */
+PA_API pa_status pa_expand_blocks_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                                      const int64_t* src_dst, int64_t num_pairs, int num_kv_heads, int head_size,
+                                      int block_size, int64_t num_out_blocks, int64_t num_blocks,
+                                      pa_dtype out_dtype, float k_scale, float v_scale, void* stream);
+
+/* pa_copy_blocks on FP4 pools (the bytes of the tiles). */
+PA_API pa_status pa_copy_blocks_fp4(void* k_cache, void* v_cache, const int64_t* src_dst, int64_t num_pairs,
+                                    int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                                    void* stream);
+
+/* Workspace bytes of pa_decode_fp4 (0 for arguments it would reject, or when it needs none). */
+PA_API size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                           int max_seq_len, int block_size);
+
+/*
+ * pa_decode over FP4 pools: q and out have q_dtype (PA_F16 or PA_BF16), K and V read
+ * back as code * sf * s, exactly.  Scores, softmax statistics and the weighted sum are
+ * fp32, the softmax weights are rounded once to fp16; out is rounded once to q_dtype.
+ * Conditions on sizes, tables and lengths as in pa_decode (no caller partitions); a
+ * sequence whose length lies outside [1, max_seq_len] is recorded as
+ * PA_DEVERR_SEQ_LEN and its rows of out are zero.  Deterministic: equal arguments
+ * give equal bits, whatever the physical placement of the blocks.
+ */
+PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                               int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_size,
+                               int block_size, int64_t num_blocks, float scale, void* workspace,
+                               size_t workspace_bytes, pa_dtype q_dtype, float k_scale, float v_scale,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

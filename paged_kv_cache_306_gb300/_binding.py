@@ -77,6 +77,20 @@ def load():
     lib.pa_decode_step_scaled.argtypes = [P, P, P, P, P, P, P, i64, P, i32, P, i32, i32, i32, i32, i32, i32, i64,
                                           f32, i32, P, sz, i32, i32, f32, f32, P]
     lib.pa_decode_step_scaled.restype = i32
+    # FP4 pools
+    lib.pa_fp4_tile_bytes.argtypes = [i32, i32]
+    lib.pa_fp4_tile_bytes.restype = sz
+    lib.pa_reshape_and_cache_fp4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i64, i32, f32, f32, P]
+    lib.pa_gather_cache_fp4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i64, i32, f32, f32, P]
+    lib.pa_expand_blocks_fp4.argtypes = [P, P, P, P, P, i64, i32, i32, i32, i64, i64, i32, f32, f32, P]
+    lib.pa_copy_blocks_fp4.argtypes = [P, P, P, i64, i32, i32, i32, i64, P]
+    lib.pa_decode_fp4_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.pa_decode_fp4_workspace_size.restype = sz
+    lib.pa_decode_fp4.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i64, f32, P, sz, i32, f32, f32,
+                                  P]
+    for f in (lib.pa_reshape_and_cache_fp4, lib.pa_gather_cache_fp4, lib.pa_expand_blocks_fp4,
+              lib.pa_copy_blocks_fp4, lib.pa_decode_fp4):
+        f.restype = i32
     # host-side block manager (include/pa_block_manager.h)
     lib.pa_bm_create.argtypes = [i64, i32, ctypes.POINTER(P)]
     lib.pa_bm_destroy.argtypes = [P]
@@ -402,6 +416,129 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc
     check(load().pa_prefill(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                             block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc), S, T, max_seq_len, H, hkv,
                             D, bs, nb, float(scale), dtype_code(dt), _stream(stream)))
+
+
+# --- FP4 pools -----------------------------------------------------------------------------------
+
+def pa_fp4_tile_bytes(head_size, block_size):
+    """Bytes of one (block, kv head) tile of an FP4 pool: the pools are uint8
+    [num_blocks, num_kv_heads, pa_fp4_tile_bytes(head_size, block_size)]."""
+    return load().pa_fp4_tile_bytes(head_size, block_size)
+
+
+def _fp4_pools(k_cache, v_cache, num_kv_heads, head_size):
+    """(num_blocks, block_size) of a pair of FP4 pools whose heads and dims are known."""
+    import torch
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need_here(n, t, torch.uint8, 3)
+    if k_cache.shape != v_cache.shape:
+        raise PAError(PA_ERR_INVALID_ARG, "k_cache and v_cache differ in shape")
+    nb, hkv, tile = k_cache.shape
+    if hkv != num_kv_heads:
+        raise PAError(PA_ERR_INVALID_ARG, f"the pools have {hkv} kv heads, the rows {num_kv_heads}")
+    for bs in (16, 32):
+        if tile == pa_fp4_tile_bytes(head_size, bs):
+            return nb, bs
+    raise PAError(PA_ERR_INVALID_ARG, f"no FP4 tile of head size {head_size} has {tile} bytes")
+
+
+def _need_here(name, t, dtype=None, dims=None):
+    """_need_cuda, and on the current device: the library launches there."""
+    import torch
+    _need_cuda(name, t, dtype, dims)
+    if t.device.index != torch.cuda.current_device():
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} is on {t.device}, the current device is "
+                                          f"cuda:{torch.cuda.current_device()}")
+
+
+def _fp4_rows(key, value, k_cache, v_cache, slot_mapping):
+    import torch
+    _need_here("key", key, None, 3)
+    _need_here("value", value, key.dtype, 3)
+    _need_here("slot_mapping", slot_mapping, torch.int64, 1)
+    if value.shape != key.shape or slot_mapping.numel() != key.shape[0]:
+        raise PAError(PA_ERR_INVALID_ARG, "key, value and slot_mapping must have one row per token")
+    T, hkv, d = key.shape
+    nb, bs = _fp4_pools(k_cache, v_cache, hkv, d)
+    return T, hkv, d, bs, nb, dtype_code(key.dtype)
+
+
+def pa_reshape_and_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None):
+    """Quantise key/value [T, Hkv, D] into the FP4 pools through slot_mapping (int64 [T])."""
+    T, hkv, d, bs, nb, code = _fp4_rows(key, value, k_cache, v_cache, slot_mapping)
+    check(load().pa_reshape_and_cache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+                                          T, hkv, d, bs, nb, code, k_scale, v_scale, _stream(stream)))
+
+
+def pa_gather_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None):
+    """Read the rows of slot_mapping (int64 [T]) back into key/value [T, Hkv, D] (fp32, fp16
+    or bf16); the rows of a negative slot stay as they are."""
+    T, hkv, d, bs, nb, code = _fp4_rows(key, value, k_cache, v_cache, slot_mapping)
+    check(load().pa_gather_cache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+                                     T, hkv, d, bs, nb, code, k_scale, v_scale, _stream(stream)))
+
+
+def pa_expand_blocks_fp4(k_out, v_out, k_cache, v_cache, src_dst, k_scale, v_scale, stream=None):
+    """Read whole FP4 blocks back into the 16-bit pools k_out [NB', Hkv, D/8, bs, 8] and v_out
+    [NB', Hkv, D, bs]: src_dst is int64 [n, 2] of (FP4 block, 16-bit block)."""
+    import torch
+    _need_here("k_out", k_out, None, 5)
+    _need_here("v_out", v_out, k_out.dtype, 4)
+    _need_here("src_dst", src_dst, torch.int64)
+    nbo, hkv, d, bs = v_out.shape
+    if k_out.shape != (nbo, hkv, d // 8, bs, 8):
+        raise PAError(PA_ERR_INVALID_ARG, f"k_out must be [{nbo}, {hkv}, {d // 8}, {bs}, 8]")
+    nb, bs4 = _fp4_pools(k_cache, v_cache, hkv, d)
+    if bs4 != bs:
+        raise PAError(PA_ERR_INVALID_ARG, f"block size {bs4} in the FP4 pools, {bs} in the 16-bit pools")
+    check(load().pa_expand_blocks_fp4(_ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache), _ptr(src_dst),
+                                      src_dst.numel() // 2, hkv, d, bs, nbo, nb, dtype_code(k_out.dtype), k_scale,
+                                      v_scale, _stream(stream)))
+
+
+def pa_copy_blocks_fp4(k_cache, v_cache, src_dst, head_size, stream=None):
+    """Copy whole blocks of the FP4 pools: src_dst is int64 [n, 2] of (src, dst)."""
+    import torch
+    _need_here("src_dst", src_dst, torch.int64)
+    hkv = k_cache.shape[1] if k_cache.dim() == 3 else 0
+    nb, bs = _fp4_pools(k_cache, v_cache, hkv, head_size)
+    check(load().pa_copy_blocks_fp4(_ptr(k_cache), _ptr(v_cache), _ptr(src_dst), src_dst.numel() // 2, hkv, head_size,
+                                    bs, nb, _stream(stream)))
+
+
+def pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size):
+    return load().pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size)
+
+
+def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len, k_scale, v_scale,
+                  workspace=None, stream=None):
+    """Decode attention over FP4 pools; writes out [S, H, D] in q's dtype (fp16 or bf16).
+
+    max_seq_len is a host-side bound on seq_lens.  When the call needs a workspace
+    and none is given, one is taken from torch's allocator.  Returns the workspace
+    tensor used (or None).
+    """
+    import torch
+    _need_here("q", q, None, 3)
+    _need_here("out", out, q.dtype, 3)
+    _need_here("block_tables", block_tables, torch.int32, 2)
+    _need_here("seq_lens", seq_lens, torch.int32, 1)
+    S, H, D = q.shape
+    if out.shape != q.shape or block_tables.shape[0] != S or seq_lens.numel() != S:
+        raise PAError(PA_ERR_INVALID_ARG, "q, out, block_tables and seq_lens must agree on the sequences")
+    hkv = k_cache.shape[1] if k_cache.dim() == 3 else 0
+    nb, bs = _fp4_pools(k_cache, v_cache, hkv, D)
+    lib = load()
+    need = lib.pa_decode_fp4_workspace_size(S, H, hkv, D, max_seq_len, bs)
+    workspace = _workspace(need, workspace, q.device, stream)
+    ws_bytes = 0
+    if workspace is not None:
+        _need_here("workspace", workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    check(lib.pa_decode_fp4(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                            block_tables.shape[1], _ptr(seq_lens), S, max_seq_len, H, hkv, D, bs, nb, scale,
+                            _ptr(workspace), ws_bytes, dtype_code(q.dtype), k_scale, v_scale, _stream(stream)))
+    return workspace
 
 
 def pa_get_device_error(stream=None):

@@ -90,6 +90,38 @@ pa_status check_decode_shape(int num_seqs, int num_heads, int num_kv_heads, int 
   return PA_OK;
 }
 
+// Checks shared by the FP4 calls.
+bool fp4_scale_ok(float s) { return s >= 0x1p-64f && s <= 0x1p64f; }
+
+pa_status check_fp4(int num_kv_heads, int head_size, int block_size, int64_t num_blocks, float k_scale, float v_scale) {
+  if (num_kv_heads < 1 || num_blocks < 1) return fail(PA_ERR_INVALID_ARG, "num_kv_heads and num_blocks must be positive");
+  if (num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads %d > 65535", num_kv_heads);
+  if (head_size != 64 && head_size != 128) return fail(PA_ERR_UNSUPPORTED, "head_size %d not in {64, 128}", head_size);
+  if (block_size != 16 && block_size != 32)
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d not in {16, 32}", block_size);
+  if (!fp4_scale_ok(k_scale) || !fp4_scale_ok(v_scale))
+    return fail(PA_ERR_INVALID_ARG, "k_scale and v_scale must lie in [2^-64, 2^64]");
+  return PA_OK;
+}
+
+// The arguments of the calls that go through a slot mapping.
+pa_status check_fp4_rows(const void* key, const void* value, const void* k_cache, const void* v_cache,
+                         const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_size,
+                         pa_dtype dtype) {
+  if (dtype != PA_F32 && dtype != PA_F16 && dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "rows beside an FP4 cache are fp32, fp16 or bf16");
+  if (num_tokens < 0 || num_tokens > 0x7fffffffLL) return fail(PA_ERR_INVALID_ARG, "num_tokens %lld", (long long)num_tokens);
+  // a launch has a thread per group of 16 dims: its grid must stay below 2^31 CTAs
+  if (num_tokens * num_kv_heads > 0x7fffffffLL * (16 * 256 / head_size))
+    return fail(PA_ERR_UNSUPPORTED, "too many rows (%lld tokens, %d kv heads)", (long long)num_tokens, num_kv_heads);
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slot_mapping, 8))
+    return fail(PA_ERR_ALIGNMENT, "key/value/caches need 16-byte, slot_mapping 8-byte alignment");
+  return PA_OK;
+}
+
 // How one pa_decode call is cut into launches and how its workspace is laid out.
 struct DecodePlan {
   pa::DecodeKind kind;
@@ -614,6 +646,150 @@ pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* 
     if (ce != cudaSuccess) return cuda_fail(ce, "prefill launch");
   }
   return PA_OK;
+}
+
+size_t pa_fp4_tile_bytes(int head_size, int block_size) {
+  if ((head_size != 64 && head_size != 128) || (block_size != 16 && block_size != 32)) return 0;
+  return (size_t)block_size * (head_size / 2 + head_size / 16);
+}
+
+pa_status pa_reshape_and_cache_fp4(const void* key, const void* value, void* k_cache, void* v_cache,
+                                   const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_size,
+                                   int block_size, int64_t num_blocks, pa_dtype key_dtype, float k_scale,
+                                   float v_scale, void* stream) {
+  pa_status st = check_fp4(num_kv_heads, head_size, block_size, num_blocks, k_scale, v_scale);
+  if (st == PA_OK)
+    st = check_fp4_rows(key, value, k_cache, v_cache, slot_mapping, num_tokens, num_kv_heads, head_size, key_dtype);
+  if (st != PA_OK || num_tokens == 0) return st;
+  unsigned* err = nullptr;
+  st = device_error_ptr(&err);
+  if (st != PA_OK) return st;
+  int n = 0;
+  const cudaError_t ce = pa::launch_reshape_and_cache_fp4(
+      key, value, k_cache, v_cache, slot_mapping, num_tokens, num_kv_heads, head_size, block_size, num_blocks,
+      static_cast<int>(key_dtype), k_scale, v_scale, err, static_cast<cudaStream_t>(stream), &n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "FP4 reshape_and_cache launch");
+}
+
+pa_status pa_gather_cache_fp4(void* key, void* value, const void* k_cache, const void* v_cache,
+                              const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_size,
+                              int block_size, int64_t num_blocks, pa_dtype out_dtype, float k_scale, float v_scale,
+                              void* stream) {
+  pa_status st = check_fp4(num_kv_heads, head_size, block_size, num_blocks, k_scale, v_scale);
+  if (st == PA_OK)
+    st = check_fp4_rows(key, value, k_cache, v_cache, slot_mapping, num_tokens, num_kv_heads, head_size, out_dtype);
+  if (st != PA_OK || num_tokens == 0) return st;
+  unsigned* err = nullptr;
+  st = device_error_ptr(&err);
+  if (st != PA_OK) return st;
+  int n = 0;
+  const cudaError_t ce = pa::launch_gather_cache_fp4(
+      key, value, k_cache, v_cache, slot_mapping, num_tokens, num_kv_heads, head_size, block_size, num_blocks,
+      static_cast<int>(out_dtype), k_scale, v_scale, err, static_cast<cudaStream_t>(stream), &n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "FP4 gather_cache launch");
+}
+
+pa_status pa_expand_blocks_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                               const int64_t* src_dst, int64_t num_pairs, int num_kv_heads, int head_size,
+                               int block_size, int64_t num_out_blocks, int64_t num_blocks, pa_dtype out_dtype,
+                               float k_scale, float v_scale, void* stream) {
+  pa_status st = check_fp4(num_kv_heads, head_size, block_size, num_blocks, k_scale, v_scale);
+  if (st != PA_OK) return st;
+  if (out_dtype != PA_F16 && out_dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "FP4 blocks are expanded into fp16 or bf16 pools");
+  if (num_out_blocks < 1) return fail(PA_ERR_INVALID_ARG, "num_out_blocks %lld < 1", (long long)num_out_blocks);
+  if (num_pairs < 0 || num_pairs > 0x7fffffffLL) return fail(PA_ERR_INVALID_ARG, "num_pairs %lld", (long long)num_pairs);
+  if (num_pairs == 0) return PA_OK;
+  if (!k_out || !v_out || !k_cache || !v_cache || !src_dst) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(src_dst, 8))
+    return fail(PA_ERR_ALIGNMENT, "pools need 16-byte, src_dst 8-byte alignment");
+  unsigned* err = nullptr;
+  st = device_error_ptr(&err);
+  if (st != PA_OK) return st;
+  int n = 0;
+  const cudaError_t ce = pa::launch_expand_blocks_fp4(
+      k_out, v_out, k_cache, v_cache, src_dst, num_pairs, num_kv_heads, head_size, block_size, num_out_blocks,
+      num_blocks, static_cast<int>(out_dtype), k_scale, v_scale, err, static_cast<cudaStream_t>(stream), &n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "FP4 expand_blocks launch");
+}
+
+pa_status pa_copy_blocks_fp4(void* k_cache, void* v_cache, const int64_t* src_dst, int64_t num_pairs,
+                             int num_kv_heads, int head_size, int block_size, int64_t num_blocks, void* stream) {
+  pa_status st = check_fp4(num_kv_heads, head_size, block_size, num_blocks, 1.f, 1.f);
+  if (st != PA_OK) return st;
+  if (num_pairs < 0 || num_pairs > 0x7fffffffLL) return fail(PA_ERR_INVALID_ARG, "num_pairs %lld", (long long)num_pairs);
+  if (num_pairs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !src_dst) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src_dst, 8))
+    return fail(PA_ERR_ALIGNMENT, "caches need 16-byte, src_dst 8-byte alignment");
+  unsigned* err = nullptr;
+  st = device_error_ptr(&err);
+  if (st != PA_OK) return st;
+  int n = 0;
+  const cudaError_t ce = pa::launch_copy_blocks(
+      k_cache, v_cache, src_dst, num_pairs, (int64_t)num_kv_heads * (int64_t)pa_fp4_tile_bytes(head_size, block_size),
+      num_blocks, err, static_cast<cudaStream_t>(stream), &n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "copy_blocks launch");
+}
+
+size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len,
+                                    int block_size) {
+  if (check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, PA_F16) != PA_OK)
+    return 0;
+  return 0;
+}
+
+pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                        int max_seq_len, int num_heads, int num_kv_heads, int head_size, int block_size,
+                        int64_t num_blocks, float scale, void* workspace, size_t workspace_bytes, pa_dtype q_dtype,
+                        float k_scale, float v_scale, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  if (q_dtype != PA_F16 && q_dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "an FP4 cache is read by fp16 or bf16 queries");
+  pa_status st = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, q_dtype);
+  if (st == PA_OK) st = check_fp4(num_kv_heads, head_size, block_size, num_blocks, k_scale, v_scale);
+  if (st != PA_OK) return st;
+  if (max_blocks_per_seq < 1 || (long long)max_seq_len > (long long)max_blocks_per_seq * block_size)
+    return fail(PA_ERR_INVALID_ARG, "max_seq_len %d exceeds max_blocks_per_seq %d * block_size %d", max_seq_len,
+                max_blocks_per_seq, block_size);
+  const double scale_log2 = static_cast<double>(scale) * k_scale * 1.4426950408889634;
+  if (!std::isfinite(scale) || !std::isfinite(static_cast<float>(scale_log2)))
+    return fail(PA_ERR_INVALID_ARG, "scale (times k_scale) is not finite");
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+    return fail(PA_ERR_ALIGNMENT, "q/out/caches need 16-byte, block_tables/seq_lens 4-byte alignment");
+  pa::Fp4DecodeParams p{};
+  st = device_error_ptr(&p.err);
+  if (st != PA_OK) return st;
+  p.out = out;
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.num_blocks = num_blocks;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.group = num_heads / num_kv_heads;
+  p.max_seq_len = max_seq_len;
+  p.scale_log2 = static_cast<float>(scale_log2);
+  p.out_scale = v_scale;
+  int n = 0;
+  const cudaError_t ce = pa::launch_decode_fp4(q_dtype == PA_BF16, head_size, block_size, p,
+                                               static_cast<cudaStream_t>(stream), &n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "FP4 decode launch");
 }
 
 pa_status pa_get_device_error(int* code, void* stream) {

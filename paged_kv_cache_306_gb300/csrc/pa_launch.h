@@ -197,4 +197,39 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int64_t* src_
                                int64_t block_bytes, int64_t num_blocks, unsigned* err, cudaStream_t stream,
                                int* launches);
 
+// FP4 pools (fp4_cache.cu, fp4_decode.cu).  head_size 64 or 128, block_size 16 or 32.
+cudaError_t launch_reshape_and_cache_fp4(const void* key, const void* value, void* k_cache, void* v_cache,
+                                         const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads,
+                                         int head_size, int block_size, int64_t num_blocks, int key_dtype,
+                                         float k_scale, float v_scale, unsigned* err, cudaStream_t stream,
+                                         int* launches);
+cudaError_t launch_gather_cache_fp4(void* key, void* value, const void* k_cache, const void* v_cache,
+                                    const int64_t* slot_mapping, int64_t num_tokens, int num_kv_heads, int head_size,
+                                    int block_size, int64_t num_blocks, int out_dtype, float k_scale, float v_scale,
+                                    unsigned* err, cudaStream_t stream, int* launches);
+cudaError_t launch_expand_blocks_fp4(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                                     const int64_t* src_dst, int64_t num_pairs, int num_kv_heads, int head_size,
+                                     int block_size, int64_t num_out_blocks, int64_t num_blocks, int out_dtype,
+                                     float k_scale, float v_scale, unsigned* err, cudaStream_t stream, int* launches);
+struct Fp4DecodeParams {
+  void* out;                    // [S, H, D] in the query dtype
+  const void* q;                // [S, H, D]
+  const void* k_cache;          // [NB, Hkv, tile bytes]
+  const void* v_cache;
+  const int32_t* block_tables;  // [S, max_blocks_per_seq]
+  const int32_t* seq_lens;      // [S]
+  unsigned* err;
+  long long num_blocks;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_heads;
+  int num_kv_heads;
+  int group;                    // num_heads / num_kv_heads
+  int max_seq_len;
+  float scale_log2;             // scale * k_scale * log2(e)
+  float out_scale;              // v_scale
+};
+cudaError_t launch_decode_fp4(bool q_is_bf16, int head_size, int block_size, const Fp4DecodeParams& p,
+                              cudaStream_t stream, int* launches);
+
 }  // namespace pa

@@ -1,0 +1,566 @@
+"""GPU parity of the FP4 cache calls against the oracle (oracle/fp4.py and the fp64 decode).
+
+The write and the reads back are exact: the tiles' bytes, and the values rounded as
+documented.  Decode is held to a bound derived per output row.  With w the exact
+softmax weights, A = sum_t w_t |v_t|, L tokens and D dims:
+  * a weight is rounded once to fp16: 2^-11 of it, or at most 2^-25 of the largest weight
+    when it is below fp16's normal range -- 2^-11 A + L 2^-24 max|v| with room for the second;
+  * a score is a sum of D fp32 products scaled once: off by at most
+    d = (D + 8) 2^-23 * scale * |q| max|k| + 2^-20 (the exponential's own error included), which moves
+    weights and their sum by that factor each -- 2 d A;
+  * the weighted sums are accumulated in fp32, at most one addition per 8 tokens and a merge
+    of partial results -- (L / 8 + 64) 2^-22 A;
+  * the output is rounded once: half a step of its type.
+"""
+import math
+import zlib
+
+import numpy as np
+import pytest
+
+import oracle
+import workloads as W
+from helpers import TOL, as_f64, half_ulp, same_bytes
+from oracle import fp4
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+KS, VS = 0.0173, 0.0214
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import paged_kv_cache_306_gb300 as pa
+    pa.load()
+
+
+def rng_of(*key):
+    return np.random.default_rng(zlib.crc32(repr(key).encode()))
+
+
+def store(x, dtype):
+    """float32 values rounded to the dtype: (numpy storage, float64 values)."""
+    with np.errstate(over="ignore"):
+        a = W.cast(np.asarray(x, np.float32), dtype)
+    return a, oracle.widen(a, dtype)
+
+
+def cuda(a, dtype=None):
+    return W.to_torch(a, dtype, "cuda") if dtype else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def no_error():
+    import paged_kv_cache_306_gb300 as pa
+    code = pa.pa_get_device_error()
+    assert code == 0, pa.DEVICE_ERRORS[code]
+
+
+def rounded(v64, dtype):
+    """fl_T(fl32(v)): what a read gives for an exact value."""
+    with np.errstate(over="ignore"):
+        return oracle.widen(W.cast(v64.astype(np.float32), dtype), dtype)
+
+
+def random_pool(rng, NB, Hkv, D, bs, s, of, std=1.0):
+    """(tiles, logical codes, logical scales): quantised normal rows whose channels differ in size."""
+    x = rng.standard_normal((NB, Hkv, bs, D)).astype(np.float32) * std
+    x *= np.exp(0.7 * rng.standard_normal((1, Hkv, 1, D))).astype(np.float32)
+    c, f = fp4.quantise(x.astype(np.float64), s)
+    return fp4.pack(c, f, of), c, f
+
+
+# --- the write -----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,bs", [(64, 16), (64, 32), (128, 16), (128, 32)])
+@pytest.mark.parametrize("scales", [(KS, VS), (2.0 ** -6, 2.0 ** -7), (1.0, 3.0e-5)])
+def test_write_is_exact_and_touches_nothing_else(dtype, D, bs, scales):
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of(dtype, D, bs, scales)
+    NB, Hkv, T = 23, 3, 77
+    x = rng.standard_normal((2, T, Hkv, D)).astype(np.float32)
+    x[:, :40] *= np.exp(2 * rng.standard_normal((2, 40, Hkv, D // 16))).repeat(16, -1)
+    x[:, 8:16] *= 2.0 ** -11 * scales[0]         # scales that are subnormal codes, or zero
+    x[:, 16:20] *= 2.0e4 * scales[0]             # past the largest code
+    x[:, 20] = 0.0
+    x[:, 21] = -0.0
+    x[:, 22, :, 5] = np.nan
+    x[:, 23, :, 17] = np.inf
+    x[:, 24, :, 33] = -np.inf
+    x[:, 25] = np.round(x[:, 25] * 4) / 4        # ties between codes
+    x[:, 25, :, ::16] = 6.0
+    (key, k64), (value, v64) = store(x[0], dtype), store(x[1], dtype)
+    slots = rng.permutation(NB * bs)[:T].astype(np.int64)
+    slots[[3, 11]] = -1
+    slots[12] = -(1 << 40)
+    before = rng.integers(0, 256, (2, NB, Hkv, fp4.tile_bytes(D, bs)), dtype=np.uint8)
+    kt, vt = cuda(before[0]), cuda(before[1])
+    pa.pa_reshape_and_cache_fp4(cuda(key, dtype), cuda(value, dtype), kt, vt, cuda(slots), *scales)
+    no_error()
+    for of, got, rows, s, b in (("k", kt, k64, scales[0], before[0]), ("v", vt, v64, scales[1], before[1])):
+        logical = fp4.unpack(b, D, bs, of)
+        fp4.write(rows, logical, slots, s)
+        assert np.array_equal(got.cpu().numpy(), fp4.pack(*logical, of)), of
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_write_and_read_of_many_rows(dtype):
+    """More rows than a wave of CTAs; every fp16 / bf16 mantissa meets every scale mantissa many times."""
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("many", dtype)
+    NB, Hkv, D, bs, T = 1300, 5, 128, 16, 20001
+    x = (rng.standard_normal((2, T, Hkv, D)) * np.exp(rng.standard_normal((2, T, Hkv, 1)))).astype(np.float32)
+    (key, k64), (value, v64) = store(x[0], dtype), store(x[1], dtype)
+    slots = rng.permutation(NB * bs)[:T].astype(np.int64)
+    kt = torch.zeros(NB, Hkv, fp4.tile_bytes(D, bs), dtype=torch.uint8, device="cuda")
+    vt = torch.zeros_like(kt)
+    st = cuda(slots)
+    pa.pa_reshape_and_cache_fp4(cuda(key, dtype), cuda(value, dtype), kt, vt, st, KS, VS)
+    rk, rv = torch.empty_like(cuda(key, dtype)), torch.empty_like(cuda(key, dtype))
+    pa.pa_gather_cache_fp4(rk, rv, kt, vt, st, KS, VS)
+    no_error()
+    for got, rows, s in ((rk, k64, KS), (rv, v64, VS)):
+        want = rounded(fp4.values(*fp4.quantise(rows, s), s), dtype)
+        assert np.array_equal(oracle.widen(W.from_torch(got, dtype), dtype), want)
+
+
+def test_write_reports_a_slot_beyond_the_pool_and_writes_the_others():
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("slot")
+    NB, Hkv, D, bs = 4, 2, 64, 16
+    key, k64 = store(rng.standard_normal((4, Hkv, D)), "f16")
+    kt = torch.zeros(NB, Hkv, fp4.tile_bytes(D, bs), dtype=torch.uint8, device="cuda")
+    vt = torch.zeros_like(kt)
+    slots = np.array([5, NB * bs, 1 << 45, 63], np.int64)
+    pa.pa_reshape_and_cache_fp4(cuda(key, "f16"), cuda(key, "f16"), kt, vt, cuda(slots), KS, KS)
+    assert pa.pa_get_device_error() == 3
+    for of, got in (("k", kt), ("v", vt)):
+        logical = fp4.unpack(np.zeros((NB, Hkv, fp4.tile_bytes(D, bs)), np.uint8), D, bs, of)
+        fp4.write(k64, logical, [5, -1, -1, 63], KS)
+        assert np.array_equal(got.cpu().numpy(), fp4.pack(*logical, of))
+
+
+# --- the reads back -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,bs", [(64, 16), (64, 32), (128, 16), (128, 32)])
+def test_gather_is_exact_and_leaves_padded_rows(dtype, D, bs):
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("gather", dtype, D, bs)
+    NB, Hkv, T = 9, 3, 133
+    tiles = rng.integers(0, 256, (2, NB, Hkv, fp4.tile_bytes(D, bs)), dtype=np.uint8)   # any codes, any scale bytes
+    slots = rng.integers(0, NB * bs, T).astype(np.int64)                                # repeats among them
+    slots[[0, 50, T - 1]] = [-1, NB * bs, -7]
+    rows = torch.full((2, T + 2, Hkv, D), 7.0, device="cuda").to(torch.float32 if dtype == "f32" else
+                                                                 torch.float16 if dtype == "f16" else torch.bfloat16)
+    pa.pa_gather_cache_fp4(rows[0, 1:-1], rows[1, 1:-1], cuda(tiles[0]), cuda(tiles[1]), cuda(slots), KS, VS)
+    assert pa.pa_get_device_error() == 3
+    for got, of, t, s in ((rows[0], "k", tiles[0], KS), (rows[1], "v", tiles[1], VS)):
+        want = np.full((T + 2, Hkv, D), 7.0)
+        v = rounded(fp4.pool_values(t, D, bs, of, s), dtype)
+        for i, slot in enumerate(slots):
+            if 0 <= slot < NB * bs:
+                want[i + 1] = v[slot // bs, :, slot % bs]
+        assert np.array_equal(oracle.widen(W.from_torch(got, dtype), dtype), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,bs", [(64, 16), (64, 32), (128, 16), (128, 32)])
+def test_expand_is_exact_and_touches_nothing_else(dtype, D, bs):
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("expand", dtype, D, bs)
+    NB, NBO, Hkv = 11, 17, 3
+    tiles = rng.integers(0, 256, (2, NB, Hkv, fp4.tile_bytes(D, bs)), dtype=np.uint8)
+    pairs = np.stack([rng.integers(0, NB, 9), rng.permutation(NBO)[:9]], 1).astype(np.int64)
+    pairs = np.concatenate([pairs, [[NB, 3], [-1, 3], [2, NBO], [2, -5]]])                # four refused on the device
+    td = torch.float16 if dtype == "f16" else torch.bfloat16
+    ko = torch.full((NBO, Hkv, D // 8, bs, 8), 7.0, dtype=td, device="cuda")
+    vo = torch.full((NBO, Hkv, D, bs), 7.0, dtype=td, device="cuda")
+    pa.pa_expand_blocks_fp4(ko, vo, cuda(tiles[0]), cuda(tiles[1]), cuda(pairs), KS, VS)
+    assert pa.pa_get_device_error() == 5
+    k, v = np.full(ko.shape, 7.0), np.full(vo.shape, 7.0)
+    kx = rounded(fp4.pool_values(tiles[0], D, bs, "k", KS), dtype)
+    vx = rounded(fp4.pool_values(tiles[1], D, bs, "v", VS), dtype)
+    for s, d in pairs[:9]:
+        k[d] = kx[s].reshape(Hkv, bs, D // 8, 8).transpose(0, 2, 1, 3)
+        v[d] = vx[s].transpose(0, 2, 1)
+    assert np.array_equal(oracle.widen(W.from_torch(ko, dtype), dtype), k, equal_nan=True)
+    assert np.array_equal(oracle.widen(W.from_torch(vo, dtype), dtype), v, equal_nan=True)
+
+
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 32)])
+def test_copy_blocks_moves_tiles(D, bs):
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("copy", D, bs)
+    before = rng.integers(0, 256, (2, 12, 5, fp4.tile_bytes(D, bs)), dtype=np.uint8)
+    kt, vt = cuda(before[0]), cuda(before[1])
+    pairs = np.array([[0, 7], [0, 8], [3, 11]], np.int64)
+    pa.pa_copy_blocks_fp4(kt, vt, cuda(pairs), D)
+    no_error()
+    want = before.copy()
+    for s, d in pairs:
+        want[:, d] = before[:, s]
+    assert np.array_equal(kt.cpu().numpy(), want[0]) and np.array_equal(vt.cpu().numpy(), want[1])
+
+
+# --- decode ------------------------------------------------------------------------------------------
+
+class Case:
+    """Sequences over shuffled blocks of random FP4 pools; slots past a sequence's end hold NaN scales."""
+
+    def __init__(self, lens, G, Hkv, D, bs, q_dtype, *key, q_std=1.0, extra=3, std=1.0):
+        rng = rng_of("decode", tuple(lens[:4]), len(lens), G, Hkv, D, bs, q_dtype, *key)
+        self.lens, self.D, self.bs, self.Hkv, self.q_dtype = list(lens), D, bs, Hkv, q_dtype
+        n = [-(-L // bs) for L in lens]
+        NB = sum(n) + extra
+        perm = rng.permutation(NB).astype(np.int32)
+        self.table = np.full((len(lens), max(n) + 1), -1, np.int32)
+        at = 0
+        self.pools = []
+        for of, s in (("k", KS), ("v", VS)):
+            _, c, f = random_pool(rng, NB, Hkv, D, bs, s, of, std)
+            self.pools.append((c, f))
+        for i, m in enumerate(n):
+            self.table[i, :m] = perm[at:at + m]
+            at += m
+            if m and lens[i] % bs:
+                for c, f in self.pools:
+                    c[self.table[i, m - 1], :, lens[i] % bs:] = 7
+                    f[self.table[i, m - 1], :, lens[i] % bs:] = fp4.NAN_SCALE
+        self.k, self.v = (fp4.pack(c, f, of) for (c, f), of in zip(self.pools, "kv"))
+        q = rng.standard_normal((len(lens), G * Hkv, D)).astype(np.float32) * q_std
+        self.q, self.q64 = store(q, q_dtype)
+        self.scale = 1 / math.sqrt(D)
+        self.max_len = max(max(lens), 1)
+
+    def upload(self):
+        return dict(q=cuda(self.q, self.q_dtype), k=cuda(self.k), v=cuda(self.v), table=cuda(self.table),
+                    lens=cuda(np.array(self.lens, np.int32)))
+
+    def run(self, t=None, out=None, max_len=None, **kw):
+        import paged_kv_cache_306_gb300 as pa
+        t = self.upload() if t is None else t
+        out = torch.full_like(t["q"], math.nan) if out is None else out
+        pa.pa_decode_fp4(out, t["q"], t["k"], t["v"], t["table"], t["lens"], self.scale, max_len or self.max_len, KS,
+                         VS, **kw)
+        return out
+
+    def reference(self, seqs=None):
+        """(exact out, bound without the final rounding) [n, H, D]."""
+        seqs = range(len(self.lens)) if seqs is None else seqs
+        k64, v64 = fp4.f64_pools(self.k, self.v, self.D, self.bs, KS, VS)
+        table, lens = self.table[list(seqs)], np.array(self.lens, np.int32)[list(seqs)]
+        q = np.ascontiguousarray(self.q[list(seqs)])
+        args = (table, lens, self.scale, "f64")
+        out = oracle.decode(q, k64, v64, *args, q_dtype=self.q_dtype)
+        mass = oracle.decode(q, k64, np.abs(v64), *args, q_dtype=self.q_dtype)
+        kn = np.nanmax(np.sqrt((np.moveaxis(k64, 3, 2).reshape(*k64.shape[:2], self.bs, -1) ** 2).sum(-1)))
+        qn = np.sqrt((self.q64[list(seqs)] ** 2).sum(-1, keepdims=True))
+        d = (self.D + 8) * 2.0 ** -23 * self.scale * qn * kn + 2.0 ** -20
+        L = lens.astype(np.float64)[:, None, None]
+        rel = 2.0 ** -11 + 2 * d + (L / 8 + 64) * 2.0 ** -22
+        return out, rel * mass + L * 2.0 ** -24 * np.nanmax(np.abs(v64))
+
+    def check(self, out, seqs=None):
+        got = as_f64(out)
+        got = got if seqs is None else got[list(seqs)]
+        ref, bound = self.reference(seqs)
+        assert np.isfinite(got).all()
+        excess = np.abs(got - ref) - bound - half_ulp(np.abs(ref) + bound, self.q_dtype)
+        assert excess.max() <= 0, f"off by {np.abs(got - ref).max():.3e}, {excess.max():.3e} past the bound"
+
+
+EDGES = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 127, 130, 300]
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,bs", [(64, 16), (64, 32), (128, 16), (128, 32)])
+@pytest.mark.parametrize("G", [1, 2, 3, 7, 8, 9, 16, 17, 40])
+def test_decode_lengths_and_groups(q_dtype, D, bs, G):
+    c = Case(EDGES, G, 2, D, bs, q_dtype)
+    out = c.run()
+    no_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("q_dtype,D,bs,G,Hkv,lens", [
+    ("f16", 128, 16, 7, 4, [4096, 512, 1000, 2047, 1]),
+    ("bf16", 128, 16, 4, 8, [9001]),
+    ("bf16", 64, 32, 10, 1, [20000, 3]),
+    ("f16", 64, 16, 1, 5, [1, 1, 1, 7000, 1]),
+    ("f16", 128, 32, 20, 1, [5000, 4999, 5001]),
+    ("f16", 128, 16, 1, 32, [513, 600]),
+])
+def test_decode_long_and_ragged(q_dtype, D, bs, G, Hkv, lens):
+    c = Case(lens, G, Hkv, D, bs, q_dtype)
+    out = c.run()
+    no_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("S,G,Hkv,D,bs", [(1, 4, 2, 128, 16), (1500, 2, 2, 64, 16), (2100, 1, 1, 128, 32),
+                                         (1024, 8, 1, 64, 32), (1025, 16, 1, 64, 16)])
+def test_decode_many_sequences(S, G, Hkv, D, bs):
+    rng = rng_of("many", S)
+    c = Case([int(x) for x in rng.integers(1, 90, S)], G, Hkv, D, bs, "f16")
+    out = c.run()
+    no_error()
+    c.check(out)
+
+
+def test_decode_with_a_loose_length_bound():
+    """max_seq_len far above the lengths: the tables are wide, the sequences short."""
+    c = Case([5, 40, 100], 4, 2, 128, 16, "f16")
+    c.table = np.concatenate([c.table, np.full((3, 3000), -1, np.int32)], 1)
+    out = c.run(max_len=16 * 2000)
+    no_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+def test_decode_heads_of_very_different_size(q_dtype):
+    """bf16 heads from 2^-20 to 2^20 (fp16 from 2^-10 to 2^6), peaked softmaxes among them."""
+    c = Case([1, 77, 200], 8, 2, 128, 16, q_dtype)
+    span = np.linspace(-20, 20, 16) if q_dtype == "bf16" else np.linspace(-10, 6, 16)
+    c.q, c.q64 = store(oracle.widen(c.q, q_dtype).astype(np.float32) * (2.0 ** np.round(span))[None, :, None], q_dtype)
+    out = c.run()
+    no_error()
+    got = as_f64(out)
+    ref, bound = c.reference()
+    # a peaked head's weights move with the score's error: heads whose error exceeds 1/8 are held to the range of V
+    fine = bound < 0.125 * np.abs(ref).max()
+    excess = np.abs(got - ref) - bound - half_ulp(np.abs(ref) + bound, q_dtype)
+    assert np.isfinite(got).all() and fine.mean() > 0.4 and excess[fine].max() <= 0
+
+
+def test_lengths_outside_the_contract_give_zero_rows_and_an_error():
+    import paged_kv_cache_306_gb300 as pa
+    c = Case([40, 17, 90, 33], 4, 2, 64, 16, "f16")
+    t = c.upload()
+    t["lens"] = cuda(np.array([40, 0, -3, 91], np.int32))
+    out = c.run(t)
+    assert pa.pa_get_device_error() == 2
+    assert not out[1:].any()
+    c.check(out, [0])
+    t["lens"].zero_()
+    out = c.run(t)
+    assert pa.pa_get_device_error() == 2 and not out.any()
+
+
+def test_block_ids_outside_the_pool_are_reported():
+    import paged_kv_cache_306_gb300 as pa
+    for bad in (-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1):
+        c = Case([40, 90, 100], 4, 2, 64, 16, "f16")
+        c.table[1, 3] = bad
+        out = c.run()
+        assert pa.pa_get_device_error() == 1
+        c.check(out, [0, 2])
+
+
+def test_placement_and_repetition_do_not_change_a_bit():
+    c = Case([700, 33, 1, 4000], 7, 2, 128, 16, "bf16", extra=40)
+    a = c.run()
+    assert same_bytes(a, c.run())
+    rng = rng_of("move")
+    to = rng.permutation(len(c.k)).astype(np.int32)
+    k, v = np.empty_like(c.k), np.empty_like(c.v)
+    k[to], v[to] = c.k, c.v
+    c.k, c.v, c.table = k, v, np.where(c.table >= 0, to[c.table], -1).astype(np.int32)
+    assert same_bytes(a, c.run())
+    no_error()
+
+
+def test_decode_writes_only_its_rows_and_its_workspace():
+    import paged_kv_cache_306_gb300 as pa
+    c = Case([700, 33, 1, 1500], 10, 2, 128, 16, "f16")
+    t = c.upload()
+    big = torch.full((8,) + t["q"].shape[1:], math.nan, dtype=torch.float16, device="cuda")
+    need = pa.pa_decode_fp4_workspace_size(4, 20, 2, 128, c.max_len, 16)
+    ws = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    before = {n: x.clone() for n, x in t.items()}
+    c.run(t, out=big[2:6], workspace=ws[256:256 + need] if need else None)
+    no_error()
+    assert torch.isnan(big[:2]).all() and torch.isnan(big[6:]).all()
+    assert bool((ws[:256] == 0xA5).all()) and bool((ws[256 + need:] == 0xA5).all())
+    assert all(same_bytes(before[n], t[n]) for n in t)
+    c.check(big[2:6])
+
+
+def test_a_short_workspace_is_refused():
+    import paged_kv_cache_306_gb300 as pa
+    c = Case([1000, 800], 4, 2, 128, 16, "f16")
+    t = c.upload()
+    need = pa.pa_decode_fp4_workspace_size(2, 8, 2, 128, c.max_len, 16)
+    if not need:
+        return
+    lib, B = pa.load(), pa._binding
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(t["q"])
+    for ptr, n, status in ((ws.data_ptr(), need - 1, B.PA_ERR_WORKSPACE), (0, need, B.PA_ERR_WORKSPACE),
+                           (ws.data_ptr() + 8, need, B.PA_ERR_ALIGNMENT)):
+        st = lib.pa_decode_fp4(out.data_ptr(), t["q"].data_ptr(), t["k"].data_ptr(), t["v"].data_ptr(),
+                               t["table"].data_ptr(), t["table"].shape[1], t["lens"].data_ptr(), 2, c.max_len, 8, 2,
+                               128, 16, c.k.shape[0], c.scale, ptr, n, B.PA_F16, KS, VS, None)
+        assert st == status
+
+
+def test_a_captured_call_follows_its_inputs():
+    """One captured call replayed over growing, shrinking and equal batches; the workspace and the pools
+    keep what the last replay left."""
+    import paged_kv_cache_306_gb300 as pa
+    cases = [Case(lens, 4, 2, 128, 16, "f16", extra=0) for lens in
+             ([3000, 1, 500, 2999], [1, 1, 1, 1], [2000, 2000, 2000, 2000], [17, 3000, 1, 64], [1, 1, 1, 3000])]
+    blocks = max(len(c.k) for c in cases)
+    width = max(c.table.shape[1] for c in cases)
+    t = dict(q=torch.empty(4, 8, 128, dtype=torch.float16, device="cuda"),
+             k=torch.empty((blocks,) + cases[0].k.shape[1:], dtype=torch.uint8, device="cuda"),
+             table=torch.full((4, width), -1, dtype=torch.int32, device="cuda"),
+             lens=torch.ones(4, dtype=torch.int32, device="cuda"))
+    t["v"] = torch.empty_like(t["k"])
+
+    def load(c):
+        u = c.upload()
+        for n in ("q", "lens"):
+            t[n].copy_(u[n])
+        t["table"].fill_(-1)
+        t["table"][:, :c.table.shape[1]] = u["table"]
+        for n in ("k", "v"):
+            t[n][:len(c.k)] = u[n]
+
+    out = torch.empty_like(t["q"])
+    need = pa.pa_decode_fp4_workspace_size(4, 8, 2, 128, 3000, 16)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    load(cases[0])
+    cases[0].run(t, out=out, max_len=3000, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cases[0].run(t, out=out, max_len=3000, workspace=ws)
+    for c in cases + cases[::-1]:
+        load(c)
+        out.fill_(math.nan)
+        g.replay()
+        no_error()
+        c.check(out)
+
+
+def test_calls_on_two_streams_with_their_own_workspaces():
+    cases = [Case([2500, 100, 64], 4, 2, 128, 16, "f16"), Case([300, 2500], 4, 4, 128, 16, "f16", 2)]
+    ts = [c.upload() for c in cases]
+    outs = [torch.full_like(t["q"], math.nan) for t in ts]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, t, o, s in zip(cases, ts, outs, streams):
+            c.run(t, out=o, stream=s)      # each takes a workspace of its own, on a stream that is not current
+    torch.cuda.synchronize()
+    no_error()
+    for c, o in zip(cases, outs):
+        c.check(o)
+
+
+def test_pools_past_32_bit_offsets():
+    """Blocks at the end of pools of more than 4 GiB each: the write, both reads and decode."""
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("far")
+    Hkv, D, bs, L = 8, 128, 32, 100
+    NB = (1 << 32) // (Hkv * fp4.tile_bytes(D, bs)) + 5000
+    kt = torch.empty(NB, Hkv, fp4.tile_bytes(D, bs), dtype=torch.uint8, device="cuda")
+    vt = torch.empty_like(kt)
+    blocks = np.array([NB - 1, NB - 3, 2, NB - 2])
+    slots = np.array([int(blocks[t // bs]) * bs + t % bs for t in range(L)], np.int64)
+    (key, k64), (value, v64) = (store(rng.standard_normal((L, Hkv, D)), "f16") for _ in range(2))
+    pa.pa_reshape_and_cache_fp4(cuda(key, "f16"), cuda(value, "f16"), kt, vt, cuda(slots), KS, VS)
+    rk, rv = torch.empty(2, L, Hkv, D, dtype=torch.float16, device="cuda")
+    pa.pa_gather_cache_fp4(rk, rv, kt, vt, cuda(slots), KS, VS)
+    no_error()
+    want = fp4.values(*fp4.quantise(k64, KS), KS), fp4.values(*fp4.quantise(v64, VS), VS)
+    assert np.array_equal(as_f64(rk), rounded(want[0], "f16")) and np.array_equal(as_f64(rv), rounded(want[1], "f16"))
+    ko = torch.zeros(5, Hkv, D // 8, bs, 8, dtype=torch.float16, device="cuda")
+    vo = torch.zeros(5, Hkv, D, bs, dtype=torch.float16, device="cuda")
+    pa.pa_expand_blocks_fp4(ko, vo, kt, vt, cuda(np.array([[NB - 3, 4]], np.int64)), KS, VS)
+    no_error()
+    assert np.array_equal(as_f64(vo[4]).transpose(2, 0, 1), rounded(want[1][32:64], "f16"))
+    c = Case([L], 2, Hkv, D, bs, "f16", "far", extra=0)
+    c.table = np.arange(4, dtype=np.int32)[None]
+    small = [torch.stack([p[int(b)] for b in blocks]) for p in (kt, vt)]
+    c.k, c.v = (p.cpu().numpy() for p in small)
+    for p, of in ((c.k, "k"), (c.v, "v")):   # what lies past the sequence was never written: give it values for the bound
+        codes, f = fp4.unpack(p, D, bs, of)
+        f[3, :, L - 96:] = 0
+        p[...] = fp4.pack(codes, f, of)
+    t = c.upload()
+    t.update(k=kt, v=vt, table=cuda(blocks.astype(np.int32)[None]))
+    out = c.run(t)
+    no_error()
+    c.check(out)
+
+
+# --- as they are used together ------------------------------------------------------------------------
+
+def test_a_serving_run_over_an_fp4_cache():
+    """Prompts in two chunks (quantising write; the context expanded for pa_prefill), then a fork and steps
+    of copy-on-write, write and decode, the block manager handing out the blocks."""
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("serve")
+    Hkv, G, D, bs, NB = 2, 4, 128, 16, 64
+    H, scale = Hkv * G, 1 / math.sqrt(D)
+    bm = pa.BlockManager(NB, bs)
+    kt = torch.full((NB, Hkv, fp4.tile_bytes(D, bs)), 0xFF, dtype=torch.uint8, device="cuda")
+    vt = torch.full_like(kt, 0xFF)
+    logical = [fp4.unpack(kt.cpu().numpy(), D, bs, "k"), fp4.unpack(vt.cpu().numpy(), D, bs, "v")]
+    rows = {}
+
+    def write(slots):
+        (key, k64), (value, v64) = (store(rng.standard_normal((len(slots), Hkv, D)), "f16") for _ in range(2))
+        pa.pa_reshape_and_cache_fp4(cuda(key, "f16"), cuda(value, "f16"), kt, vt, cuda(slots), KS, VS)
+        fp4.write(k64, logical[0], slots, KS)
+        fp4.write(v64, logical[1], slots, VS)
+
+    def pools64():
+        return fp4.f64_pools(fp4.pack(*logical[0], "k"), fp4.pack(*logical[1], "v"), D, bs, KS, VS)
+
+    # prompts: the second chunk attends to everything through 16-bit copies of the blocks
+    for sid, n in ((0, 100), (1, 37)):
+        rows[sid] = bm.add_sequence(sid, n)
+    first = {0: 60, 1: 5}
+    write(np.concatenate([rows[s][:first[s]] for s in (0, 1)]))
+    write(np.concatenate([rows[s][first[s]:] for s in (0, 1)]))
+    table, lens = bm.block_tables([0, 1], 8)
+    used = np.unique(table[table >= 0]).astype(np.int64)
+    ko = torch.zeros(NB, Hkv, D // 8, bs, 8, dtype=torch.float16, device="cuda")
+    vo = torch.zeros(NB, Hkv, D, bs, dtype=torch.float16, device="cuda")
+    pa.pa_expand_blocks_fp4(ko, vo, kt, vt, cuda(np.stack([used, used], 1)), KS, VS)
+    qsl = np.array([0, 40, 72], np.int32)
+    q = store(rng.standard_normal((72, H, D)), "f16")[0]
+    out = torch.empty(72, H, D, dtype=torch.float16, device="cuda")
+    pa.pa_prefill(out, cuda(q, "f16"), ko, vo, cuda(table), cuda(lens), cuda(qsl), scale, int(lens.max()))
+    no_error()
+    k16 = W.from_torch(ko, "f16")
+    v16 = W.from_torch(vo, "f16")
+    ref = oracle.prefill(q, k16, v16, table, lens, qsl, scale, "f16")
+    assert (np.abs(as_f64(out) - ref) - half_ulp(ref, "f16")).max() <= TOL["f16"]
+    x = rounded(fp4.values(*logical[0], KS), "f16")[used].reshape(len(used), Hkv, bs, D // 8, 8).transpose(0, 1, 3, 2, 4)
+    assert np.array_equal(oracle.widen(k16, "f16")[used], x, equal_nan=True)
+    # steps
+    bm.fork(0, 2)
+    for step in range(20):
+        slots, copies = bm.append_tokens([0, 1, 2])
+        if len(copies):
+            pa.pa_copy_blocks_fp4(kt, vt, cuda(copies), D)
+            for codes, f in logical:
+                for s, d in copies:
+                    codes[d], f[d] = codes[s], f[s]
+        write(slots)
+        table, lens = bm.block_tables([0, 1, 2], 8)
+        q = store(rng.standard_normal((3, H, D)), "f16")[0]
+        got = torch.empty(3, H, D, dtype=torch.float16, device="cuda")
+        pa.pa_decode_fp4(got, cuda(q, "f16"), kt, vt, cuda(table), cuda(lens), scale, 8 * bs, KS, VS)
+        if step % 5 == 0:
+            no_error()
+            ref = oracle.decode(q, *pools64(), table, lens, scale, "f64", q_dtype="f16")
+            assert (np.abs(as_f64(got) - ref) - half_ulp(ref, "f16")).max() <= TOL["f16"]
+    bm.close()
