@@ -122,6 +122,37 @@ pa_status check_fp4_rows(const void* key, const void* value, const void* k_cache
   return PA_OK;
 }
 
+// How one pa_decode_fp4 call is cut into launches, and its workspace: nothing when a
+// launch is one CTA, else room for two pieces per CTA.
+struct Fp4Plan {
+  int chunk;  // sequences per launch
+  int grid;
+  size_t off_ml, off_seg, bytes;
+};
+
+pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len, Fp4Plan* pl) {
+  const int sms = sm_count();
+  if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
+  // chunks of 32 tokens: those of one unit and of one sequence's units stay within int32, those of a
+  // launch within 2^40 (a warp's share, 1 / 16 of a CTA's at least, then stays within int32)
+  const long long units = pa::fp4_decode_units(num_heads, num_kv_heads), per_unit = max_seq_len / 32 + 1;
+  if (units * per_unit > 0x7fffffffLL)
+    return fail(PA_ERR_UNSUPPORTED, "num_heads %d with max_seq_len %d: too many pieces of work", num_heads, max_seq_len);
+  long long chunk = num_seqs < pa::kMaxSeqsPerLaunch ? num_seqs : pa::kMaxSeqsPerLaunch;
+  if (chunk > 0x7fffffffLL / per_unit) chunk = 0x7fffffffLL / per_unit;
+  if (chunk > (1LL << 40) / (units * per_unit)) chunk = (1LL << 40) / (units * per_unit);
+  if (chunk < 1) chunk = 1;
+  pl->chunk = static_cast<int>(chunk);
+  pl->grid = pa::fp4_decode_grid(sms, pl->chunk, num_heads, num_kv_heads, max_seq_len);
+  pl->off_ml = pl->off_seg = pl->bytes = 0;
+  if (pl->grid > 1) {
+    pl->off_ml = (size_t)pl->grid * 2 * 16 * head_size * sizeof(float);
+    pl->off_seg = pl->off_ml + (size_t)pl->grid * 2 * 16 * 2 * sizeof(float);
+    pl->bytes = pl->off_seg + (size_t)pl->grid * 2 * 2 * sizeof(int);
+  }
+  return PA_OK;
+}
+
 // How one pa_decode call is cut into launches and how its workspace is laid out.
 struct DecodePlan {
   pa::DecodeKind kind;
@@ -739,9 +770,11 @@ pa_status pa_copy_blocks_fp4(void* k_cache, void* v_cache, const int64_t* src_ds
 
 size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len,
                                     int block_size) {
-  if (check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, PA_F16) != PA_OK)
+  if (check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, PA_F16) != PA_OK ||
+      num_seqs == 0)
     return 0;
-  return 0;
+  Fp4Plan pl;
+  return make_fp4_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, &pl) == PA_OK ? pl.bytes : 0;
 }
 
 pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -749,8 +782,6 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
                         int max_seq_len, int num_heads, int num_kv_heads, int head_size, int block_size,
                         int64_t num_blocks, float scale, void* workspace, size_t workspace_bytes, pa_dtype q_dtype,
                         float k_scale, float v_scale, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   if (q_dtype != PA_F16 && q_dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "an FP4 cache is read by fp16 or bf16 queries");
   pa_status st = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, q_dtype);
@@ -767,29 +798,47 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4))
     return fail(PA_ERR_ALIGNMENT, "q/out/caches need 16-byte, block_tables/seq_lens 4-byte alignment");
+  Fp4Plan pl;
+  st = make_fp4_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, &pl);
+  if (st != PA_OK) return st;
+  if (pl.bytes && (!workspace || workspace_bytes < pl.bytes))
+    return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", pl.bytes, workspace ? workspace_bytes : 0);
+  if (pl.bytes && !aligned(workspace, 16)) return fail(PA_ERR_ALIGNMENT, "workspace needs 16-byte alignment");
   pa::Fp4DecodeParams p{};
   st = device_error_ptr(&p.err);
   if (st != PA_OK) return st;
-  p.out = out;
-  p.q = q;
+  if (pl.bytes) {
+    char* ws = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+    p.part_seg = reinterpret_cast<int2*>(ws + pl.off_seg);
+  }
   p.k_cache = k_cache;
   p.v_cache = v_cache;
-  p.block_tables = block_tables;
-  p.seq_lens = seq_lens;
   p.num_blocks = num_blocks;
   p.max_blocks_per_seq = max_blocks_per_seq;
-  p.num_seqs = num_seqs;
   p.num_heads = num_heads;
   p.num_kv_heads = num_kv_heads;
   p.group = num_heads / num_kv_heads;
+  p.units = pa::fp4_decode_units(num_heads, num_kv_heads);
   p.max_seq_len = max_seq_len;
   p.scale_log2 = static_cast<float>(scale_log2);
   p.out_scale = v_scale;
-  int n = 0;
-  const cudaError_t ce = pa::launch_decode_fp4(q_dtype == PA_BF16, head_size, block_size, p,
-                                               static_cast<cudaStream_t>(stream), &n);
-  g_launches.fetch_add(n, std::memory_order_relaxed);
-  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "FP4 decode launch");
+  p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
+  const size_t row_bytes = (size_t)num_heads * head_size * 2;
+  for (int c0 = 0; c0 < num_seqs; c0 += pl.chunk) {
+    p.num_seqs = num_seqs - c0 < pl.chunk ? num_seqs - c0 : pl.chunk;
+    p.q = static_cast<const char*>(q) + (size_t)c0 * row_bytes;
+    p.out = static_cast<char*>(out) + (size_t)c0 * row_bytes;
+    p.block_tables = block_tables + (size_t)c0 * max_blocks_per_seq;
+    p.seq_lens = seq_lens + c0;
+    int n = 0;
+    const cudaError_t ce = pa::launch_decode_fp4(q_dtype == PA_BF16, head_size, block_size, p, pl.grid,
+                                                 static_cast<cudaStream_t>(stream), &n);
+    g_launches.fetch_add(n, std::memory_order_relaxed);
+    if (ce != cudaSuccess) return cuda_fail(ce, "FP4 decode launch");
+  }
+  return PA_OK;
 }
 
 pa_status pa_get_device_error(int* code, void* stream) {

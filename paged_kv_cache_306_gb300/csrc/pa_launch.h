@@ -225,11 +225,22 @@ struct Fp4DecodeParams {
   int num_heads;
   int num_kv_heads;
   int group;                    // num_heads / num_kv_heads
+  int units;                    // head units per sequence: a kv head's query heads, 16 at a time
   int max_seq_len;
   float scale_log2;             // scale * k_scale * log2(e)
   float out_scale;              // v_scale
+  unsigned long long test_wait_ns;  // > 0 only in the timeout-path test (see pa_set_test_wait_limit)
+  // the workspace (null when the grid is one CTA): two pieces per CTA, 16 rows each
+  float* part_o;                // [2 grid, 16, D]: unnormalised partial outputs
+  float2* part_ml;              // [2 grid, 16]: (maximum in log2 units, sum)
+  int2* part_seg;               // [2 grid]: (segment or -1, whether the piece ends it)
 };
-cudaError_t launch_decode_fp4(bool q_is_bf16, int head_size, int block_size, const Fp4DecodeParams& p,
+inline int fp4_decode_units(int num_heads, int num_kv_heads) {
+  return num_kv_heads * ((num_heads / num_kv_heads + 15) / 16);
+}
+// CTAs of a launch of num_seqs sequences.
+int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len);
+cudaError_t launch_decode_fp4(bool q_is_bf16, int head_size, int block_size, const Fp4DecodeParams& p, int grid,
                               cudaStream_t stream, int* launches);
 
 }  // namespace pa

@@ -259,7 +259,7 @@ class Case:
         mass = oracle.decode(q, k64, np.abs(v64), *args, q_dtype=self.q_dtype)
         kn = np.nanmax(np.sqrt((np.moveaxis(k64, 3, 2).reshape(*k64.shape[:2], self.bs, -1) ** 2).sum(-1)))
         qn = np.sqrt((self.q64[list(seqs)] ** 2).sum(-1, keepdims=True))
-        d = (self.D + 8) * 2.0 ** -23 * self.scale * qn * kn + 2.0 ** -20
+        d = (self.D + 8) * 2.0 ** -23 * abs(self.scale) * qn * kn + 2.0 ** -20
         L = lens.astype(np.float64)[:, None, None]
         rel = 2.0 ** -11 + 2 * d + (L / 8 + 64) * 2.0 ** -22
         return out, rel * mass + L * 2.0 ** -24 * np.nanmax(np.abs(v64))
@@ -495,6 +495,33 @@ def test_pools_past_32_bit_offsets():
     t = c.upload()
     t.update(k=kt, v=vt, table=cuda(blocks.astype(np.int32)[None]))
     out = c.run(t)
+    no_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("lens,G", [([1, 17, 300, 2500, 40, 900], 7), ([30], 2), ([6000, 5000], 12)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(lens, G):
+    """The first pipeline wait of every warp is made on a barrier nothing completes, for 2 ms: it runs out
+    as a real timeout would, the copies in flight are drained, the call returns."""
+    import paged_kv_cache_306_gb300 as pa
+    c = Case(lens, G, 2, 128, 16, "f16")
+    t = c.upload()
+    try:
+        pa.pa_set_test_wait_limit(2_000_000)
+        c.run(t)
+    finally:
+        pa.pa_set_test_wait_limit(0)
+    assert pa.pa_get_device_error() == 4 and pa.pa_get_device_error() == 0
+    out = c.run(t)
+    no_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.09, 3.0e-5])
+def test_decode_scales_of_any_sign(scale):
+    c = Case([1, 40, 333], 3, 2, 64, 16, "bf16")
+    c.scale = scale
+    out = c.run()
     no_error()
     c.check(out)
 
