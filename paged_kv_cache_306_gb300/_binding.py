@@ -7,6 +7,7 @@ Every step of the computation runs in the library's kernels; there is no
 fallback path, and a missing library is an error.
 """
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -426,20 +427,13 @@ def pa_fp4_tile_bytes(head_size, block_size):
     return load().pa_fp4_tile_bytes(head_size, block_size)
 
 
-def _fp4_pools(k_cache, v_cache, num_kv_heads, head_size):
-    """(num_blocks, block_size) of a pair of FP4 pools whose heads and dims are known."""
+@functools.lru_cache(maxsize=None)
+def _fp4_torch():
+    """What the FP4 calls take from torch on every call, looked up once.  These calls run in a
+    few microseconds on the GPU, so their checks and marshalling are kept as short."""
     import torch
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need_here(n, t, torch.uint8, 3)
-    if k_cache.shape != v_cache.shape:
-        raise PAError(PA_ERR_INVALID_ARG, "k_cache and v_cache differ in shape")
-    nb, hkv, tile = k_cache.shape
-    if hkv != num_kv_heads:
-        raise PAError(PA_ERR_INVALID_ARG, f"the pools have {hkv} kv heads, the rows {num_kv_heads}")
-    for bs in (16, 32):
-        if tile == pa_fp4_tile_bytes(head_size, bs):
-            return nb, bs
-    raise PAError(PA_ERR_INVALID_ARG, f"no FP4 tile of head size {head_size} has {tile} bytes")
+    codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+    return torch.uint8, torch.int32, torch.int64, codes, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _need_here(name, t, dtype=None, dims=None):
@@ -451,57 +445,96 @@ def _need_here(name, t, dtype=None, dims=None):
                                           f"cuda:{torch.cuda.current_device()}")
 
 
-def _fp4_rows(key, value, k_cache, v_cache, slot_mapping):
-    import torch
-    _need_here("key", key, None, 3)
-    _need_here("value", value, key.dtype, 3)
-    _need_here("slot_mapping", slot_mapping, torch.int64, 1)
-    if value.shape != key.shape or slot_mapping.numel() != key.shape[0]:
+def _fp4_refuse(*needs):
+    """Raise the error of the first of needs (name, tensor, dtype, dims) that does not hold."""
+    for n in needs:
+        _need_here(*n)
+    raise PAError(PA_ERR_INVALID_ARG, "tensor arguments do not fit together")  # not reached
+
+
+def _fp4_tile(nb, hkv, tile, v_shape, num_kv_heads, head_size):
+    """Block size of FP4 pools of shape (nb, hkv, tile) whose heads and dims are known."""
+    if v_shape != (nb, hkv, tile):
+        raise PAError(PA_ERR_INVALID_ARG, "k_cache and v_cache differ in shape")
+    if hkv != num_kv_heads:
+        raise PAError(PA_ERR_INVALID_ARG, f"the pools have {hkv} kv heads, the rows {num_kv_heads}")
+    bs = 16 * tile // (9 * head_size) if head_size else 0     # 9/16 byte per element
+    if bs not in (16, 32) or 16 * tile != 9 * head_size * bs:
+        raise PAError(PA_ERR_INVALID_ARG, f"no FP4 tile of head size {head_size} has {tile} bytes")
+    return bs
+
+
+def _fp4_rows(call, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream):
+    """The two calls that go through a slot mapping: checks, then the C call."""
+    u8, _, i64, codes, current, raw_stream = _fp4_torch()
+    dt, dev = key.dtype, key.get_device()
+    if not (dev >= 0 and dev == current() and key.dim() == 3 and key.is_contiguous()
+            and value.dtype is dt and value.get_device() == dev and value.is_contiguous()
+            and k_cache.dtype is u8 and k_cache.get_device() == dev and k_cache.dim() == 3 and k_cache.is_contiguous()
+            and v_cache.dtype is u8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and slot_mapping.dtype is i64 and slot_mapping.get_device() == dev and slot_mapping.is_contiguous()):
+        _fp4_refuse(("key", key, None, 3), ("value", value, dt, 3), ("k_cache", k_cache, u8, 3),
+                    ("v_cache", v_cache, u8, 3), ("slot_mapping", slot_mapping, i64, 1))
+    shape = key.shape
+    T, hkv, d = shape
+    if value.shape != shape or slot_mapping.shape != (T,):
         raise PAError(PA_ERR_INVALID_ARG, "key, value and slot_mapping must have one row per token")
-    T, hkv, d = key.shape
-    nb, bs = _fp4_pools(k_cache, v_cache, hkv, d)
-    return T, hkv, d, bs, nb, dtype_code(key.dtype)
+    nb, h, tile = k_cache.shape
+    bs = _fp4_tile(nb, h, tile, v_cache.shape, hkv, d)
+    code = codes[dt] if dt in codes else dtype_code(dt)
+    st = call(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T,
+              hkv, d, bs, nb, code, float(k_scale), float(v_scale),
+              raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check(st)
 
 
 def pa_reshape_and_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None):
     """Quantise key/value [T, Hkv, D] into the FP4 pools through slot_mapping (int64 [T])."""
-    T, hkv, d, bs, nb, code = _fp4_rows(key, value, k_cache, v_cache, slot_mapping)
-    check(load().pa_reshape_and_cache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-                                          T, hkv, d, bs, nb, code, k_scale, v_scale, _stream(stream)))
+    _fp4_rows(load().pa_reshape_and_cache_fp4, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream)
 
 
 def pa_gather_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None):
     """Read the rows of slot_mapping (int64 [T]) back into key/value [T, Hkv, D] (fp32, fp16
     or bf16); the rows of a negative slot stay as they are."""
-    T, hkv, d, bs, nb, code = _fp4_rows(key, value, k_cache, v_cache, slot_mapping)
-    check(load().pa_gather_cache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-                                     T, hkv, d, bs, nb, code, k_scale, v_scale, _stream(stream)))
+    _fp4_rows(load().pa_gather_cache_fp4, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream)
 
 
 def pa_expand_blocks_fp4(k_out, v_out, k_cache, v_cache, src_dst, k_scale, v_scale, stream=None):
     """Read whole FP4 blocks back into the 16-bit pools k_out [NB', Hkv, D/8, bs, 8] and v_out
     [NB', Hkv, D, bs]: src_dst is int64 [n, 2] of (FP4 block, 16-bit block)."""
-    import torch
-    _need_here("k_out", k_out, None, 5)
-    _need_here("v_out", v_out, k_out.dtype, 4)
-    _need_here("src_dst", src_dst, torch.int64)
+    u8, _, i64, codes, current, raw_stream = _fp4_torch()
+    dt, dev = k_out.dtype, k_out.get_device()
+    if not (dev >= 0 and dev == current() and k_out.is_contiguous()
+            and v_out.dtype is dt and v_out.get_device() == dev and v_out.dim() == 4 and v_out.is_contiguous()
+            and k_cache.dtype is u8 and k_cache.get_device() == dev and k_cache.dim() == 3 and k_cache.is_contiguous()
+            and v_cache.dtype is u8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and src_dst.dtype is i64 and src_dst.get_device() == dev and src_dst.is_contiguous()):
+        _fp4_refuse(("k_out", k_out, None, 5), ("v_out", v_out, dt, 4), ("k_cache", k_cache, u8, 3),
+                    ("v_cache", v_cache, u8, 3), ("src_dst", src_dst, i64, None))
     nbo, hkv, d, bs = v_out.shape
     if k_out.shape != (nbo, hkv, d // 8, bs, 8):
         raise PAError(PA_ERR_INVALID_ARG, f"k_out must be [{nbo}, {hkv}, {d // 8}, {bs}, 8]")
-    nb, bs4 = _fp4_pools(k_cache, v_cache, hkv, d)
-    if bs4 != bs:
-        raise PAError(PA_ERR_INVALID_ARG, f"block size {bs4} in the FP4 pools, {bs} in the 16-bit pools")
-    check(load().pa_expand_blocks_fp4(_ptr(k_out), _ptr(v_out), _ptr(k_cache), _ptr(v_cache), _ptr(src_dst),
-                                      src_dst.numel() // 2, hkv, d, bs, nbo, nb, dtype_code(k_out.dtype), k_scale,
-                                      v_scale, _stream(stream)))
+    nb, h, tile = k_cache.shape
+    if _fp4_tile(nb, h, tile, v_cache.shape, hkv, d) != bs:
+        raise PAError(PA_ERR_INVALID_ARG, f"block size {bs} in the 16-bit pools, another in the FP4 pools")
+    code = codes[dt] if dt in codes else dtype_code(dt)
+    st = load().pa_expand_blocks_fp4(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                     src_dst.data_ptr(), src_dst.numel() // 2, hkv, d, bs, nbo, nb, code, float(k_scale),
+                                     float(v_scale),
+                                     raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        check(st)
 
 
 def pa_copy_blocks_fp4(k_cache, v_cache, src_dst, head_size, stream=None):
     """Copy whole blocks of the FP4 pools: src_dst is int64 [n, 2] of (src, dst)."""
     import torch
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need_here(n, t, torch.uint8, 3)
     _need_here("src_dst", src_dst, torch.int64)
-    hkv = k_cache.shape[1] if k_cache.dim() == 3 else 0
-    nb, bs = _fp4_pools(k_cache, v_cache, hkv, head_size)
+    nb, hkv, tile = k_cache.shape
+    bs = _fp4_tile(nb, hkv, tile, v_cache.shape, hkv, head_size)
     check(load().pa_copy_blocks_fp4(_ptr(k_cache), _ptr(v_cache), _ptr(src_dst), src_dst.numel() // 2, hkv, head_size,
                                     bs, nb, _stream(stream)))
 
@@ -515,29 +548,49 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_s
     """Decode attention over FP4 pools; writes out [S, H, D] in q's dtype (fp16 or bf16).
 
     max_seq_len is a host-side bound on seq_lens.  When the call needs a workspace
-    and none is given, one is taken from torch's allocator.  Returns the workspace
-    tensor used (or None).
+    and none is given, or too small a one, one is taken from torch's allocator.
+    Returns the workspace tensor used (or None).
     """
-    import torch
-    _need_here("q", q, None, 3)
-    _need_here("out", out, q.dtype, 3)
-    _need_here("block_tables", block_tables, torch.int32, 2)
-    _need_here("seq_lens", seq_lens, torch.int32, 1)
-    S, H, D = q.shape
-    if out.shape != q.shape or block_tables.shape[0] != S or seq_lens.numel() != S:
+    u8, i32, _, codes, current, raw_stream = _fp4_torch()
+    dt, dev = q.dtype, q.get_device()
+    if not (dev >= 0 and dev == current() and q.dim() == 3 and q.is_contiguous()
+            and out.dtype is dt and out.get_device() == dev and out.is_contiguous()
+            and k_cache.dtype is u8 and k_cache.get_device() == dev and k_cache.dim() == 3 and k_cache.is_contiguous()
+            and v_cache.dtype is u8 and v_cache.get_device() == dev and v_cache.is_contiguous()
+            and block_tables.dtype is i32 and block_tables.get_device() == dev and block_tables.dim() == 2
+            and block_tables.is_contiguous()
+            and seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.is_contiguous()):
+        _fp4_refuse(("q", q, None, 3), ("out", out, dt, 3), ("k_cache", k_cache, u8, 3), ("v_cache", v_cache, u8, 3),
+                    ("block_tables", block_tables, i32, 2), ("seq_lens", seq_lens, i32, 1))
+    shape = q.shape
+    S, H, D = shape
+    rows, width = block_tables.shape
+    if out.shape != shape or rows != S or seq_lens.shape != (S,):
         raise PAError(PA_ERR_INVALID_ARG, "q, out, block_tables and seq_lens must agree on the sequences")
-    hkv = k_cache.shape[1] if k_cache.dim() == 3 else 0
-    nb, bs = _fp4_pools(k_cache, v_cache, hkv, D)
+    nb, hkv, tile = k_cache.shape
+    bs = _fp4_tile(nb, hkv, tile, v_cache.shape, hkv, D)
+    code = codes[dt] if dt in codes else dtype_code(dt)
     lib = load()
-    need = lib.pa_decode_fp4_workspace_size(S, H, hkv, D, max_seq_len, bs)
-    workspace = _workspace(need, workspace, q.device, stream)
-    ws_bytes = 0
-    if workspace is not None:
-        _need_here("workspace", workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    check(lib.pa_decode_fp4(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                            block_tables.shape[1], _ptr(seq_lens), S, max_seq_len, H, hkv, D, bs, nb, scale,
-                            _ptr(workspace), ws_bytes, dtype_code(q.dtype), k_scale, v_scale, _stream(stream)))
+    if workspace is None:
+        workspace = _workspace(lib.pa_decode_fp4_workspace_size(S, H, hkv, D, max_seq_len, bs), None, q.device, stream)
+    while True:
+        ws = ws_bytes = 0
+        if workspace is not None:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                _fp4_refuse(("workspace", workspace, None, None))
+            ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        st = lib.pa_decode_fp4(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                               block_tables.data_ptr(), width, seq_lens.data_ptr(), S, max_seq_len, H, hkv, D, bs, nb,
+                               float(scale), ws, ws_bytes, code, float(k_scale), float(v_scale),
+                               raw_stream(dev) if stream is None else stream.cuda_stream)
+        if st != PA_ERR_WORKSPACE:
+            break
+        need = lib.pa_decode_fp4_workspace_size(S, H, hkv, D, max_seq_len, bs)
+        if ws_bytes >= need:
+            break
+        workspace = _workspace(need, None, q.device, stream)
+    if st:
+        check(st)
     return workspace
 
 

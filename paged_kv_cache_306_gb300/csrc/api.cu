@@ -130,17 +130,18 @@ struct Fp4Plan {
   size_t off_ml, off_seg, bytes;
 };
 
-pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len, Fp4Plan* pl) {
+pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len,
+                        int64_t num_blocks, Fp4Plan* pl) {
   const int sms = sm_count();
   if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
-  // chunks of 32 tokens: those of one unit and of one sequence's units stay within int32, those of a
-  // launch within 2^40 (a warp's share, 1 / 16 of a CTA's at least, then stays within int32)
-  const long long units = pa::fp4_decode_units(num_heads, num_kv_heads), per_unit = max_seq_len / 32 + 1;
-  if (units * per_unit > 0x7fffffffLL)
+  if (num_blocks > 0x7fffffffLL / num_kv_heads)
+    return fail(PA_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles (num_blocks * num_kv_heads)");
+  // the chunks (32 tokens of one unit) of a launch stay within int32
+  const long long per_seq = pa::fp4_decode_units(num_heads, num_kv_heads) * ((long long)max_seq_len / 32 + 1);
+  if (per_seq > 0x7fffffffLL)
     return fail(PA_ERR_UNSUPPORTED, "num_heads %d with max_seq_len %d: too many pieces of work", num_heads, max_seq_len);
   long long chunk = num_seqs < pa::kMaxSeqsPerLaunch ? num_seqs : pa::kMaxSeqsPerLaunch;
-  if (chunk > 0x7fffffffLL / per_unit) chunk = 0x7fffffffLL / per_unit;
-  if (chunk > (1LL << 40) / (units * per_unit)) chunk = (1LL << 40) / (units * per_unit);
+  if (chunk > 0x7fffffffLL / per_seq) chunk = 0x7fffffffLL / per_seq;
   if (chunk < 1) chunk = 1;
   pl->chunk = static_cast<int>(chunk);
   pl->grid = pa::fp4_decode_grid(sms, pl->chunk, num_heads, num_kv_heads, max_seq_len);
@@ -774,7 +775,7 @@ size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_head
       num_seqs == 0)
     return 0;
   Fp4Plan pl;
-  return make_fp4_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, &pl) == PA_OK ? pl.bytes : 0;
+  return make_fp4_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, 1, &pl) == PA_OK ? pl.bytes : 0;
 }
 
 pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -799,7 +800,7 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
       !aligned(block_tables, 4) || !aligned(seq_lens, 4))
     return fail(PA_ERR_ALIGNMENT, "q/out/caches need 16-byte, block_tables/seq_lens 4-byte alignment");
   Fp4Plan pl;
-  st = make_fp4_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, &pl);
+  st = make_fp4_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, num_blocks, &pl);
   if (st != PA_OK) return st;
   if (pl.bytes && (!workspace || workspace_bytes < pl.bytes))
     return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", pl.bytes, workspace ? workspace_bytes : 0);
@@ -824,7 +825,6 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
   p.max_seq_len = max_seq_len;
   p.scale_log2 = static_cast<float>(scale_log2);
   p.out_scale = v_scale;
-  p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
   const size_t row_bytes = (size_t)num_heads * head_size * 2;
   for (int c0 = 0; c0 < num_seqs; c0 += pl.chunk) {
     p.num_seqs = num_seqs - c0 < pl.chunk ? num_seqs - c0 : pl.chunk;

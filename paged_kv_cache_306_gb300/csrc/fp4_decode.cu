@@ -9,8 +9,9 @@
 //   * Work: a segment is (sequence, head unit), cut into chunks of 32 tokens.  All
 //     chunks of the launch are laid end to end; the grid is at most one CTA per SM and
 //     every warp of it takes one equal run of chunks, crossing segments.
-//   * Copies: each warp has its own ring of stages; a chunk is one or two blocks of K and
-//     of V, each a contiguous tile, brought in by bulk copies that signal an mbarrier.
+//   * Copies: each warp has its own ring of stages in shared memory, filled by asynchronous
+//     16-byte copies (cp.async) of its own lanes: a chunk is one or two blocks of K and of V,
+//     each a contiguous tile.  No other warp takes part, so a warp waits on nobody.
 //   * Math: m16n8k16 tensor-core tiles with fp16 operands: S^T = K Q^T, O^T += V^T P^T,
 //     tokens and dims on the 16-row side, query heads on the 8-column side.  A code is
 //     widened by one conversion per two codes and one multiplication by its group's scale
@@ -34,32 +35,30 @@ namespace pa {
 
 namespace {
 
-constexpr int kChunk = 32;                       // tokens of a stage
-constexpr uint64_t kFp4WaitNs = 1000000000ull;   // 1 s, then PA_DEVERR_TIMEOUT
-constexpr float kNoScore = -1e30f;               // below every score (|score| < 2^33)
+constexpr int kChunk = 32;            // tokens
+constexpr float kNoScore = -1e30f;    // below every score (|score| < 2^33)
+constexpr float kSlack = 8.f;         // how far weights may exceed 1, in log2 units
 
 // NT: 8-column tiles of query heads (a unit has up to 8 NT heads).
 template <int D, int NT>
 struct Fp4Shape {
-  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kWarps = NT == 1 ? 12 : 8;
   static constexpr int kRows = 8 * NT;
   static constexpr int kStage = 2 * kChunk * (D / 2 + D / 16);
-  static constexpr int kStages = 147456 / (kWarps * kStage);  // 144 KiB of copies in flight
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kPiece = kRows * D * 4;                // an unnormalised partial output
-  static constexpr int kFirst = kRing;                        // [warps]: the piece a warp starts with
-  static constexpr int kMl = kFirst + kWarps * kPiece;        // [2 warps][rows]: (m, l)
-  static constexpr int kBars = kMl + 2 * kWarps * kRows * 8;  // [warps][stages], and one nothing completes
-  static constexpr int kSeg = kBars + (kWarps * kStages + 2) * 8;  // [2 warps] int2: (segment, flags)
-  static constexpr int kLen = kSeg + 2 * kWarps * 8;          // [seqs]
-  static constexpr int kPre = kLen + kMaxSeqsPerLaunch * 4;   // [seqs + 1], then the scan's warp sums
+  static constexpr int kStages = (NT == 1 ? 2 : 4) * (128 / D);
+  static constexpr int kPiece = kRows * D * 4;                  // an unnormalised partial output
+  static constexpr int kFirst = kWarps * kStages * kStage;      // [warps]: the piece a warp starts with
+  static constexpr int kMl = kFirst + kWarps * kPiece;          // [2 warps][rows]: (m, l)
+  static constexpr int kSeg = kMl + 2 * kWarps * kRows * 8;     // [2 warps] int2: (sequence or -1, unit and kBegins)
+  static constexpr int kLen = kSeg + 2 * kWarps * 8;            // [seqs]
+  static constexpr int kPre = kLen + kMaxSeqsPerLaunch * 4;     // [seqs + 1], then the scan's warp sums
   static constexpr int kBytes = kPre + (kMaxSeqsPerLaunch + 1 + kWarps + 3) * 4;
   static_assert(kStages >= 2 && kPiece <= kStages * kStage, "a warp's last piece takes its ring's place");
-  static_assert(kRing % 128 == 0 && kPiece % 16 == 0 && kMl % 16 == 0 && kBars % 8 == 0 && kSeg % 8 == 0, "alignment");
-  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert(kStage % 128 == 0 && kMl % 16 == 0, "alignment");
+  static_assert(kWarps <= 31 && kBytes <= 227 * 1024, "a bit per warp; shared memory per CTA");
 };
 
-constexpr int kBegins = 1, kEnds = 2;  // a piece holds its segment's first / last chunk
+constexpr int kBegins = 1 << 30;  // beside a unit's number: the piece holds its segment's first chunk
 
 __device__ __forceinline__ float ex2(float x) {  // |relative error| < 2^-22, 0 below 2^-126
   float y;
@@ -67,7 +66,37 @@ __device__ __forceinline__ float ex2(float x) {  // |relative error| < 2^-22, 0 
   return y;
 }
 
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel) { return __byte_perm(a, 0, sel); }
+__device__ __forceinline__ void copy16(uint32_t dst, const unsigned char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the last N groups of this lane's copies have landed
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// One half of a pair, twice.
+__device__ __forceinline__ uint32_t low2(uint32_t a) {
+  const __half2 r = __low2half2(*reinterpret_cast<const __half2*>(&a));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t high2(uint32_t a) {
+  const __half2 r = __high2half2(*reinterpret_cast<const __half2*>(&a));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// d += a b, and d = a b (the first product of a sum, with no zeroing of d before it).
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 // One warp's running softmax of a unit's query heads.
 template <typename T, int D, int BS, int NT>
@@ -76,17 +105,27 @@ struct Fp4Math {
   static constexpr int KW = D / 32;  // words of codes a lane holds of a K row
   static constexpr int VW = D / 64;  // and of a V row
   static constexpr int TILE = fp4::tile_bytes(D, BS);
-  static constexpr int kSub = BS == 16 ? TILE : 16 * (D / 2);        // codes of the chunk's second 16 tokens
-  static constexpr int kSubScale = BS == 16 ? TILE : 16 * (D / 16);  // and their scales
 
   uint32_t qb[KS][NT][2];
   float acc[KS][NT][4];
-  float m_[NT][2], l_[NT][2], hs_[NT][2];
+  float lacc[NT][4];  // the weights' sums of heads 8n + 2 t4 + {0, 1} (twice): a product with ones
+  // of those heads: the reference m of the exponents, -m hs, the score above which m moves, hs
+  float m_[NT][2], off_[NT][2], lim_[NT][2], hs_[NT][2];
   int g, t4;
+  int k_at, ks_at, v_at[2], vs_at;  // this lane's places in a sub-tile (fp4::code_at and its scales')
 
   __device__ __forceinline__ void init(int lane) {
     g = lane >> 2;
     t4 = lane & 3;
+    const int row = ((g >> 1) ^ ((g & 1) ? 3 : 0)) + 4 * (g & 1);  // of token tok; of tok + 2: 8 rows on
+    k_at = row * (D / 2) + ((t4 * (D / 8)) ^ (D == 128 ? ((row >> 1) & 1) << 5 : 0));
+    ks_at = BS * (D / 2) + g * (D / 8) + t4 * (D / 32);
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {  // of tokens 4 t4 + {0, 2} and {1, 3}; i: 4 i rows on
+      const int r = t4 ^ (odd ? 3 : 0);
+      v_at[odd] = r * (D / 2) + (D == 128 ? (8 * g) ^ (((r >> 1) & 1) << 5) : 4 * g);
+    }
+    vs_at = BS * (D / 2) + (D == 128 ? g : g >> 1) * 16 + 4 * t4;
   }
 
   __device__ __forceinline__ void reset() {
@@ -95,21 +134,19 @@ struct Fp4Math {
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[k][n][0] = acc[k][n][1] = acc[k][n][2] = acc[k][n][3] = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      lacc[n][0] = lacc[n][1] = lacc[n][2] = lacc[n][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m_[n][c] = kNoScore;
-        l_[n][c] = 0.f;
+        m_[n][c] = lim_[n][c] = kNoScore;  // the first chunk sets them
+        off_[n][c] = INFINITY;
       }
+    }
   }
 
   // Q^T fragments: lane (g, t4) holds dims D/4 t4 .. of head 8n + g, four per k-step, as
-  // the K words hold them.  scale_log2 may be negative: its sign goes into q, so that the
-  // largest score is the largest exponent.  bf16 heads become fp16 with a power of two
-  // taken from the head's largest |q| (every element keeps its 8 bits), put back by hs_.
-  __device__ __forceinline__ void load_q(const T* q, int nh, float scale_log2) {
-    const uint32_t flip = scale_log2 < 0.f ? 0x80008000u : 0u;
-    const float mag = fabsf(scale_log2);
+  // the K words hold them.
+  __device__ __forceinline__ void load_q(const T* q, int nh) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = 8 * n + g;
@@ -117,11 +154,30 @@ struct Fp4Math {
       for (int k = 0; k < KS / 2; ++k) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (h < nh) w = *reinterpret_cast<const uint4*>(q + h * D + t4 * (D / 4) + 8 * k);
-        qb[2 * k][n][0] = w.x ^ flip;
-        qb[2 * k][n][1] = w.y ^ flip;
-        qb[2 * k + 1][n][0] = w.z ^ flip;
-        qb[2 * k + 1][n][1] = w.w ^ flip;
+        qb[2 * k][n][0] = w.x;
+        qb[2 * k][n][1] = w.y;
+        qb[2 * k + 1][n][0] = w.z;
+        qb[2 * k + 1][n][1] = w.w;
       }
+    }
+  }
+
+  // scale_log2 may be negative: its sign goes into q, so that the largest score is the
+  // largest exponent.  bf16 heads become fp16 with a power of two taken from the head's
+  // largest |q| (every element keeps its 8 bits), put back by hs_.
+  __device__ __forceinline__ void scale_q(float scale_log2) {
+    const float mag = fabsf(scale_log2);
+    if (scale_log2 < 0.f) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          qb[k][n][0] ^= 0x80008000u;
+          qb[k][n][1] ^= 0x80008000u;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
       hs_[n][0] = hs_[n][1] = mag;
       if constexpr (!std::is_same<T, __half>::value) {
         float mx = 0.f;
@@ -152,56 +208,85 @@ struct Fp4Math {
     }
   }
 
-  // One chunk: `rem` valid tokens (more than 31: all).  kc, vc: the stage's K and V tiles.
-  __device__ __forceinline__ void chunk(const unsigned char* kc, const unsigned char* vc, int rem) {
-    float sc[2][NT][4];
-    // rows g and g + 8 of S^T are tokens tok and tok + 2 of a sub-tile
-    const int tok = 4 * (g >> 1) + (g & 1);
-    const int krow = ((g >> 1) ^ ((g & 1) ? 3 : 0)) + 4 * (g & 1);  // fp4::code_at's row of tok; tok + 2: 8 rows on
-    const int kat = krow * (D / 2) + ((t4 * (D / 8)) ^ (D == 128 ? ((krow >> 1) & 1) << 5 : 0));
+  // A chunk's bytes as this lane needs them.
+  struct Raw {
+    uint32_t lo[2][KW], hi[2][KW], ks[2];  // K codes of tokens tok and tok + 2 of each sub-tile, their scales
+    uint32_t x[2][4][VW], vs[2];           // V codes of tokens 4 t4 + i, dims 16 g .. (D 128) or 8 g .. (D 64)
+  };
+
+  static constexpr int kSub = BS == 16 ? TILE : 16 * (D / 2);        // codes of the chunk's second 16 tokens
+  static constexpr int kSubScale = BS == 16 ? TILE : 16 * (D / 16);  // and their scales
+
+  __device__ __forceinline__ void fetch_k(const unsigned char* kc, Raw& f) const {
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      uint32_t lo[KW], hi[KW], f[4];  // codes of the two rows; their groups' scales (pairs equal)
-      const unsigned char* base = kc + mt * kSub + kat;
-      const unsigned char* sbase = kc + BS * (D / 2) + mt * kSubScale;
+      const unsigned char *at = kc + mt * kSub + k_at, *sc = kc + mt * kSubScale + ks_at;
       if constexpr (D == 128) {
-        const uint4 a = *reinterpret_cast<const uint4*>(base), b = *reinterpret_cast<const uint4*>(base + 4 * D);
-        lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w;
-        hi[0] = b.x, hi[1] = b.y, hi[2] = b.z, hi[3] = b.w;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(sbase + g * 16 + t4 * 4);
-        const uint32_t s0 = fp4::e4m3x2_to_f16x2(w), s1 = fp4::e4m3x2_to_f16x2(w >> 16);
-        f[0] = prmt(s0, 0x1010), f[1] = prmt(s0, 0x3232), f[2] = prmt(s1, 0x1010), f[3] = prmt(s1, 0x3232);
+        const uint4 a = *reinterpret_cast<const uint4*>(at), b = *reinterpret_cast<const uint4*>(at + 4 * D);
+        f.lo[mt][0] = a.x, f.lo[mt][1] = a.y, f.lo[mt][2] = a.z, f.lo[mt][KW - 1] = a.w;
+        f.hi[mt][0] = b.x, f.hi[mt][1] = b.y, f.hi[mt][2] = b.z, f.hi[mt][KW - 1] = b.w;
+        f.ks[mt] = *reinterpret_cast<const uint32_t*>(sc);
       } else {
-        const uint2 a = *reinterpret_cast<const uint2*>(base), b = *reinterpret_cast<const uint2*>(base + 4 * D);
-        lo[0] = a.x, lo[1] = a.y;
-        hi[0] = b.x, hi[1] = b.y;
-        const uint32_t s = fp4::e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sbase + g * 8 + t4 * 2));
-        f[0] = f[1] = prmt(s, 0x1010), f[2] = f[3] = prmt(s, 0x3232);
+        const uint2 a = *reinterpret_cast<const uint2*>(at), b = *reinterpret_cast<const uint2*>(at + 4 * D);
+        f.lo[mt][0] = a.x, f.lo[mt][KW - 1] = a.y;
+        f.hi[mt][0] = b.x, f.hi[mt][KW - 1] = b.y;
+        f.ks[mt] = *reinterpret_cast<const uint16_t*>(sc);
       }
-      float so[NT][4];  // the odd k-steps' sums: two chains of MMAs instead of one
+    }
+  }
+
+  __device__ __forceinline__ void fetch_v(const unsigned char* vc, Raw& f) const {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[mt][n][c] = so[n][c] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const unsigned char* at = vc + mt * kSub + v_at[i & 1] + i * 2 * D;
+        if constexpr (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(at);
+          f.x[mt][i][0] = w.x, f.x[mt][i][VW - 1] = w.y;
+        } else {
+          f.x[mt][i][0] = *reinterpret_cast<const uint32_t*>(at);
+        }
+      }
+      f.vs[mt] = *reinterpret_cast<const uint32_t*>(vc + mt * kSubScale + vs_at);
+    }
+  }
+
+  // S^T of a chunk.
+  __device__ __forceinline__ void scores(const Raw& f, float (&sc)[2][NT][4]) const {
+    uint32_t sf[2][4];  // the two rows' groups' scales, each twice
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
+    for (int mt = 0; mt < 2; ++mt) {
+      if constexpr (D == 128) {
+        const uint32_t s0 = fp4::e4m3x2_to_f16x2(f.ks[mt]), s1 = fp4::e4m3x2_to_f16x2(f.ks[mt] >> 16);
+        sf[mt][0] = low2(s0), sf[mt][1] = high2(s0), sf[mt][2] = low2(s1), sf[mt][3] = high2(s1);
+      } else {
+        const uint32_t s = fp4::e4m3x2_to_f16x2(f.ks[mt]);
+        sf[mt][0] = sf[mt][1] = low2(s), sf[mt][2] = sf[mt][3] = high2(s);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < KW; ++w)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {  // the sub-tiles' chains of MMAs in turn
         uint32_t a[4], b[4];
-        fp4::e2m1x8_to_f16x2(lo[w], a);
-        fp4::e2m1x8_to_f16x2(hi[w], b);
-        const uint32_t fa = f[D == 128 ? w / 2 : 0], fb = f[2 + (D == 128 ? w / 2 : 0)];
+        fp4::e2m1x8_to_f16x2(f.lo[mt][w], a);
+        fp4::e2m1x8_to_f16x2(f.hi[mt][w], b);
+        const uint32_t fa = sf[mt][D == 128 ? w / 2 : 0], fb = sf[mt][2 + (D == 128 ? w / 2 : 0)];
         const uint32_t a0[4] = {fp4::hmul2(a[0], fa), fp4::hmul2(b[0], fb), fp4::hmul2(a[1], fa), fp4::hmul2(b[1], fb)};
         const uint32_t a1[4] = {fp4::hmul2(a[2], fa), fp4::hmul2(b[2], fb), fp4::hmul2(a[3], fa), fp4::hmul2(b[3], fb)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma_16816<__half>(sc[mt][n], a0, qb[2 * w][n][0], qb[2 * w][n][1]);
-          mma_16816<__half>(so[n], a1, qb[2 * w + 1][n][0], qb[2 * w + 1][n][1]);
+          if (w == 0) mma_first(sc[mt][n], a0, qb[0][n][0], qb[0][n][1]);
+          else mma_add(sc[mt][n], a0, qb[2 * w][n][0], qb[2 * w][n][1]);
+          mma_add(sc[mt][n], a1, qb[2 * w + 1][n][0], qb[2 * w + 1][n][1]);
         }
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[mt][n][c] += so[n][c];
-    }
+  }
+
+  // The scores of a chunk become weights, in fp16 as the operand P^T; `rem` valid tokens (more than 31: all).
+  __device__ __forceinline__ void weigh(float (&sc)[2][NT][4], uint32_t (&pb)[2][NT][2], int rem) {
+    const int tok = 4 * (g >> 1) + (g & 1);  // rows g and g + 8 of S^T are tokens tok and tok + 2 of a sub-tile
     const bool part = rem < kChunk;  // the sequence's last chunk: what lies past its end may be anything
     if (part) {
 #pragma unroll
@@ -212,68 +297,47 @@ struct Fp4Math {
           for (int c = 0; c < 4; ++c)
             if (16 * mt + tok + (c >> 1) * 2 >= rem) sc[mt][n][c] = kNoScore;
     }
-    // running maximum (over the eight lanes of a head) and weights
-    bool moved = false;
-    float corr[NT][2];
+    // The exponents' reference m is the largest score of some earlier chunk.  It moves only when a
+    // score is more than kSlack above it (in log2 units): until then weights stay below 2^kSlack, which
+    // fp16 holds with the same 11 bits, and the chunk needs no reduction over lanes and no rescaling.
+    float top[NT][2];
+    bool moves = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v = fmaxf(fmaxf(sc[0][n][c], sc[0][n][c + 2]), fmaxf(sc[1][n][c], sc[1][n][c + 2]));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float mn = fmaxf(m_[n][c], v), off = -mn * hs_[n][c];
-        corr[n][c] = ex2((m_[n][c] - mn) * hs_[n][c]);
-        moved |= mn != m_[n][c];
-        m_[n][c] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float p = ex2(fmaf(sc[mt][n][c + 2 * r], hs_[n][c], off));
-            if (part && 16 * mt + tok + 2 * r >= rem) p = 0.f;
-            sc[mt][n][c + 2 * r] = p;
-            sum += p;
-          }
-        l_[n][c] = l_[n][c] * corr[n][c] + sum;
+        top[n][c] = fmaxf(fmaxf(sc[0][n][c], sc[0][n][c + 2]), fmaxf(sc[1][n][c], sc[1][n][c + 2]));
+        moves |= top[n][c] > lim_[n][c];
       }
-    if (__any_sync(0xffffffffu, moved)) {
+    if (__any_sync(0xffffffffu, moves)) move(top);
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[k][n][0] *= corr[n][0];
-          acc[k][n][1] *= corr[n][1];
-          acc[k][n][2] *= corr[n][0];
-          acc[k][n][3] *= corr[n][1];
-        }
-    }
-    // O^T += V^T P^T: the weights rounded to fp16 (11 bits, as the operands are fp16)
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t pb[NT][2];
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          pb[n][r] = movmatrix_trans(pack2<__half>(sc[mt][n][2 * r], sc[mt][n][2 * r + 1]));
-      uint32_t x[4][VW];  // codes of tokens 4 t4 + i, dims 16 g .. (D 128) or 8 g .. (D 64)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = (t4 ^ ((i & 1) ? 3 : 0)) + 4 * i;
-        const unsigned char* at = vc + mt * kSub + row * (D / 2);
-        if constexpr (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(at + ((8 * g) ^ (((row >> 1) & 1) << 5)));
-          x[i][0] = w.x, x[i][VW - 1] = w.y;
-        } else {
-          x[i][0] = *reinterpret_cast<const uint32_t*>(at + 4 * g);
+        for (int c = 0; c < 4; ++c) {
+          sc[mt][n][c] = ex2(fmaf(sc[mt][n][c], hs_[n][c & 1], off_[n][c & 1]));
+          if (part && 16 * mt + tok + (c >> 1) * 2 >= rem) sc[mt][n][c] = 0.f;
         }
+    // rounded to fp16 (11 bits, as the operands are fp16); their sums are of what was rounded
+    const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          pb[mt][n][r] = movmatrix_trans(pack2<__half>(sc[mt][n][2 * r], sc[mt][n][2 * r + 1]));
+        mma_add(lacc[n], ones, pb[mt][n][0], pb[mt][n][1]);
       }
-      uint32_t w = *reinterpret_cast<const uint32_t*>(vc + BS * (D / 2) + mt * kSubScale +
-                                                      (D == 128 ? g : g >> 1) * 16 + 4 * t4);
-      if (part) {  // a scale past the end may be NaN, and 0 * NaN would stay
+  }
+
+  // O^T += V^T P^T.
+  __device__ __forceinline__ void add(const Raw& f, const uint32_t (&pb)[2][NT][2], int rem) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t w = f.vs[mt];
+      if (rem < kChunk) {  // a scale past the end may be NaN, and 0 * NaN would stay
         const int ok = rem - 16 * mt - 4 * t4;
         w = ok >= 4 ? w : ok <= 0 ? 0u : w & ((1u << (8 * ok)) - 1u);
       }
@@ -282,34 +346,45 @@ struct Fp4Math {
       for (int v = 0; v < VW; ++v) {
         constexpr uint32_t kLow = 0x0f0f0f0fu;
         uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims, token pairs
-        fp4::e2m1x8_to_f16x2((x[0][v] & kLow) | ((x[1][v] << 4) & ~kLow), e01);
-        fp4::e2m1x8_to_f16x2(((x[0][v] >> 4) & kLow) | (x[1][v] & ~kLow), o01);
-        fp4::e2m1x8_to_f16x2((x[2][v] & kLow) | ((x[3][v] << 4) & ~kLow), e23);
-        fp4::e2m1x8_to_f16x2(((x[2][v] >> 4) & kLow) | (x[3][v] & ~kLow), o23);
+        fp4::e2m1x8_to_f16x2((f.x[mt][0][v] & kLow) | ((f.x[mt][1][v] << 4) & ~kLow), e01);
+        fp4::e2m1x8_to_f16x2(((f.x[mt][0][v] >> 4) & kLow) | (f.x[mt][1][v] & ~kLow), o01);
+        fp4::e2m1x8_to_f16x2((f.x[mt][2][v] & kLow) | ((f.x[mt][3][v] << 4) & ~kLow), e23);
+        fp4::e2m1x8_to_f16x2(((f.x[mt][2][v] >> 4) & kLow) | (f.x[mt][3][v] & ~kLow), o23);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
           const uint32_t a[4] = {fp4::hmul2(e01[b], f01), fp4::hmul2(o01[b], f01), fp4::hmul2(e23[b], f23),
                                  fp4::hmul2(o23[b], f23)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_16816<__half>(acc[4 * v + b][n], a, pb[n][0], pb[n][1]);
+          for (int n = 0; n < NT; ++n) mma_add(acc[4 * v + b][n], a, pb[mt][n][0], pb[mt][n][1]);
         }
       }
     }
   }
 
-  // Complete the sums; the maximum in log2 units.
-  __device__ __forceinline__ void finish() {
+  // Move the reference to the largest score so far and bring what is summed to it.
+  __device__ __forceinline__ void move(const float (&top)[NT][2]) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      float f[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v = l_[n][c];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        l_[n][c] = v;
-        m_[n][c] *= hs_[n][c];
+        float v = fmaxf(top[n][c], m_[n][c]);
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        const float off = -v * hs_[n][c];
+        f[c] = ex2(off - off_[n][c]);
+        m_[n][c] = v;
+        off_[n][c] = off;
+        lim_[n][c] = v + __fdividef(kSlack, hs_[n][c]);  // (hs 0: infinity)
+        lacc[n][c] *= f[c];
+        lacc[n][c + 2] *= f[c];
       }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[k][n][c] *= f[c & 1];
+    }
   }
 
   // Lane (g, t4) holds dims D/8 g .. of heads 8n + 2 t4 + {0, 1}.
@@ -320,7 +395,7 @@ struct Fp4Math {
       for (int c = 0; c < 2; ++c) {
         const int h = 8 * n + 2 * t4 + c;
         if (h >= nh) continue;
-        const float f = oscale / l_[n][c];
+        const float f = oscale / lacc[n][c];
 #pragma unroll
         for (int k = 0; k < KS; k += 4) {
           uint32_t w[4];
@@ -331,23 +406,35 @@ struct Fp4Math {
       }
   }
 
-  __device__ __forceinline__ void store_piece(float* o, float2* ml) const {
+  // A piece in shared memory: vectors of 4 dims, [head parts (n, c)][vectors of D/8 dims][lane ^ vector],
+  // so that neither the lanes that write nor those that read a head's row meet in a bank.
+  __device__ __forceinline__ void store_piece(float4* o, float2* ml) const {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int h = 8 * n + 2 * t4 + c;
 #pragma unroll
         for (int k = 0; k < KS; k += 2)
-          *reinterpret_cast<float4*>(o + h * D + g * (D / 8) + 2 * k) =
+          o[((2 * n + c) * (KS / 2) + k / 2) * 32 + ((4 * g + t4) ^ (k / 2))] =
               make_float4(acc[k][n][c], acc[k][n][c + 2], acc[k + 1][n][c], acc[k + 1][n][c + 2]);
-        if (g == 0) ml[h] = make_float2(m_[n][c], l_[n][c]);
+        if (g == 0) ml[8 * n + 2 * t4 + c] = make_float2(-off_[n][c], lacc[n][c]);
       }
+  }
+  // Dims 4 i .. 4 i + 3 of head r of a piece.
+  __device__ __forceinline__ static const float4* piece_at(const float4* o, int r, int i) {
+    const int v = i % (KS / 2), gg = i / (KS / 2);
+    return o + ((2 * (r >> 3) + (r & 1)) * (KS / 2) + v) * 32 + ((4 * gg + ((r >> 1) & 3)) ^ v);
   }
 };
 
 // Head unit u: its kv head, first query head and number of them.
 __device__ __forceinline__ void unit_heads(const Fp4DecodeParams& p, int u, int& kvh, int& h0, int& nh) {
+  if (p.group <= 16) {
+    kvh = u;
+    h0 = u * p.group;
+    nh = p.group;
+    return;
+  }
   const int per = (p.group + 15) >> 4;
   kvh = u / per;
   h0 = kvh * p.group + (u - kvh * per) * 16;
@@ -362,28 +449,26 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char* ring = smem + warp * STAGES * Sh::kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kBars) + warp * STAGES;
-  uint64_t* never = reinterpret_cast<uint64_t*>(smem + Sh::kBars) + WARPS * STAGES;
-  int2* s_seg = reinterpret_cast<int2*>(smem + Sh::kSeg);
+  // entry e: a warp's first piece has a place of its own, its last one takes its ring's
+  auto piece = [&](int e) {
+    return reinterpret_cast<float4*>(e & 1 ? smem + (e >> 1) * STAGES * Sh::kStage
+                                           : smem + Sh::kFirst + (e >> 1) * Sh::kPiece);
+  };
   float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
+  int2* s_seg = reinterpret_cast<int2*>(smem + Sh::kSeg);
   int* s_len = reinterpret_cast<int*>(smem + Sh::kLen);
   int* s_pre = reinterpret_cast<int*>(smem + Sh::kPre);
   int* s_sum = s_pre + kMaxSeqsPerLaunch + 1;
 
-  if (lane == 0) {
-    for (int st = 0; st < STAGES; ++st) mbar_init(&bars[st], 1);
-    if (warp == 0) mbar_init(never, 1);
-    fence_barrier_init();
-    s_seg[2 * warp] = s_seg[2 * warp + 1] = make_int2(-1, 0);
-  }
+  if (lane < 2) s_seg[2 * warp + lane] = make_int2(-1, 0);  // no piece
   griddep_launch_dependents();
+  griddep_wait();
 
-  // Lengths (0 when outside [1, max_seq_len]) and the prefix sum of their chunks.  seq_lens
-  // is read before the wait on the previous kernel (no kernel of this library writes it).
+  // Lengths (0 when outside [1, max_seq_len]) and the prefix sum of their chunks.
   const int S = p.num_seqs, U = p.units;
   bool bad = false;
   {
-    constexpr int PER = kMaxSeqsPerLaunch / (WARPS * 32);
+    constexpr int PER = (kMaxSeqsPerLaunch + WARPS * 32 - 1) / (WARPS * 32);
     int n[PER], sum = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -416,8 +501,6 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     if (tid == WARPS * 32 - 1) s_pre[S] = before;
     __syncthreads();
   }
-  griddep_wait();  // from here on: memory the previous kernel may have written
-
   if (bad && blockIdx.x == 0) {
     if (tid == 0) set_error(p.err, kErrSeqLen);
     for (int s = 0; s < S; ++s) {
@@ -427,128 +510,148 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     }
   }
 
-  // This warp's run of the launch's chunks; with fewer chunks than warps, one each.
-  const long long total = (long long)s_pre[S] * U;
-  const long long workers = min(total, (long long)gridDim.x * WARPS);
-  const long long me = (long long)blockIdx.x * WARPS + warp;
-  const long long start = me < workers ? me * total / workers : total;
-  const int len = me < workers ? static_cast<int>((me + 1) * total / workers - start) : 0;
-
-  // Position -> (sequence, unit, chunk of it).
-  auto locate = [&](long long at, int& s, int& u, int& j) {
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((long long)s_pre[mid] * U <= at) lo = mid;
-      else hi = mid - 1;
-    }
-    s = lo;
-    const int n = s_pre[s + 1] - s_pre[s];
-    const int r = static_cast<int>(at - (long long)s_pre[s] * U);
-    u = r / n;
-    j = r - u * n;
-  };
+  // This warp's run of the launch's chunks (fewer than 2^31); with fewer chunks than warps, one each.
+  const int total = s_pre[S] * U;
+  const int workers = min(total, static_cast<int>(gridDim.x) * WARPS);
+  const int me = blockIdx.x * WARPS + warp;
+  int start = 0, len = 0;
+  if (me < workers) {
+    const int share = total / workers, more = total - share * workers;
+    start = me * share + min(me, more);
+    len = share + (me < more);
+  }
 
   if (len > 0) {
-    // Lane i looks up position start + 32 group + i: its blocks (-1: past the sequence) and kv head.
-    auto look_up = [&](int group, int (&blk)[NB], int& kvh) {
-      const int k = 32 * group + lane;
-      kvh = 0;
+    // The sequence of the run's first chunk: the last one whose prefix is at most start / U, found
+    // by the warp together in 32-way steps (empty sequences have their successor's prefix).
+    int s0 = 0;
+    {
+      const int at = start / U;
+      for (int step = S > 32 ? (S + 31) / 32 : 1;;) {
+        const int i = s0 + lane * step;
+        s0 += (31 - __clz(__ballot_sync(0xffffffffu, i < S && s_pre[min(i, S)] <= at))) * step;
+        if (step == 1) break;
+        step = 1;
+      }
+    }
+    // The run's first chunk is chunk j of unit u of sequence s.
+    int s = s0, u, j;
+    {
+      const int n = s_pre[s + 1] - s_pre[s], r = start - s_pre[s] * U;
+      u = r / n;
+      j = r - u * n;
+    }
+    int L, n, h0, nh, kvh;
+    Math math;
+    math.init(lane);
+    auto fetch_q = [&]() {
+      L = s_len[s];
+      n = (L + kChunk - 1) / kChunk;
+      unit_heads(p, u, kvh, h0, nh);
+      math.load_q(static_cast<const T*>(p.q) + ((long long)s * p.num_heads + h0) * D, nh);
+    };
+    fetch_q();
+
+    // Lane i looks up position 32 group + i of the run: the numbers of its tiles (-1: past the sequence).
+    int gs = s, gu = u, gj = j;  // the group's first position
+    auto look_up = [&](int group, int (&tile)[NB]) {
+      int ls = gs, lu = gu, lj = gj + lane;
+      for (int c = s_pre[ls + 1] - s_pre[ls]; lj >= c;) {
+        lj -= c;
+        if (++lu < U) continue;
+        lu = 0;
+        do {
+          if (++ls == S) break;
+          c = s_pre[ls + 1] - s_pre[ls];
+        } while (c == 0);
+        if (ls == S) break;
+      }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) blk[b] = -1;
-      if (k < len) {
-        int s, u, j, h0, nh;
-        locate(start + k, s, u, j);
-        unit_heads(p, u, kvh, h0, nh);
-        const int nblk = (s_len[s] + BS - 1) / BS;
+      for (int b = 0; b < NB; ++b) tile[b] = -1;
+      if (32 * group + lane < len) {
+        int hk, h, c;
+        unit_heads(p, lu, hk, h, c);
+        const int nblk = (s_len[ls] + BS - 1) / BS;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          if (j * NB + b >= nblk) continue;
-          int id = p.block_tables[(long long)s * p.max_blocks_per_seq + j * NB + b];
+          if (lj * NB + b >= nblk) continue;
+          int id = p.block_tables[(long long)ls * p.max_blocks_per_seq + lj * NB + b];
           if (id < 0 || id >= p.num_blocks) {  // record it, read block 0 instead
             set_error(p.err, kErrBlockId);
             id = 0;
           }
-          blk[b] = id;
+          tile[b] = id * p.num_kv_heads + hk;
         }
       }
+      // the next group starts right after lane 31 (a chunk index past its unit is brought in range there)
+      gs = __shfl_sync(0xffffffffu, ls, 31);
+      gu = __shfl_sync(0xffffffffu, lu, 31);
+      gj = __shfl_sync(0xffffffffu, lj, 31) + 1;
     };
-    int blk_cur[NB], kvh_cur, blk_nxt[NB], kvh_nxt, group = 0;
-    look_up(0, blk_cur, kvh_cur);
-    look_up(1, blk_nxt, kvh_nxt);
-    // Chunk k into its stage: K tiles, then V tiles; lane i < 2 NB issues copy i.
+    int cur[NB], nxt[NB], group = 0;
+    look_up(0, cur);
+    if (len > 32) look_up(1, nxt);
+    // Chunk k into its stage: K tiles, then V tiles, 16 bytes a lane at a time.  (The second tile of a
+    // chunk that ends in its first block is not read; the first is copied again.)
     auto issue = [&](int k) {
       if ((k >> 5) != group) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) blk_cur[b] = blk_nxt[b];
-        kvh_cur = kvh_nxt;
-        look_up(++group + 1, blk_nxt, kvh_nxt);
+        for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
+        if (32 * (++group + 1) < len) look_up(group + 1, nxt);
       }
-      int id[NB], n = 0;
+      const unsigned char* from[2 * NB];  // tile i, less the pieces before it: piece x of the chunk is at from[i] + 16 x
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        id[b] = __shfl_sync(0xffffffffu, blk_cur[b], k & 31);
-        n += id[b] >= 0;
+        int t = __shfl_sync(0xffffffffu, cur[b], k & 31);
+        if (b > 0 && t < 0) t = __shfl_sync(0xffffffffu, cur[0], k & 31);
+        from[b] = static_cast<const unsigned char*>(p.k_cache) + (long long)t * TILE + (16 * lane - b * TILE);
+        from[NB + b] = static_cast<const unsigned char*>(p.v_cache) + (long long)t * TILE + (16 * lane - (NB + b) * TILE);
       }
-      const int kvh = __shfl_sync(0xffffffffu, kvh_cur, k & 31);
-      const int st = k % STAGES;
-      if (lane == 0) mbar_arrive_expect_tx(&bars[st], 2 * n * TILE);
-      __syncwarp();
-      const int b = lane % NB, mine = NB == 1 ? id[0] : (b ? id[NB - 1] : id[0]);
-      if (lane < 2 * NB && mine >= 0) {
-        const void* pool = lane < NB ? p.k_cache : p.v_cache;
-        bulk_copy_g2s(ring + st * Sh::kStage + lane * TILE,
-                      static_cast<const unsigned char*>(pool) + ((long long)mine * p.num_kv_heads + kvh) * TILE, TILE,
-                      &bars[st]);
+      constexpr int kPer = TILE / 16, kAll = 2 * NB * kPer;  // 16-byte pieces of a tile, of a chunk
+      const uint32_t to = smem_addr(ring) + (k % STAGES) * Sh::kStage + 16 * lane;
+#pragma unroll
+      for (int x = 0; x < kAll; x += 32) {
+        const int i0 = x / kPer, i1 = (x + 31 < kAll ? x + 31 : kAll - 1) / kPer;  // at most two tiles
+        const unsigned char* src = from[i0];
+        if (i1 != i0 && x + lane >= i1 * kPer) src = from[i1];
+        if (x + 32 <= kAll || x + lane < kAll) copy16(to + 16 * x, src + 16 * x);
       }
     };
-    for (int k = 0; k < STAGES && k < len; ++k) issue(k);
+    for (int k = 0; k < STAGES; ++k) {  // a group of copies per chunk, empty past the end
+      if (k < len) issue(k);
+      copies_close();
+    }
 
-    Math math;
-    math.init(lane);
-    int s, u, j, L, n, h0, nh, kvh;
-    locate(start, s, u, j);
+    math.reset();
+    math.scale_q(p.scale_log2);
     int j0 = j;  // where the current piece starts
-    auto enter = [&]() {
-      L = s_len[s];
-      n = (L + kChunk - 1) / kChunk;
-      unit_heads(p, u, kvh, h0, nh);
-      math.reset();
-      math.load_q(static_cast<const T*>(p.q) + ((long long)s * p.num_heads + h0) * D, nh, p.scale_log2);
-    };
-    enter();
     for (int k = 0; k < len; ++k) {
-      const int st = k % STAGES;
-      const bool ok = __all_sync(0xffffffffu, (p.test_wait_ns && k == 0)
-                                                  ? mbar_wait_bounded(never, 0, p.test_wait_ns)
-                                                  : mbar_wait_bounded(&bars[st], (k / STAGES) & 1, kFp4WaitNs));
-      if (!ok) {  // record it, and let the copies in flight land
-        if (lane == 0) set_error(p.err, kErrTimeout);
-        for (int i = k; i < len && i < k + STAGES; ++i)
-          mbar_wait_bounded(&bars[i % STAGES], (i / STAGES) & 1, kFp4WaitNs / 8);
-        break;
-      }
-      const unsigned char* stage = ring + st * Sh::kStage;
-      math.chunk(stage, stage + NB * TILE, L - j * kChunk);
+      copies_wait<STAGES - 1>();
       __syncwarp();
-      if (k + STAGES < len) {
-        fence_proxy_async_smem();
-        issue(k + STAGES);
-      }
+      const unsigned char* stage = ring + (k % STAGES) * Sh::kStage;
+      const int rem = L - j * kChunk;
+      typename Math::Raw raw;
+      float sc[2][NT][4];
+      uint32_t pb[2][NT][2];
+      math.fetch_k(stage, raw);
+      math.scores(raw, sc);
+      math.fetch_v(stage + NB * TILE, raw);
+      __syncwarp();
+      if (k + STAGES < len) issue(k + STAGES);  // the chunk is in registers: refill its stage
+      copies_close();
+      math.weigh(sc, pb, rem);
+      math.add(raw, pb, rem);
       ++j;
       const bool ends = j == n, last = k + 1 == len;
       if (!ends && !last) continue;
-      math.finish();
       if (j0 == 0 && ends) {
         math.store_out(static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0) * D, nh, p.out_scale);
       } else {
-        // a piece that ends its segment but did not begin it can only be this warp's first, the other
-        // kind only its last, whose room is the ring: its copies have all been read
+        // a piece that ends its segment but did not begin it can only be this warp's first (entry
+        // 2 warp), the other kind only its last (entry 2 warp + 1)
         const int e = 2 * warp + (ends ? 0 : 1);
-        float* o = reinterpret_cast<float*>(ends ? smem + Sh::kFirst + warp * Sh::kPiece : ring);
-        __syncwarp();
-        math.store_piece(o, s_ml + e * Sh::kRows);
-        if (lane == 0) s_seg[e] = make_int2(s * U + u, (j0 == 0 ? kBegins : 0) | (ends ? kEnds : 0));
+        math.store_piece(piece(e), s_ml + e * Sh::kRows);
+        if (lane == 0) s_seg[e] = make_int2(s, u | (j0 == 0 ? kBegins : 0));
       }
       if (last) break;
       if (ends && ++u == U) {
@@ -558,72 +661,63 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
         } while (s_pre[s + 1] == s_pre[s]);
       }
       j = j0 = 0;
-      enter();
+      fetch_q();
+      math.reset();
+      math.scale_q(p.scale_log2);
     }
   }
   __syncthreads();
 
-  // The CTA's pieces in order: entry e = 2 warp + {0, 1}; runs of entries of one segment are merged.
-  // Lane e holds entry e (2 WARPS <= 32).
-  const int2 mine = lane < 2 * WARPS ? s_seg[lane] : make_int2(-1, 0);
-  const uint32_t have = __ballot_sync(0xffffffffu, mine.x >= 0);
-  const uint32_t below = have & ((1u << lane) - 1u);
-  const int prev = __shfl_sync(0xffffffffu, mine.x, below ? 31 - __clz(below) : 0);
-  const uint32_t heads = __ballot_sync(0xffffffffu, mine.x >= 0 && (below == 0 || prev != mine.x));
-  int task = 0;
+  // The CTA's pieces: a run of them is one segment's, one per warp, warps w0 .. w1.  A run starts
+  // with a last piece that begins its segment, or with warp 0; it stops at the first warp after
+  // that has a first piece (which ends the segment), or with the CTA's last working warp.  A
+  // thread takes 4 dims of a head of a run.
+  const int2 first = lane < WARPS ? s_seg[2 * lane] : make_int2(-1, 0);
+  const int2 final = lane < WARPS ? s_seg[2 * lane + 1] : make_int2(-1, 0);
+  const uint32_t firsts = __ballot_sync(0xffffffffu, first.x >= 0), finals = __ballot_sync(0xffffffffu, final.x >= 0);
+  const uint32_t begin = __ballot_sync(0xffffffffu, final.x >= 0 && (final.y & kBegins));
+  constexpr int kVecs = D / 4;
   int2 out0 = make_int2(-1, 0), out1 = make_int2(-1, 0);
-  for (uint32_t hd = heads; hd; hd &= hd - 1) {
-    const int e0 = __ffs(hd) - 1;
-    const uint32_t next = hd & (hd - 1);
-    const uint32_t run = have & ~((1u << e0) - 1u) & (next ? (next & -next) - 1u : 0xffffffffu);
-    const int e1 = 31 - __clz(run);
-    const int seg = __shfl_sync(0xffffffffu, mine.x, e0);
-    const bool begins = __shfl_sync(0xffffffffu, mine.y, e0) & kBegins;
-    const bool ends = __shfl_sync(0xffffffffu, mine.y, e1) & kEnds;
-    if (!begins) out0 = make_int2(seg, ends);
-    else if (!ends) out1 = make_int2(seg, 0);
-    const int s = seg / U;
+  int task = tid;
+  // bit 0 of `heads` below: the run that warp 0 starts without beginning a segment; bit w + 1: one that warp w begins
+  for (uint32_t heads = begin << 1 | (firsts & 1u) | (finals & ~begin & 1u); heads; heads &= heads - 1) {
+    const int hd = __ffs(heads) - 1, w0 = hd ? hd - 1 : 0;
+    const bool alone = hd == 0 && (firsts & 1u);  // warp 0's first piece ends a segment that an earlier CTA began
+    const uint32_t stops = alone ? 1u : firsts & ~((2u << w0) - 1u);
+    const bool begins = hd != 0, ends = stops != 0;
+    const int w1 = ends ? __ffs(stops) - 1 : 31 - __clz(finals);
+    const int2 seg = s_seg[alone ? 0 : 2 * w0 + 1];
+    const int s = seg.x, u = seg.y & ~kBegins;
+    if (!begins) out0 = make_int2(s * U + u, ends);
+    else if (!ends) out1 = make_int2(s * U + u, 0);
     int kvh, h0, nh;
-    unit_heads(p, seg - s * U, kvh, h0, nh);
-    for (int r = 0; r < nh; ++r, ++task) {
-      if (task % WARPS != warp) continue;
-      constexpr int C = D / 32;
-      using Vec = std::conditional_t<C == 4, float4, float2>;
-      float M = -INFINITY, W = 0.f, O[C] = {};
-      const float2 ml = (run >> lane) & 1u ? s_ml[lane * Sh::kRows + r] : make_float2(-INFINITY, 0.f);
-      M = ml.x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float f = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
-      W = f * ml.y;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-      for (uint32_t e = run; e; e &= e - 1) {
-        const int i = __ffs(e) - 1;
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const unsigned char* at = i & 1 ? smem + (i >> 1) * STAGES * Sh::kStage
-                                        : smem + Sh::kFirst + (i >> 1) * Sh::kPiece;
-        const Vec v = *reinterpret_cast<const Vec*>(reinterpret_cast<const float*>(at) + r * D + lane * C);
-        const float* vf = reinterpret_cast<const float*>(&v);
-#pragma unroll
-        for (int c = 0; c < C; ++c) O[c] = fmaf(fi, vf[c], O[c]);
+    unit_heads(p, u, kvh, h0, nh);
+    for (; task < nh * kVecs; task += WARPS * 32) {
+      const int r = task / kVecs, v = task % kVecs;
+      auto entry = [&](int w) { return 2 * w + (ends && w == w1 ? 0 : 1); };
+      float M = -INFINITY, W = 0.f;
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w) M = fmaxf(M, s_ml[entry(w) * Sh::kRows + r].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w) {
+        const float2 ml = s_ml[entry(w) * Sh::kRows + r];
+        const float4 x = *Math::piece_at(piece(entry(w)), r, v);
+        const float f = ex2(ml.x - M);
+        W = fmaf(f, ml.y, W);
+        o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, x.z, o.z), fmaf(f, x.w, o.w));
       }
       if (begins && ends) {
-        T* out = static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + lane * C;
         const float il = p.out_scale / W;
-#pragma unroll
-        for (int c = 0; c < C; c += 2)
-          *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(O[c] * il, O[c + 1] * il);
-      } else if (p.part_o) {  // (null only in a grid of one CTA, which leaves such a piece only when aborted)
-        const long long slot = 2 * (long long)blockIdx.x + (begins ? 1 : 0);
-        Vec v;
-        float* vf = reinterpret_cast<float*>(&v);
-#pragma unroll
-        for (int c = 0; c < C; ++c) vf[c] = O[c];
-        *reinterpret_cast<Vec*>(p.part_o + (slot * 16 + r) * D + lane * C) = v;
-        if (lane == 0) p.part_ml[slot * 16 + r] = make_float2(M, W);
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + 4 * v) =
+            make_uint2(pack2<T>(o.x * il, o.y * il), pack2<T>(o.z * il, o.w * il));
+      } else {
+        const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+        reinterpret_cast<float4*>(p.part_o)[(slot * 16 + r) * kVecs + v] = o;
+        if (v == 0) p.part_ml[slot * 16 + r] = make_float2(M, W);
       }
     }
+    task -= nh * kVecs;
   }
   if (tid == 0 && p.part_seg) {
     p.part_seg[2 * blockIdx.x] = out0;
@@ -633,63 +727,79 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
 
 // CTA b merges the segment whose first piece ends CTA b's run (if there is one): that
 // piece is slot 2 b + 1, the others are slots 2 (b + 1), 2 (b + 2), ... up to the one
-// that ends the segment.  A warp per query head.
-constexpr int kFp4MergeWarps = 8;
+// that ends the segment.  A warp per query head; everything a segment of up to 4 pieces
+// needs is loaded at once, before it is known how many there are.
+constexpr int kFp4MergeWarps = 8, kFp4MergeBatch = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kFp4MergeWarps * 32) decode_fp4_merge_kernel(const Fp4DecodeParams p, int ctas) {
-  griddep_wait();
-  griddep_launch_dependents();
   constexpr int C = D / 32;
   using Vec = std::conditional_t<C == 4, float4, float2>;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seg = p.part_seg[2 * b + 1].x;
-  if (seg < 0) return;
-  int rest = 0;  // pieces after the first
-  for (int i0 = b + 1; i0 < ctas; i0 += 32) {
-    const int2 d = i0 + lane < ctas ? p.part_seg[2 * (i0 + lane)] : make_int2(-1, 1);
-    const uint32_t stop = __ballot_sync(0xffffffffu, d.x != seg || d.y);
-    if (stop) {
-      const int at = __ffs(stop) - 1;
-      rest += at + (__shfl_sync(0xffffffffu, d.x, at) == seg);  // (another segment: an aborted launch)
-      break;
-    }
-    rest += 32;
+  const int b = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kFp4MergeWarps + (threadIdx.x >> 5);
+  auto slot = [&](int i) { return i == 0 ? 2 * b + 1 : 2 * (b + i); };  // of piece i
+  griddep_wait();
+  griddep_launch_dependents();
+  int2 info = make_int2(-1, 0);  // lane i: of piece i
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (b + lane < ctas) {
+    info = p.part_seg[slot(lane)];
+    ml = p.part_ml[slot(lane) * 16 + r];
   }
+  Vec o[kFp4MergeBatch];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kFp4MergeBatch; ++i)
+      if (b + i0 + i < ctas) o[i] = *reinterpret_cast<const Vec*>(p.part_o + (slot(i0 + i) * 16 + r) * D + lane * C);
+  };
+  load(0);
+  const int seg = __shfl_sync(0xffffffffu, info.x, 0);
+  if (seg < 0) return;
   const int s = seg / p.units;
   int kvh, h0, nh;
   unit_heads(p, seg - s * p.units, kvh, h0, nh);
-  for (int r = warp; r < nh; r += kFp4MergeWarps) {
-    float RM = -INFINITY, RW = 0.f, RO[C] = {};
-    for (int i0 = 0; i0 <= rest; i0 += 32) {
-      const int cnt = min(32, rest + 1 - i0);
-      auto slot = [&](int i) { return i == 0 ? 2 * (long long)b + 1 : 2 * (long long)(b + i); };
-      const float2 ml = lane < cnt ? p.part_ml[slot(i0 + lane) * 16 + r] : make_float2(-INFINITY, 0.f);
-      float M = fmaxf(ml.x, RM);
+  if (r >= nh) return;
+  float M = -INFINITY, W = 0.f, O[C] = {};
+  for (int i0 = 0;; i0 += 32) {  // 32 pieces at a time
+    // up to the piece that ends the segment
+    const uint32_t stop = __ballot_sync(0xffffffffu, info.x != seg || info.y);
+    int cnt = 32;
+    if (stop) {
+      cnt = __ffs(stop) - 1;
+      cnt += __shfl_sync(0xffffffffu, info.x, cnt) == seg;
+    }
+    if (lane >= cnt) ml = make_float2(-INFINITY, 0.f);
+    float top = fmaxf(ml.x, M);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float f = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
-      float W = f * ml.y;
+    for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float keep = ex2(M - top), f = ex2(ml.x - top);
+    float w = f * ml.y;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-      const float keep = RW > 0.f ? ex2(RM - M) : 0.f;
-      RM = M;
-      RW = RW * keep + W;
+    for (int x = 1; x < 32; x <<= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
+    M = top;
+    W = W * keep + w;
 #pragma unroll
-      for (int c = 0; c < C; ++c) RO[c] *= keep;
-      for (int i = 0; i < cnt; ++i) {
-        const Vec v = *reinterpret_cast<const Vec*>(p.part_o + (slot(i0 + i) * 16 + r) * D + lane * C);
-        const float* vf = reinterpret_cast<const float*>(&v);
-        const float fi = __shfl_sync(0xffffffffu, f, i);
+    for (int c = 0; c < C; ++c) O[c] *= keep;
+    for (int i1 = 0; i1 < cnt; i1 += kFp4MergeBatch) {
+      if (i0 + i1 > 0) load(i0 + i1);
 #pragma unroll
-        for (int c = 0; c < C; ++c) RO[c] = fmaf(fi, vf[c], RO[c]);
+      for (int i = 0; i < kFp4MergeBatch; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, (i1 + i) & 31);
+        const float* v = reinterpret_cast<const float*>(&o[i]);
+        if (i1 + i < cnt) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) O[c] = fmaf(fi, v[c], O[c]);
+        }
       }
     }
-    const float il = p.out_scale / RW;
-    T* out = static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + lane * C;
-#pragma unroll
-    for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(RO[c] * il, RO[c + 1] * il);
+    if (stop) break;
+    const int at = b + i0 + 32 + lane;  // the CTA of piece i0 + 32 + lane
+    info = at < ctas ? p.part_seg[2 * at] : make_int2(-1, 0);
+    ml = at < ctas ? p.part_ml[2 * at * 16 + r] : make_float2(-INFINITY, 0.f);
   }
+  const float il = p.out_scale / W;
+  T* out = static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + lane * C;
+#pragma unroll
+  for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(O[c] * il, O[c + 1] * il);
 }
 
 template <typename T, int D, int BS, int NT>
@@ -709,7 +819,7 @@ cudaError_t launch_t(const Fp4DecodeParams& p, int grid, cudaStream_t stream, in
   if (e != cudaSuccess) return e;
   *launches = 1;
   if (grid == 1) return cudaSuccess;  // one CTA: nothing is cut at a CTA's end
-  e = launch_pdl(decode_fp4_merge_kernel<T, D>, dim3(grid - 1), dim3(kFp4MergeWarps * 32), 0, stream, p, grid);
+  e = launch_pdl(decode_fp4_merge_kernel<T, D>, dim3(grid - 1, NT), dim3(kFp4MergeWarps * 32), 0, stream, p, grid);
   if (e == cudaSuccess) *launches = 2;
   return e;
 }
@@ -736,7 +846,7 @@ cudaError_t launch_shape(int head_size, int block_size, const Fp4DecodeParams& p
 constexpr int kFp4MinChunks = 2;
 
 int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len) {
-  const int group = num_heads / num_kv_heads, warps = group <= 8 ? 16 : 8;
+  const int group = num_heads / num_kv_heads, warps = group <= 8 ? Fp4Shape<128, 1>::kWarps : Fp4Shape<128, 2>::kWarps;
   const long long chunks = (long long)num_seqs * fp4_decode_units(num_heads, num_kv_heads) *
                            ((max_seq_len + kChunk - 1) / kChunk);
   const long long want = (chunks + kFp4MinChunks * warps - 1) / (kFp4MinChunks * warps);

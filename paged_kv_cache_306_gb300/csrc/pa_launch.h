@@ -229,7 +229,6 @@ struct Fp4DecodeParams {
   int max_seq_len;
   float scale_log2;             // scale * k_scale * log2(e)
   float out_scale;              // v_scale
-  unsigned long long test_wait_ns;  // > 0 only in the timeout-path test (see pa_set_test_wait_limit)
   // the workspace (null when the grid is one CTA): two pieces per CTA, 16 rows each
   float* part_o;                // [2 grid, 16, D]: unnormalised partial outputs
   float2* part_ml;              // [2 grid, 16]: (maximum in log2 units, sum)

@@ -499,24 +499,6 @@ def test_pools_past_32_bit_offsets():
     c.check(out)
 
 
-@pytest.mark.parametrize("lens,G", [([1, 17, 300, 2500, 40, 900], 7), ([30], 2), ([6000, 5000], 12)])
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(lens, G):
-    """The first pipeline wait of every warp is made on a barrier nothing completes, for 2 ms: it runs out
-    as a real timeout would, the copies in flight are drained, the call returns."""
-    import paged_kv_cache_306_gb300 as pa
-    c = Case(lens, G, 2, 128, 16, "f16")
-    t = c.upload()
-    try:
-        pa.pa_set_test_wait_limit(2_000_000)
-        c.run(t)
-    finally:
-        pa.pa_set_test_wait_limit(0)
-    assert pa.pa_get_device_error() == 4 and pa.pa_get_device_error() == 0
-    out = c.run(t)
-    no_error()
-    c.check(out)
-
-
 @pytest.mark.parametrize("scale", [0.0, -0.09, 3.0e-5])
 def test_decode_scales_of_any_sign(scale):
     c = Case([1, 40, 333], 3, 2, 64, 16, "bf16")
