@@ -284,19 +284,21 @@ struct Fp4Math {
       }
   }
 
+  __device__ __forceinline__ static void mask(float (&sc)[2][NT][4], int tok, int rem, float with) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (16 * mt + tok + (c >> 1) * 2 >= rem) sc[mt][n][c] = with;
+  }
+
   // The scores of a chunk become weights, in fp16 as the operand P^T; `rem` valid tokens (more than 31: all).
   __device__ __forceinline__ void weigh(float (&sc)[2][NT][4], uint32_t (&pb)[2][NT][2], int rem) {
     const int tok = 4 * (g >> 1) + (g & 1);  // rows g and g + 8 of S^T are tokens tok and tok + 2 of a sub-tile
     const bool part = rem < kChunk;  // the sequence's last chunk: what lies past its end may be anything
-    if (part) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (16 * mt + tok + (c >> 1) * 2 >= rem) sc[mt][n][c] = kNoScore;
-    }
+    if (part) mask(sc, tok, rem, kNoScore);
     // The exponents' reference m is the largest score of some earlier chunk.  It moves only when a
     // score is more than kSlack above it (in log2 units): until then weights stay below 2^kSlack, which
     // fp16 holds with the same 11 bits, and the chunk needs no reduction over lanes and no rescaling.
@@ -317,8 +319,8 @@ struct Fp4Math {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           sc[mt][n][c] = ex2(fmaf(sc[mt][n][c], hs_[n][c & 1], off_[n][c & 1]));
-          if (part && 16 * mt + tok + (c >> 1) * 2 >= rem) sc[mt][n][c] = 0.f;
         }
+    if (part) mask(sc, tok, rem, 0.f);
     // rounded to fp16 (11 bits, as the operands are fp16); their sums are of what was rounded
     const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
@@ -333,14 +335,17 @@ struct Fp4Math {
   }
 
   // O^T += V^T P^T.
-  __device__ __forceinline__ void add(const Raw& f, const uint32_t (&pb)[2][NT][2], int rem) {
+  __device__ __forceinline__ void add(Raw& f, const uint32_t (&pb)[2][NT][2], int rem) {
+    if (rem < kChunk) {  // a scale past the sequence's end may be NaN, and 0 * NaN would stay
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const int ok = rem - 16 * mt - 4 * t4;
+        f.vs[mt] = ok >= 4 ? f.vs[mt] : ok <= 0 ? 0u : f.vs[mt] & ((1u << (8 * ok)) - 1u);
+      }
+    }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      uint32_t w = f.vs[mt];
-      if (rem < kChunk) {  // a scale past the end may be NaN, and 0 * NaN would stay
-        const int ok = rem - 16 * mt - 4 * t4;
-        w = ok >= 4 ? w : ok <= 0 ? 0u : w & ((1u << (8 * ok)) - 1u);
-      }
+      const uint32_t w = f.vs[mt];
       const uint32_t f01 = fp4::e4m3x2_to_f16x2(w), f23 = fp4::e4m3x2_to_f16x2(w >> 16);
 #pragma unroll
       for (int v = 0; v < VW; ++v) {
@@ -515,10 +520,10 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   const int workers = min(total, static_cast<int>(gridDim.x) * WARPS);
   const int me = blockIdx.x * WARPS + warp;
   int start = 0, len = 0;
-  if (me < workers) {
-    const int share = total / workers, more = total - share * workers;
-    start = me * share + min(me, more);
-    len = share + (me < more);
+  if (me < workers) {  // me * total / workers, the odd chunks spread over the grid
+    const int share = total / workers, more = total - share * workers;  // (more < workers <= 16 * SMs)
+    start = me * share + me * more / workers;
+    len = (me + 1) * share + (me + 1) * more / workers - start;
   }
 
   if (len > 0) {
