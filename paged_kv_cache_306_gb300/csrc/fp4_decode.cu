@@ -73,6 +73,13 @@ __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_g
 template <int N>  // all but the last N groups of this lane's copies have landed
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// The value in memory at this moment, whatever an earlier load of this kernel saw.
+__device__ __forceinline__ int ld_now(const int32_t* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // One half of a pair, twice.
 __device__ __forceinline__ uint32_t low2(uint32_t a) {
   const __half2 r = __low2half2(*reinterpret_cast<const __half2*>(&a));
@@ -467,22 +474,77 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
 
   if (lane < 2) s_seg[2 * warp + lane] = make_int2(-1, 0);  // no piece
   griddep_launch_dependents();
-  griddep_wait();
 
-  // Lengths (0 when outside [1, max_seq_len]) and the prefix sum of their chunks.
+  // The schedule: lengths (0 when outside [1, max_seq_len]), the prefix sum of their chunks,
+  // this warp's run of chunks and its first 32 chunks' tiles.  It is made before the wait on
+  // the previous kernel, from what seq_lens and block_tables hold then, and kept only if both
+  // read the same after it (they seldom change at the last moment); nothing is written or
+  // reported before that.  On a busy stream this hides some 3000 cycles.
   const int S = p.num_seqs, U = p.units;
-  bool bad = false;
-  {
-    constexpr int PER = (kMaxSeqsPerLaunch + WARPS * 32 - 1) / (WARPS * 32);
+  constexpr int PER = (kMaxSeqsPerLaunch + WARPS * 32 - 1) / (WARPS * 32);
+  int lens[PER];  // of sequences tid * PER + k
+#pragma unroll
+  for (int k = 0; k < PER; ++k) lens[k] = tid * PER + k < S ? ld_now(p.seq_lens + tid * PER + k) : 0;
+  int start = 0, len = 0, s = 0, u = 0, j = 0;  // the run; its first chunk is chunk j of unit u of sequence s
+  int gs = 0, gu = 0, gj = 0;                   // the first position of the next 32 to look up
+  int cur[NB], nxt[NB];                         // lane i: the blocks, then the tiles, of position i of 32 (-1: none)
+  bool bad = false;                             // some length is outside the contract
+
+  // Lane i looks up the blocks of position i of the next 32, and the kv head of all of them.
+  auto look_up = [&](int positions, int (&id)[NB], int& head) {
+    int ls = gs, lu = gu, lj = gj + lane;
+    for (int c = s_pre[ls + 1] - s_pre[ls]; lj >= c;) {
+      lj -= c;
+      if (++lu < U) continue;
+      lu = 0;
+      do {
+        if (++ls == S) break;
+        c = s_pre[ls + 1] - s_pre[ls];
+      } while (c == 0);
+      if (ls == S) break;
+    }
+    head = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) id[b] = -1;
+    if (lane < positions) {
+      int h, c;
+      unit_heads(p, lu, head, h, c);
+      const int nblk = (s_len[ls] + BS - 1) / BS;
+      const int32_t* row = p.block_tables + (long long)ls * p.max_blocks_per_seq + lj * NB;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (lj * NB + b >= nblk) continue;
+        const int v = ld_now(row + b);
+        id[b] = v < 0 ? 0x7fffffff : v;  // (past any pool)
+      }
+    }
+    // the next group starts right after lane 31 (a chunk index past its unit is brought in range there)
+    gs = __shfl_sync(0xffffffffu, ls, 31);
+    gu = __shfl_sync(0xffffffffu, lu, 31);
+    gj = __shfl_sync(0xffffffffu, lj, 31) + 1;
+  };
+  // Blocks to tiles; one outside the pool is recorded, and block 0 read instead.
+  auto to_tiles = [&](int (&id)[NB], int head) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      if (id[b] < 0) continue;
+      if (id[b] >= p.num_blocks) {
+        set_error(p.err, kErrBlockId);
+        id[b] = 0;
+      }
+      id[b] = id[b] * p.num_kv_heads + head;
+    }
+  };
+
+  for (bool waited = false;; waited = true) {
     int n[PER], sum = 0;
+    bad = false;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int i = tid * PER + k;
-      int L = i < S ? p.seq_lens[i] : 0;
-      if (L < 1 || L > p.max_seq_len) {
-        L = 0;
-        bad |= i < S;
-      }
+      const bool out = lens[k] < 1 || lens[k] > p.max_seq_len;
+      const int L = out ? 0 : lens[k];
+      bad |= out && i < S;
       if (i < S) s_len[i] = L;
       n[k] = (L + kChunk - 1) / kChunk;
       sum += n[k];
@@ -495,8 +557,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     }
     if (lane == 31) s_sum[warp] = incl;
     bad = __syncthreads_or(bad);
-    int before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int i = tid * PER + k;
@@ -505,48 +566,70 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     }
     if (tid == WARPS * 32 - 1) s_pre[S] = before;
     __syncthreads();
-  }
-  if (bad && blockIdx.x == 0) {
-    if (tid == 0) set_error(p.err, kErrSeqLen);
-    for (int s = 0; s < S; ++s) {
-      if (s_len[s] != 0) continue;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (long long)s * p.num_heads * D);
-      for (int i = tid; i < p.num_heads * D / 8; i += WARPS * 32) out[i] = make_uint4(0, 0, 0, 0);
+
+    // An equal share of the launch's chunks (fewer than 2^31); with fewer chunks than warps, one each.
+    const int total = s_pre[S] * U;
+    const int workers = min(total, static_cast<int>(gridDim.x) * WARPS);
+    const int me = blockIdx.x * WARPS + warp;
+    start = len = 0;
+    if (me < workers) {  // me * total / workers, the odd chunks spread over the grid
+      const int share = total / workers, more = total - share * workers;  // (more < workers <= 16 * SMs)
+      start = me * share + me * more / workers;
+      len = (me + 1) * share + (me + 1) * more / workers - start;
+    }
+    int head = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) cur[b] = -1;
+    if (len > 0) {
+      // The sequence: the last one whose prefix is at most the start, found by the warp together in
+      // 32-way steps (empty sequences have their successor's prefix).
+      s = 0;
+      for (int step = S > 32 ? (S + 31) / 32 : 1;; step = 1) {
+        const int i = s + lane * step;
+        s += (31 - __clz(__ballot_sync(0xffffffffu, i < S && s_pre[min(i, S)] * U <= start))) * step;
+        if (step == 1) break;
+      }
+      const int c = s_pre[s + 1] - s_pre[s], r = start - s_pre[s] * U;
+      u = r / c;
+      j = r - u * c;
+      gs = s, gu = u, gj = j;
+      look_up(len, cur, head);
+    }
+    bool again = false;
+    if (!waited) {
+      griddep_wait();
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int now = tid * PER + k < S ? ld_now(p.seq_lens + tid * PER + k) : 0;
+        again |= now != lens[k];
+        lens[k] = now;
+      }
+      if (len > 0) {
+        int now[NB];
+        gs = s, gu = u, gj = j;
+        look_up(len, now, head);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) again |= now[b] != cur[b];
+      }
+      again = __syncthreads_or(again);
+    }
+    if (!again) {
+      to_tiles(cur, head);
+      break;
     }
   }
 
-  // This warp's run of the launch's chunks (fewer than 2^31); with fewer chunks than warps, one each.
-  const int total = s_pre[S] * U;
-  const int workers = min(total, static_cast<int>(gridDim.x) * WARPS);
-  const int me = blockIdx.x * WARPS + warp;
-  int start = 0, len = 0;
-  if (me < workers) {  // me * total / workers, the odd chunks spread over the grid
-    const int share = total / workers, more = total - share * workers;  // (more < workers <= 16 * SMs)
-    start = me * share + me * more / workers;
-    len = (me + 1) * share + (me + 1) * more / workers - start;
+  if (bad && blockIdx.x == 0) {
+    if (tid == 0) set_error(p.err, kErrSeqLen);
+    for (int i = 0; i < S; ++i) {
+      if (s_len[i] != 0) continue;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (long long)i * p.num_heads * D);
+      for (int x = tid; x < p.num_heads * D / 8; x += WARPS * 32) out[x] = make_uint4(0, 0, 0, 0);
+    }
   }
 
   if (len > 0) {
-    // The sequence of the run's first chunk: the last one whose prefix is at most start / U, found
-    // by the warp together in 32-way steps (empty sequences have their successor's prefix).
-    int s0 = 0;
-    {
-      const int at = start / U;
-      for (int step = S > 32 ? (S + 31) / 32 : 1;;) {
-        const int i = s0 + lane * step;
-        s0 += (31 - __clz(__ballot_sync(0xffffffffu, i < S && s_pre[min(i, S)] <= at))) * step;
-        if (step == 1) break;
-        step = 1;
-      }
-    }
-    // The run's first chunk is chunk j of unit u of sequence s.
-    int s = s0, u, j;
-    {
-      const int n = s_pre[s + 1] - s_pre[s], r = start - s_pre[s] * U;
-      u = r / n;
-      j = r - u * n;
-    }
-    int L, n, h0, nh, kvh;
+    int L, n, h0, nh, kvh, group = 0;
     Math math;
     math.init(lane);
     auto fetch_q = [&]() {
@@ -556,53 +639,19 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       math.load_q(static_cast<const T*>(p.q) + ((long long)s * p.num_heads + h0) * D, nh);
     };
     fetch_q();
-
-    // Lane i looks up position 32 group + i of the run: the numbers of its tiles (-1: past the sequence).
-    int gs = s, gu = u, gj = j;  // the group's first position
-    auto look_up = [&](int group, int (&tile)[NB]) {
-      int ls = gs, lu = gu, lj = gj + lane;
-      for (int c = s_pre[ls + 1] - s_pre[ls]; lj >= c;) {
-        lj -= c;
-        if (++lu < U) continue;
-        lu = 0;
-        do {
-          if (++ls == S) break;
-          c = s_pre[ls + 1] - s_pre[ls];
-        } while (c == 0);
-        if (ls == S) break;
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) tile[b] = -1;
-      if (32 * group + lane < len) {
-        int hk, h, c;
-        unit_heads(p, lu, hk, h, c);
-        const int nblk = (s_len[ls] + BS - 1) / BS;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          if (lj * NB + b >= nblk) continue;
-          int id = p.block_tables[(long long)ls * p.max_blocks_per_seq + lj * NB + b];
-          if (id < 0 || id >= p.num_blocks) {  // record it, read block 0 instead
-            set_error(p.err, kErrBlockId);
-            id = 0;
-          }
-          tile[b] = id * p.num_kv_heads + hk;
-        }
-      }
-      // the next group starts right after lane 31 (a chunk index past its unit is brought in range there)
-      gs = __shfl_sync(0xffffffffu, ls, 31);
-      gu = __shfl_sync(0xffffffffu, lu, 31);
-      gj = __shfl_sync(0xffffffffu, lj, 31) + 1;
+    auto look_up_next = [&](int positions) {
+      int head;
+      look_up(positions, nxt, head);
+      to_tiles(nxt, head);
     };
-    int cur[NB], nxt[NB], group = 0;
-    look_up(0, cur);
-    if (len > 32) look_up(1, nxt);
+    if (len > 32) look_up_next(len - 32);
     // Chunk k into its stage: K tiles, then V tiles, 16 bytes a lane at a time.  (The second tile of a
     // chunk that ends in its first block is not read; the first is copied again.)
     auto issue = [&](int k) {
       if ((k >> 5) != group) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
-        if (32 * (++group + 1) < len) look_up(group + 1, nxt);
+        if (32 * (++group + 1) < len) look_up_next(len - 32 * (group + 1));
       }
       const unsigned char* from[2 * NB];  // tile i, less the pieces before it: piece x of the chunk is at from[i] + 16 x
 #pragma unroll

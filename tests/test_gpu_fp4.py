@@ -447,6 +447,34 @@ def test_a_captured_call_follows_its_inputs():
         c.check(out)
 
 
+def test_lengths_and_tables_written_right_before_the_call():
+    """The kernel may look at both while the previous kernel still runs: what that one writes must count."""
+    cases = [Case(lens, 4, 2, 128, 16, "f16", i, extra=0) for i, lens in
+             enumerate(([3000, 1, 500, 2999], [1, 1, 1, 1], [17, 3000, 1, 64], [800, 790, 30, 2000]))]
+    width = max(c.table.shape[1] for c in cases)
+    ups = [c.upload() for c in cases]
+    tables = []
+    for u in ups:
+        t = torch.full((4, width), -1, dtype=torch.int32, device="cuda")
+        t[:, :u["table"].shape[1]] = u["table"]
+        tables.append(t)
+    lens, table = torch.ones(4, dtype=torch.int32, device="cuda"), torch.zeros_like(tables[0])
+    outs = []
+    for rep in range(12):
+        i = rep % 4
+        u = ups[i]
+        pad = torch.zeros(1 << 24, device="cuda").cumsum(0)     # a kernel before, so that the host runs ahead
+        table.copy_(tables[i])
+        lens.copy_(u["lens"])
+        outs.append((i, cases[i].run(dict(u, table=table, lens=lens), max_len=3000)))
+        if rep >= 8:                                            # a call of the library in between
+            outs.append((i, cases[i].run(dict(u, table=table, lens=lens), max_len=3000)))
+        del pad
+    no_error()
+    for i, out in outs:
+        cases[i].check(out)
+
+
 def test_calls_on_two_streams_with_their_own_workspaces():
     cases = [Case([2500, 100, 64], 4, 2, 128, 16, "f16"), Case([300, 2500], 4, 4, 128, 16, "f16", 2)]
     ts = [c.upload() for c in cases]
