@@ -127,7 +127,7 @@ pa_status check_fp4_rows(const void* key, const void* value, const void* k_cache
 struct Fp4Plan {
   int chunk;  // sequences per launch
   int grid;
-  size_t off_ml, off_seg, bytes;
+  size_t off_ml, off_tag, bytes;
 };
 
 pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len,
@@ -145,11 +145,11 @@ pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_
   if (chunk < 1) chunk = 1;
   pl->chunk = static_cast<int>(chunk);
   pl->grid = pa::fp4_decode_grid(sms, pl->chunk, num_heads, num_kv_heads, max_seq_len);
-  pl->off_ml = pl->off_seg = pl->bytes = 0;
+  pl->off_ml = pl->off_tag = pl->bytes = 0;
   if (pl->grid > 1) {
     pl->off_ml = (size_t)pl->grid * 2 * 16 * head_size * sizeof(float);
-    pl->off_seg = pl->off_ml + (size_t)pl->grid * 2 * 16 * 2 * sizeof(float);
-    pl->bytes = pl->off_seg + (size_t)pl->grid * 2 * 2 * sizeof(int);
+    pl->off_tag = pl->off_ml + (size_t)pl->grid * 2 * 16 * 2 * sizeof(float);
+    pl->bytes = pl->off_tag + (size_t)pl->grid * sizeof(uint64_t);
   }
   return PA_OK;
 }
@@ -246,6 +246,20 @@ unsigned next_epoch() {
   unsigned e = epoch.fetch_add(1, std::memory_order_relaxed) + 1;
   if (e == 0) e = epoch.fetch_add(1, std::memory_order_relaxed) + 1;
   return e;
+}
+
+// A fresh 64-bit tag for every launch whose CTAs publish pieces to one another: a
+// bijective mix of a counter that starts at a random point, never zero, so that no word
+// an uninitialised workspace may hold is mistaken for it.
+uint64_t next_tag() {
+  static std::atomic<uint64_t> count{(static_cast<uint64_t>(std::random_device{}()) << 32 | std::random_device{}()) ^
+                                     static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count())};
+  for (;;) {
+    uint64_t x = count.fetch_add(1, std::memory_order_relaxed);
+    x = (x ^ (x >> 32)) * 0x9e3779b97f4a7c15ull;
+    x ^= x >> 29;
+    if (x) return x;
+  }
 }
 
 }  // namespace
@@ -812,7 +826,7 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
     char* ws = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
-    p.part_seg = reinterpret_cast<int2*>(ws + pl.off_seg);
+    p.part_tag = reinterpret_cast<uint64_t*>(ws + pl.off_tag);
   }
   p.k_cache = k_cache;
   p.v_cache = v_cache;
@@ -825,6 +839,7 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
   p.max_seq_len = max_seq_len;
   p.scale_log2 = static_cast<float>(scale_log2);
   p.out_scale = v_scale;
+  p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
   const size_t row_bytes = (size_t)num_heads * head_size * 2;
   for (int c0 = 0; c0 < num_seqs; c0 += pl.chunk) {
     p.num_seqs = num_seqs - c0 < pl.chunk ? num_seqs - c0 : pl.chunk;
@@ -832,6 +847,7 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
     p.out = static_cast<char*>(out) + (size_t)c0 * row_bytes;
     p.block_tables = block_tables + (size_t)c0 * max_blocks_per_seq;
     p.seq_lens = seq_lens + c0;
+    p.tag = next_tag();
     int n = 0;
     const cudaError_t ce = pa::launch_decode_fp4(q_dtype == PA_BF16, head_size, block_size, p, pl.grid,
                                                  static_cast<cudaStream_t>(stream), &n);

@@ -20,10 +20,13 @@
 //     tokens interleaved by four bit operations per two words, because an operand register
 //     holds two tokens of one dim.
 //   * Merging: a warp that did a whole segment writes its output.  Pieces cut at a warp's
-//     ends go to shared memory and the CTA merges them once at its end; only pieces cut
-//     at a CTA's ends (at most two a CTA) go through the workspace to a second kernel.
-//     Every slot the second kernel reads was written by this launch, so a call replayed
-//     from a graph never meets an older launch's pieces.
+//     ends go to shared memory and the CTA merges them once at its end.  A segment cut at
+//     CTAs' ends is merged by the CTA that holds its last piece: every other CTA of it
+//     publishes its piece in the workspace with a tag of this call, and the last one waits
+//     for the tags, merges, and clears them.  It waits for CTAs of lower index only, which
+//     are dispatched before it and publish before they wait themselves; the wait is bounded.
+//     A tag is 64 random bits a launch, so the workspace needs no initialisation, and
+//     cleared when used, so a call replayed from a graph never meets an older one's.
 #include <math.h>
 
 #include <type_traits>
@@ -58,6 +61,8 @@ struct Fp4Shape {
   static_assert(kWarps <= 31 && kBytes <= 227 * 1024, "a bit per warp; shared memory per CTA");
 };
 
+constexpr uint64_t kFp4WaitNs = 1000000000ull;  // 1 s, then PA_DEVERR_TIMEOUT
+constexpr int kMergeBatch = 4;                  // pieces of other CTAs loaded at once
 constexpr int kBegins = 1 << 30;  // beside a unit's number: the piece holds its segment's first chunk
 
 __device__ __forceinline__ float ex2(float x) {  // |relative error| < 2^-22, 0 below 2^-126
@@ -78,6 +83,15 @@ __device__ __forceinline__ int ld_now(const int32_t* p) {
   int v;
   asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint64_t ld_acquire(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(uint64_t* p, uint64_t v) {
+  asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
 // One half of a pair, twice.
@@ -731,7 +745,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   const uint32_t firsts = __ballot_sync(0xffffffffu, first.x >= 0), finals = __ballot_sync(0xffffffffu, final.x >= 0);
   const uint32_t begin = __ballot_sync(0xffffffffu, final.x >= 0 && (final.y & kBegins));
   constexpr int kVecs = D / 4;
-  int2 out0 = make_int2(-1, 0), out1 = make_int2(-1, 0);
+  bool publish = false;                // this CTA's last run goes on in the next CTA
+  int tail_s = -1, tail_u = 0;         // the segment of an earlier CTA that ends in this one
   int task = tid;
   // bit 0 of `heads` below: the run that warp 0 starts without beginning a segment; bit w + 1: one that warp w begins
   for (uint32_t heads = begin << 1 | (firsts & 1u) | (finals & ~begin & 1u); heads; heads &= heads - 1) {
@@ -742,8 +757,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     const int w1 = ends ? __ffs(stops) - 1 : 31 - __clz(finals);
     const int2 seg = s_seg[alone ? 0 : 2 * w0 + 1];
     const int s = seg.x, u = seg.y & ~kBegins;
-    if (!begins) out0 = make_int2(s * U + u, ends);
-    else if (!ends) out1 = make_int2(s * U + u, 0);
+    if (!ends) publish = true;
+    else if (!begins) tail_s = s, tail_u = u;
     int kvh, h0, nh;
     unit_heads(p, u, kvh, h0, nh);
     for (; task < nh * kVecs; task += WARPS * 32) {
@@ -773,87 +788,90 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     }
     task -= nh * kVecs;
   }
-  if (tid == 0 && p.part_seg) {
-    p.part_seg[2 * blockIdx.x] = out0;
-    p.part_seg[2 * blockIdx.x + 1] = out1;
+  if (!publish && tail_s < 0) return;  // (the same for all threads of the CTA)
+  __syncthreads();
+  if (publish && tid == 0) {
+    __threadfence();
+    st_release(p.part_tag + blockIdx.x, p.tag);
   }
-}
+  if (tail_s < 0) return;
 
-// CTA b merges the segment whose first piece ends CTA b's run (if there is one): that
-// piece is slot 2 b + 1, the others are slots 2 (b + 1), 2 (b + 2), ... up to the one
-// that ends the segment.  A warp per query head; everything a segment of up to 4 pieces
-// needs is loaded at once, before it is known how many there are.
-constexpr int kFp4MergeWarps = 8, kFp4MergeBatch = 4;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kFp4MergeWarps * 32) decode_fp4_merge_kernel(const Fp4DecodeParams p, int ctas) {
+  // The segment's pieces: its first in CTA head (slot 2 head + 1), the others in slots 2 (head + i),
+  // the last of them this CTA's own.
+  const int total = s_pre[S] * U, workers = min(total, static_cast<int>(gridDim.x) * WARPS);
+  const int share = total / workers, more = total - share * workers;
+  const int at = s_pre[tail_s] * U + tail_u * (s_pre[tail_s + 1] - s_pre[tail_s]);  // its first chunk
+  int head = blockIdx.x;
+  for (;;) {  // the last CTA before this one whose first chunk is not past it
+    const int w = max(head - 1 - lane, 0) * WARPS;
+    const uint32_t from = __ballot_sync(0xffffffffu, w * share + w * more / workers <= at);
+    if (from) {
+      head -= __ffs(from);
+      break;
+    }
+    head -= 32;
+  }
+  const int pieces = static_cast<int>(blockIdx.x) - head + 1;
+  if (warp == 0) {
+    const uint64_t t0 = global_timer_ns(), limit = p.test_wait_ns ? p.test_wait_ns : kFp4WaitNs;
+    const uint64_t want = p.test_wait_ns ? ~p.tag : p.tag;  // (the test's wait: for what nobody publishes)
+    for (int c = head + lane; c < static_cast<int>(blockIdx.x); c += 32)
+      while (ld_acquire(p.part_tag + c) != want)
+        if (global_timer_ns() - t0 > limit) {
+          set_error(p.err, kErrTimeout);
+          break;
+        }
+  }
+  __syncthreads();
+  int kvh, h0, nh;
+  unit_heads(p, tail_u, kvh, h0, nh);
   constexpr int C = D / 32;
   using Vec = std::conditional_t<C == 4, float4, float2>;
-  const int b = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kFp4MergeWarps + (threadIdx.x >> 5);
-  auto slot = [&](int i) { return i == 0 ? 2 * b + 1 : 2 * (b + i); };  // of piece i
-  griddep_wait();
-  griddep_launch_dependents();
-  int2 info = make_int2(-1, 0);  // lane i: of piece i
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (b + lane < ctas) {
-    info = p.part_seg[slot(lane)];
-    ml = p.part_ml[slot(lane) * 16 + r];
-  }
-  Vec o[kFp4MergeBatch];
-  auto load = [&](int i0) {
+  auto slot = [&](int i) { return i == 0 ? 2 * head + 1 : 2 * (head + i); };
+  for (int r = warp; r < nh; r += WARPS) {  // a warp per query head, 32 pieces at a time
+    float M = -INFINITY, W = 0.f, O[C] = {};
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+      const int cnt = min(32, pieces - i0);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < cnt) ml = __ldcg(p.part_ml + slot(i0 + lane) * 16 + r);
+      Vec o[kMergeBatch];
+      auto load = [&](int i1) {
 #pragma unroll
-    for (int i = 0; i < kFp4MergeBatch; ++i)
-      if (b + i0 + i < ctas) o[i] = *reinterpret_cast<const Vec*>(p.part_o + (slot(i0 + i) * 16 + r) * D + lane * C);
-  };
-  load(0);
-  const int seg = __shfl_sync(0xffffffffu, info.x, 0);
-  if (seg < 0) return;
-  const int s = seg / p.units;
-  int kvh, h0, nh;
-  unit_heads(p, seg - s * p.units, kvh, h0, nh);
-  if (r >= nh) return;
-  float M = -INFINITY, W = 0.f, O[C] = {};
-  for (int i0 = 0;; i0 += 32) {  // 32 pieces at a time
-    // up to the piece that ends the segment
-    const uint32_t stop = __ballot_sync(0xffffffffu, info.x != seg || info.y);
-    int cnt = 32;
-    if (stop) {
-      cnt = __ffs(stop) - 1;
-      cnt += __shfl_sync(0xffffffffu, info.x, cnt) == seg;
-    }
-    if (lane >= cnt) ml = make_float2(-INFINITY, 0.f);
-    float top = fmaxf(ml.x, M);
+        for (int i = 0; i < kMergeBatch; ++i)
+          if (i1 + i < cnt)
+            o[i] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + (slot(i0 + i1 + i) * 16 + r) * D + lane * C));
+      };
+      load(0);
+      float top = fmaxf(ml.x, M);
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float keep = ex2(M - top), f = ex2(ml.x - top);
-    float w = f * ml.y;
+      for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float keep = ex2(M - top), f = ex2(ml.x - top);
+      float w = f * ml.y;
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
-    M = top;
-    W = W * keep + w;
+      for (int x = 1; x < 32; x <<= 1) w += __shfl_xor_sync(0xffffffffu, w, x);
+      M = top;
+      W = W * keep + w;
 #pragma unroll
-    for (int c = 0; c < C; ++c) O[c] *= keep;
-    for (int i1 = 0; i1 < cnt; i1 += kFp4MergeBatch) {
-      if (i0 + i1 > 0) load(i0 + i1);
+      for (int c = 0; c < C; ++c) O[c] *= keep;
+      for (int i1 = 0; i1 < cnt; i1 += kMergeBatch) {
+        if (i1 > 0) load(i1);
 #pragma unroll
-      for (int i = 0; i < kFp4MergeBatch; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, (i1 + i) & 31);
-        const float* v = reinterpret_cast<const float*>(&o[i]);
-        if (i1 + i < cnt) {
+        for (int i = 0; i < kMergeBatch; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, (i1 + i) & 31);
+          if (i1 + i < cnt) {
+            const float* v = reinterpret_cast<const float*>(&o[i]);
 #pragma unroll
-          for (int c = 0; c < C; ++c) O[c] = fmaf(fi, v[c], O[c]);
+            for (int c = 0; c < C; ++c) O[c] = fmaf(fi, v[c], O[c]);
+          }
         }
       }
     }
-    if (stop) break;
-    const int at = b + i0 + 32 + lane;  // the CTA of piece i0 + 32 + lane
-    info = at < ctas ? p.part_seg[2 * at] : make_int2(-1, 0);
-    ml = at < ctas ? p.part_ml[2 * at * 16 + r] : make_float2(-INFINITY, 0.f);
-  }
-  const float il = p.out_scale / W;
-  T* out = static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + lane * C;
+    const float il = p.out_scale / W;
+    T* out = static_cast<T*>(p.out) + ((long long)tail_s * p.num_heads + h0 + r) * D + lane * C;
 #pragma unroll
-  for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(O[c] * il, O[c + 1] * il);
+    for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(O[c] * il, O[c + 1] * il);
+  }
+  for (int c = head + tid; c < static_cast<int>(blockIdx.x); c += WARPS * 32) p.part_tag[c] = 0;
 }
 
 template <typename T, int D, int BS, int NT>
@@ -872,10 +890,7 @@ cudaError_t launch_t(const Fp4DecodeParams& p, int grid, cudaStream_t stream, in
   e = launch_pdl(decode_fp4_kernel<T, D, BS, NT>, dim3(grid), dim3(Sh::kWarps * 32), Sh::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   *launches = 1;
-  if (grid == 1) return cudaSuccess;  // one CTA: nothing is cut at a CTA's end
-  e = launch_pdl(decode_fp4_merge_kernel<T, D>, dim3(grid - 1, NT), dim3(kFp4MergeWarps * 32), 0, stream, p, grid);
-  if (e == cudaSuccess) *launches = 2;
-  return e;
+  return cudaSuccess;
 }
 
 template <typename T, int D, int BS>
@@ -896,7 +911,7 @@ cudaError_t launch_shape(int head_size, int block_size, const Fp4DecodeParams& p
 
 }  // namespace
 
-// Chunks a warp should have before another CTA is worth its part of the merge.
+// Chunks a warp should have before another CTA is worth its part of the merging.
 constexpr int kFp4MinChunks = 2;
 
 int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len) {

@@ -232,7 +232,9 @@ struct Fp4DecodeParams {
   // the workspace (null when the grid is one CTA): two pieces per CTA, 16 rows each
   float* part_o;                // [2 grid, 16, D]: unnormalised partial outputs
   float2* part_ml;              // [2 grid, 16]: (maximum in log2 units, sum)
-  int2* part_seg;               // [2 grid]: (segment or -1, whether the piece ends it)
+  uint64_t* part_tag;           // [grid]: `tag` once the CTA's piece of a segment that goes on is there
+  uint64_t tag;                 // this launch's own
+  unsigned long long test_wait_ns;  // > 0 only in the timeout-path test (see pa_set_test_wait_limit)
 };
 inline int fp4_decode_units(int num_heads, int num_kv_heads) {
   return num_kv_heads * ((num_heads / num_kv_heads + 15) / 16);

@@ -293,6 +293,8 @@ def test_decode_lengths_and_groups(q_dtype, D, bs, G):
     ("f16", 64, 16, 1, 5, [1, 1, 1, 7000, 1]),
     ("f16", 128, 32, 20, 1, [5000, 4999, 5001]),
     ("f16", 128, 16, 1, 32, [513, 600]),
+    ("f16", 64, 16, 2, 1, [150001]),                  # one segment over every CTA
+    ("bf16", 128, 16, 1, 1, [3, 60000, 1]),
 ])
 def test_decode_long_and_ragged(q_dtype, D, bs, G, Hkv, lens):
     c = Case(lens, G, Hkv, D, bs, q_dtype)
@@ -525,6 +527,42 @@ def test_pools_past_32_bit_offsets():
     out = c.run(t)
     no_error()
     c.check(out)
+
+
+@pytest.mark.parametrize("lens,G,D", [([1, 17, 300, 2500, 40, 900], 7, 128), ([6000, 5000], 12, 64), ([40000], 1, 128)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_correct(lens, G, D):
+    """Every CTA that waits for pieces of other CTAs waits for a tag nobody writes, for 2 ms: the wait runs
+    out, the call returns."""
+    import paged_kv_cache_306_gb300 as pa
+    c = Case(lens, G, 2, D, 16, "f16")
+    t = c.upload()
+    need = pa.pa_decode_fp4_workspace_size(len(lens), 2 * G, 2, D, c.max_len, 16)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    try:
+        pa.pa_set_test_wait_limit(2_000_000)
+        c.run(t, workspace=ws)
+    finally:
+        pa.pa_set_test_wait_limit(0)
+    assert pa.pa_get_device_error() == 4 and pa.pa_get_device_error() == 0
+    out = c.run(t, workspace=ws)
+    no_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("fill", [0x00, 0xFF, 0xA5])
+def test_a_workspace_may_hold_anything(fill):
+    import paged_kv_cache_306_gb300 as pa
+    c = Case([5000, 1, 900, 3000], 4, 2, 128, 16, "f16")
+    t = c.upload()
+    ws = torch.full((pa.pa_decode_fp4_workspace_size(4, 8, 2, 128, 5000, 16),), fill, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        out = c.run(t, workspace=ws)
+    no_error()
+    c.check(out)
+    short = Case([70, 2000], 8, 2, 64, 32, "bf16")       # another shape on the same workspace, and back
+    short.check(short.run(workspace=ws))
+    c.check(c.run(t, workspace=ws))
+    no_error()
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.09, 3.0e-5])
