@@ -52,7 +52,9 @@ struct Fp4Shape {
   static constexpr int kPiece = kRows * D * 4;                  // an unnormalised partial output
   static constexpr int kFirst = kWarps * kStages * kStage;      // [warps]: the piece a warp starts with
   static constexpr int kMl = kFirst + kWarps * kPiece;          // [2 warps][rows]: (m, l)
-  static constexpr int kSeg = kMl + 2 * kWarps * kRows * 8;     // [2 warps] int2: (sequence or -1, unit and kBegins)
+  static constexpr int kRun = kMl + 2 * kWarps * kRows * 8;     // [warps + 1][rows]: a run's (M, W), by its first warp
+  static constexpr int kFactor = kRun + (kWarps + 1) * kRows * 8; // [2 warps][rows]: a piece's weight in its run
+  static constexpr int kSeg = kFactor + 2 * kWarps * kRows * 4; // [2 warps] int2: (sequence or -1, unit and kBegins)
   static constexpr int kLen = kSeg + 2 * kWarps * 8;            // [seqs]
   static constexpr int kPre = kLen + kMaxSeqsPerLaunch * 4;     // [seqs + 1], then the scan's warp sums
   static constexpr int kBytes = kPre + (kMaxSeqsPerLaunch + 1 + kWarps + 3) * 4;
@@ -481,6 +483,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
                                            : smem + Sh::kFirst + (e >> 1) * Sh::kPiece);
   };
   float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
+  float2* s_run = reinterpret_cast<float2*>(smem + Sh::kRun);
+  float* s_factor = reinterpret_cast<float*>(smem + Sh::kFactor);
   int2* s_seg = reinterpret_cast<int2*>(smem + Sh::kSeg);
   int* s_len = reinterpret_cast<int*>(smem + Sh::kLen);
   int* s_pre = reinterpret_cast<int*>(smem + Sh::kPre);
@@ -501,11 +505,11 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   for (int k = 0; k < PER; ++k) lens[k] = tid * PER + k < S ? ld_now(p.seq_lens + tid * PER + k) : 0;
   int start = 0, len = 0, s = 0, u = 0, j = 0;  // the run; its first chunk is chunk j of unit u of sequence s
   int gs = 0, gu = 0, gj = 0;                   // the first position of the next 32 to look up
-  int cur[NB], nxt[NB];                         // lane i: the blocks, then the tiles, of position i of 32 (-1: none)
+  int cur[NB], nxt[NB];                         // lane i: the tiles of position i of 32 (-1: none)
   bool bad = false;                             // some length is outside the contract
 
-  // Lane i looks up the blocks of position i of the next 32, and the kv head of all of them.
-  auto look_up = [&](int positions, int (&id)[NB], int& head) {
+  // Lane i looks up position i of the next 32: its blocks (`have` of them) and their kv head.
+  auto look_up = [&](int positions, int (&id)[NB], int& have, int& head) {
     int ls = gs, lu = gu, lj = gj + lane;
     for (int c = s_pre[ls + 1] - s_pre[ls]; lj >= c;) {
       lj -= c;
@@ -517,41 +521,68 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       } while (c == 0);
       if (ls == S) break;
     }
-    head = 0;
+    have = head = 0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) id[b] = -1;
+    for (int b = 0; b < NB; ++b) id[b] = 0;
     if (lane < positions) {
       int h, c;
       unit_heads(p, lu, head, h, c);
-      const int nblk = (s_len[ls] + BS - 1) / BS;
+      have = min((s_len[ls] + BS - 1) / BS - lj * NB, NB);
       const int32_t* row = p.block_tables + (long long)ls * p.max_blocks_per_seq + lj * NB;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (lj * NB + b >= nblk) continue;
-        const int v = ld_now(row + b);
-        id[b] = v < 0 ? 0x7fffffff : v;  // (past any pool)
-      }
+      for (int b = 0; b < NB; ++b)
+        if (b < have) id[b] = ld_now(row + b);
     }
     // the next group starts right after lane 31 (a chunk index past its unit is brought in range there)
     gs = __shfl_sync(0xffffffffu, ls, 31);
     gu = __shfl_sync(0xffffffffu, lu, 31);
     gj = __shfl_sync(0xffffffffu, lj, 31) + 1;
   };
-  // Blocks to tiles; one outside the pool is recorded, and block 0 read instead.
-  auto to_tiles = [&](int (&id)[NB], int head) {
+  // Blocks to tiles (-1: none); block 0 for one outside the pool.  Whether there was one.
+  auto to_tiles = [&](const int (&id)[NB], int have, int head, int (&tile)[NB]) {
+    bool out = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      if (id[b] < 0) continue;
-      if (id[b] >= p.num_blocks) {
-        set_error(p.err, kErrBlockId);
-        id[b] = 0;
-      }
-      id[b] = id[b] * p.num_kv_heads + head;
+      const bool wrong = id[b] < 0 || id[b] >= p.num_blocks;
+      out |= b < have && wrong;
+      tile[b] = b < have ? (wrong ? 0 : id[b]) * p.num_kv_heads + head : -1;
+    }
+    return out;
+  };
+  // Chunk k, its tiles in lane k % 32, into its stage: K, then V, 16 bytes a lane at a time.  (The second
+  // tile of a chunk that ends in its first block is not read; the first is copied again.)
+  auto copy_chunk = [&](int k) {
+    const unsigned char* from[2 * NB];  // tile i, less the pieces before it: piece x of the chunk is at from[i] + 16 x
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      int t = __shfl_sync(0xffffffffu, cur[b], k & 31);
+      if (b > 0 && t < 0) t = __shfl_sync(0xffffffffu, cur[0], k & 31);
+      from[b] = static_cast<const unsigned char*>(p.k_cache) + (long long)t * TILE + (16 * lane - b * TILE);
+      from[NB + b] = static_cast<const unsigned char*>(p.v_cache) + (long long)t * TILE + (16 * lane - (NB + b) * TILE);
+    }
+    constexpr int kPer = TILE / 16, kAll = 2 * NB * kPer;  // 16-byte pieces of a tile, of a chunk
+    const uint32_t to = smem_addr(ring) + (k % STAGES) * Sh::kStage + 16 * lane;
+#pragma unroll
+    for (int x = 0; x < kAll; x += 32) {
+      const int i0 = x / kPer, i1 = (x + 31 < kAll ? x + 31 : kAll - 1) / kPer;  // at most two tiles
+      const unsigned char* src = from[i0];
+      if (i1 != i0 && x + lane >= i1 * kPer) src = from[i1];
+      if (x + 32 <= kAll || x + lane < kAll) copy16(to + 16 * x, src + 16 * x);
     }
   };
+  Math math;
+  math.init(lane);
+  int L = 0, n = 0, h0 = 0, nh = 0, kvh = 0;  // the current segment
+  auto fetch_q = [&]() {
+    L = s_len[s];
+    n = (L + kChunk - 1) / kChunk;
+    unit_heads(p, u, kvh, h0, nh);
+    math.load_q(static_cast<const T*>(p.q) + ((long long)s * p.num_heads + h0) * D, nh);
+  };
 
+  bool bad_id = false;
   for (bool waited = false;; waited = true) {
-    int n[PER], sum = 0;
+    int count[PER], sum = 0;
     bad = false;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -560,8 +591,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       const int L = out ? 0 : lens[k];
       bad |= out && i < S;
       if (i < S) s_len[i] = L;
-      n[k] = (L + kChunk - 1) / kChunk;
-      sum += n[k];
+      count[k] = (L + kChunk - 1) / kChunk;
+      sum += count[k];
     }
     int incl = sum;
 #pragma unroll
@@ -576,7 +607,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     for (int k = 0; k < PER; ++k) {
       const int i = tid * PER + k;
       if (i <= S) s_pre[i] = before;
-      before += n[k];
+      before += count[k];
     }
     if (tid == WARPS * 32 - 1) s_pre[S] = before;
     __syncthreads();
@@ -591,9 +622,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       start = me * share + me * more / workers;
       len = (me + 1) * share + (me + 1) * more / workers - start;
     }
-    int head = 0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) cur[b] = -1;
+    int id[NB] = {}, have = 0, head = 0;
     if (len > 0) {
       // The sequence: the last one whose prefix is at most the start, found by the warp together in
       // 32-way steps (empty sequences have their successor's prefix).
@@ -607,31 +636,40 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       u = r / c;
       j = r - u * c;
       gs = s, gu = u, gj = j;
-      look_up(len, cur, head);
+      look_up(len, id, have, head);
     }
-    bool again = false;
-    if (!waited) {
+    int now_len[PER], now_id[NB] = {};
+    if (!waited) {  // what has to read the same
       griddep_wait();
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int now = tid * PER + k < S ? ld_now(p.seq_lens + tid * PER + k) : 0;
-        again |= now != lens[k];
-        lens[k] = now;
-      }
+      for (int k = 0; k < PER; ++k) now_len[k] = tid * PER + k < S ? ld_now(p.seq_lens + tid * PER + k) : 0;
       if (len > 0) {
-        int now[NB];
         gs = s, gu = u, gj = j;
-        look_up(len, now, head);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) again |= now[b] != cur[b];
+        look_up(len, now_id, have, head);
       }
-      again = __syncthreads_or(again);
     }
-    if (!again) {
-      to_tiles(cur, head);
-      break;
+    // the first chunks and the query rows are asked for in the meantime (every tile lies in the pool)
+    bad_id = to_tiles(id, have, head, cur);
+    if (len > 0) fetch_q();
+#pragma unroll 1
+    for (int k = 0; k < STAGES; ++k) {  // a group of copies per chunk, empty past the end
+      if (k < len) copy_chunk(k);
+      copies_close();
     }
+    if (waited) break;
+    bool again = false;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      again |= now_len[k] != lens[k];
+      lens[k] = now_len[k];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) again |= now_id[b] != id[b];
+    if (!__syncthreads_or(again)) break;
+    copies_wait<0>();
+    __syncwarp();
   }
+  if (bad_id) set_error(p.err, kErrBlockId);
 
   if (bad && blockIdx.x == 0) {
     if (tid == 0) set_error(p.err, kErrSeqLen);
@@ -643,53 +681,21 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   }
 
   if (len > 0) {
-    int L, n, h0, nh, kvh, group = 0;
-    Math math;
-    math.init(lane);
-    auto fetch_q = [&]() {
-      L = s_len[s];
-      n = (L + kChunk - 1) / kChunk;
-      unit_heads(p, u, kvh, h0, nh);
-      math.load_q(static_cast<const T*>(p.q) + ((long long)s * p.num_heads + h0) * D, nh);
-    };
-    fetch_q();
+    int group = 0;
     auto look_up_next = [&](int positions) {
-      int head;
-      look_up(positions, nxt, head);
-      to_tiles(nxt, head);
+      int id[NB], have, head;
+      look_up(positions, id, have, head);
+      if (to_tiles(id, have, head, nxt)) set_error(p.err, kErrBlockId);
     };
     if (len > 32) look_up_next(len - 32);
-    // Chunk k into its stage: K tiles, then V tiles, 16 bytes a lane at a time.  (The second tile of a
-    // chunk that ends in its first block is not read; the first is copied again.)
     auto issue = [&](int k) {
       if ((k >> 5) != group) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
         if (32 * (++group + 1) < len) look_up_next(len - 32 * (group + 1));
       }
-      const unsigned char* from[2 * NB];  // tile i, less the pieces before it: piece x of the chunk is at from[i] + 16 x
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        int t = __shfl_sync(0xffffffffu, cur[b], k & 31);
-        if (b > 0 && t < 0) t = __shfl_sync(0xffffffffu, cur[0], k & 31);
-        from[b] = static_cast<const unsigned char*>(p.k_cache) + (long long)t * TILE + (16 * lane - b * TILE);
-        from[NB + b] = static_cast<const unsigned char*>(p.v_cache) + (long long)t * TILE + (16 * lane - (NB + b) * TILE);
-      }
-      constexpr int kPer = TILE / 16, kAll = 2 * NB * kPer;  // 16-byte pieces of a tile, of a chunk
-      const uint32_t to = smem_addr(ring) + (k % STAGES) * Sh::kStage + 16 * lane;
-#pragma unroll
-      for (int x = 0; x < kAll; x += 32) {
-        const int i0 = x / kPer, i1 = (x + 31 < kAll ? x + 31 : kAll - 1) / kPer;  // at most two tiles
-        const unsigned char* src = from[i0];
-        if (i1 != i0 && x + lane >= i1 * kPer) src = from[i1];
-        if (x + 32 <= kAll || x + lane < kAll) copy16(to + 16 * x, src + 16 * x);
-      }
+      copy_chunk(k);
     };
-    for (int k = 0; k < STAGES; ++k) {  // a group of copies per chunk, empty past the end
-      if (k < len) issue(k);
-      copies_close();
-    }
-
     math.reset();
     math.scale_q(p.scale_log2);
     int j0 = j;  // where the current piece starts
@@ -738,59 +744,93 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
 
   // The CTA's pieces: a run of them is one segment's, one per warp, warps w0 .. w1.  A run starts
   // with a last piece that begins its segment, or with warp 0; it stops at the first warp after
-  // that has a first piece (which ends the segment), or with the CTA's last working warp.  A
-  // thread takes 4 dims of a head of a run.
+  // that has a first piece (which ends the segment), or with the CTA's last working warp.
   const int2 first = lane < WARPS ? s_seg[2 * lane] : make_int2(-1, 0);
   const int2 final = lane < WARPS ? s_seg[2 * lane + 1] : make_int2(-1, 0);
   const uint32_t firsts = __ballot_sync(0xffffffffu, first.x >= 0), finals = __ballot_sync(0xffffffffu, final.x >= 0);
   const uint32_t begin = __ballot_sync(0xffffffffu, final.x >= 0 && (final.y & kBegins));
-  constexpr int kVecs = D / 4;
+  // the last warp of a run whose piece of warp w does not end it, and whether the run ends its segment
+  auto run_end = [&](int w, bool& ends) {
+    const uint32_t stops = firsts & ~((2u << w) - 1u);
+    ends = stops != 0;
+    return ends ? __ffs(stops) - 1 : 31 - __clz(finals);
+  };
+  // Every (piece, head)'s factor in its run, and the run's (M, W) beside its first piece.
+  for (int i = tid; i < 2 * WARPS * Sh::kRows; i += WARPS * 32) {
+    const int e = i / Sh::kRows, r = i % Sh::kRows, w = e >> 1;
+    if (!(((e & 1 ? finals : firsts) >> w) & 1u)) continue;
+    const uint32_t before = begin & ((1u << (w + (e & 1))) - 1u);  // a first piece's run began in an earlier warp
+    const int w0 = before ? 31 - __clz(before) : 0;
+    bool ends = true;
+    const int w1 = e & 1 ? run_end(w, ends) : w;
+    auto ml = [&](int x) { return s_ml[(2 * x + (ends && x == w1 ? 0 : 1)) * Sh::kRows + r]; };
+    float M = -INFINITY, W = 0.f;
+#pragma unroll 4
+    for (int x = w0; x <= w1; ++x) M = fmaxf(M, ml(x).x);
+    if (w == w0) {
+#pragma unroll 4
+      for (int x = w0; x <= w1; ++x) W = fmaf(ex2(ml(x).x - M), ml(x).y, W);
+      s_run[(e & 1 ? w : WARPS) * Sh::kRows + r] = make_float2(M, W);  // (a first piece alone: warp 0's)
+    }
+    s_factor[i] = ex2(s_ml[i].x - M);
+  }
+  __syncthreads();
+  // A warp takes a head of a run, a lane D/32 dims.
+  constexpr int C = D / 32, kRingBytes = STAGES * Sh::kStage;
+  using Vec = std::conditional_t<C == 4, float4, float2>;
   bool publish = false;                // this CTA's last run goes on in the next CTA
   int tail_s = -1, tail_u = 0;         // the segment of an earlier CTA that ends in this one
-  int task = tid;
+  int task = warp;
   // bit 0 of `heads` below: the run that warp 0 starts without beginning a segment; bit w + 1: one that warp w begins
   for (uint32_t heads = begin << 1 | (firsts & 1u) | (finals & ~begin & 1u); heads; heads &= heads - 1) {
     const int hd = __ffs(heads) - 1, w0 = hd ? hd - 1 : 0;
     const bool alone = hd == 0 && (firsts & 1u);  // warp 0's first piece ends a segment that an earlier CTA began
-    const uint32_t stops = alone ? 1u : firsts & ~((2u << w0) - 1u);
-    const bool begins = hd != 0, ends = stops != 0;
-    const int w1 = ends ? __ffs(stops) - 1 : 31 - __clz(finals);
+    const bool begins = hd != 0;
+    bool ends = true;
+    const int w1 = alone ? 0 : run_end(w0, ends);
     const int2 seg = s_seg[alone ? 0 : 2 * w0 + 1];
     const int s = seg.x, u = seg.y & ~kBegins;
     if (!ends) publish = true;
     else if (!begins) tail_s = s, tail_u = u;
     int kvh, h0, nh;
     unit_heads(p, u, kvh, h0, nh);
-    for (; task < nh * kVecs; task += WARPS * 32) {
-      const int r = task / kVecs, v = task % kVecs;
-      auto entry = [&](int w) { return 2 * w + (ends && w == w1 ? 0 : 1); };
-      float M = -INFINITY, W = 0.f;
+    for (; task < nh; task += WARPS) {
+      const int r = task;
+      // the same place in every piece: in the warps' rings, and at a run's end perhaps in a first piece
+      const unsigned char* at = reinterpret_cast<const unsigned char*>(Math::piece_at(
+                                    reinterpret_cast<const float4*>(smem), r, lane * C / 4)) + lane * C % 4 * 4;
+      const int rings = w1 + (ends ? 0 : 1);
+      float O[C] = {};
+      auto add = [&](const unsigned char* from, float f) {
+        const Vec v = *reinterpret_cast<const Vec*>(from);
+        const float* vf = reinterpret_cast<const float*>(&v);
+#pragma unroll
+        for (int c = 0; c < C; ++c) O[c] = fmaf(f, vf[c], O[c]);
+      };
 #pragma unroll 4
-      for (int w = w0; w <= w1; ++w) M = fmaxf(M, s_ml[entry(w) * Sh::kRows + r].x);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int w = w0; w <= w1; ++w) {
-        const float2 ml = s_ml[entry(w) * Sh::kRows + r];
-        const float4 x = *Math::piece_at(piece(entry(w)), r, v);
-        const float f = ex2(ml.x - M);
-        W = fmaf(f, ml.y, W);
-        o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, x.z, o.z), fmaf(f, x.w, o.w));
-      }
+      for (int w = w0; w < rings; ++w) add(at + w * kRingBytes, s_factor[(2 * w + 1) * Sh::kRows + r]);
+      if (ends) add(at + Sh::kFirst + w1 * Sh::kPiece, s_factor[2 * w1 * Sh::kRows + r]);
+      const float2 sum = s_run[(alone ? WARPS : w0) * Sh::kRows + r];
       if (begins && ends) {
-        const float il = p.out_scale / W;
-        *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + 4 * v) =
-            make_uint2(pack2<T>(o.x * il, o.y * il), pack2<T>(o.z * il, o.w * il));
+        const float il = p.out_scale / sum.y;
+        T* out = static_cast<T*>(p.out) + ((long long)s * p.num_heads + h0 + r) * D + lane * C;
+#pragma unroll
+        for (int c = 0; c < C; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack2<T>(O[c] * il, O[c + 1] * il);
       } else {
         const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-        reinterpret_cast<float4*>(p.part_o)[(slot * 16 + r) * kVecs + v] = o;
-        if (v == 0) p.part_ml[slot * 16 + r] = make_float2(M, W);
+        Vec v;
+        float* vf = reinterpret_cast<float*>(&v);
+#pragma unroll
+        for (int c = 0; c < C; ++c) vf[c] = O[c];
+        *reinterpret_cast<Vec*>(p.part_o + (slot * 16 + r) * D + lane * C) = v;
+        if (lane == 0) p.part_ml[slot * 16 + r] = sum;
       }
     }
-    task -= nh * kVecs;
+    task -= nh;
   }
   if (!publish && tail_s < 0) return;  // (the same for all threads of the CTA)
   __syncthreads();
-  if (publish && tid == 0) {
+  if (publish && tid == (WARPS - 1) * 32) {  // (not the warp that waits below)
     __threadfence();
     st_release(p.part_tag + blockIdx.x, p.tag);
   }
@@ -823,10 +863,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
         }
   }
   __syncthreads();
-  int kvh, h0, nh;
   unit_heads(p, tail_u, kvh, h0, nh);
-  constexpr int C = D / 32;
-  using Vec = std::conditional_t<C == 4, float4, float2>;
   auto slot = [&](int i) { return i == 0 ? 2 * head + 1 : 2 * (head + i); };
   for (int r = warp; r < nh; r += WARPS) {  // a warp per query head, 32 pieces at a time
     float M = -INFINITY, W = 0.f, O[C] = {};
