@@ -111,9 +111,9 @@ pa_status check_fp4_rows(const void* key, const void* value, const void* k_cache
   if (dtype != PA_F32 && dtype != PA_F16 && dtype != PA_BF16)
     return fail(PA_ERR_UNSUPPORTED, "rows beside an FP4 cache are fp32, fp16 or bf16");
   if (num_tokens < 0 || num_tokens > 0x7fffffffLL) return fail(PA_ERR_INVALID_ARG, "num_tokens %lld", (long long)num_tokens);
-  // a launch has a thread per group of 16 dims: its grid must stay below 2^31 CTAs
-  if (num_tokens * num_kv_heads > 0x7fffffffLL * (16 * 256 / head_size))
-    return fail(PA_ERR_UNSUPPORTED, "too many rows (%lld tokens, %d kv heads)", (long long)num_tokens, num_kv_heads);
+  if (num_tokens * num_kv_heads > 0x7fffffffLL)
+    return fail(PA_ERR_UNSUPPORTED, "more than 2^31 - 1 rows (%lld tokens, %d kv heads)", (long long)num_tokens,
+                num_kv_heads);
   if (num_tokens == 0) return PA_OK;
   if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_INVALID_ARG, "null pointer");
   if (!aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
