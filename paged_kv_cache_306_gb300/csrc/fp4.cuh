@@ -18,8 +18,6 @@
 //   * V scales: group-major, the tokens of a group adjacent.
 #pragma once
 
-#include <cuda_fp4.h>
-
 #include "pa_device.cuh"
 
 namespace pa {
@@ -71,14 +69,17 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Eight fp32 values to E2M1 codes: nearest, ties to even, at most 6.
+// Eight fp32 values to E2M1 codes: nearest, ties to even, at most 6 (a NaN: 6).
 __device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_E2M1,
-                                                        cudaRoundNearest))
-         << (8 * i);
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return w;
 }
 

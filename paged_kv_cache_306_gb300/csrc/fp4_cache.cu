@@ -110,8 +110,10 @@ __device__ __forceinline__ bool locate_row(const int64_t* slot_mapping, int rows
   return true;
 }
 
+// (16-bit rows: six CTAs of an SM in 42 registers a thread hide the loads, 62.9 -> 58.9 us for 65536
+// tokens x 8 heads x 128 dims; fp32 rows are 32 registers a thread and slow down below 50.)
 template <typename T, int D, int BS, bool kWide>
-__global__ void __launch_bounds__(kFp4Threads)
+__global__ void __launch_bounds__(kFp4Threads, sizeof(T) == 2 ? 6 : 1)
     reshape_and_cache_fp4_kernel(const T* key, const T* value, unsigned char* k_cache, unsigned char* v_cache,
                                  const int64_t* slot_mapping, int rows, int num_kv_heads, long long num_blocks,
                                  float k_scale, float v_scale, float k_inv, float v_inv, unsigned* err) {
@@ -153,28 +155,38 @@ __device__ __forceinline__ uint4 widen16(uint32_t codes, uint32_t sf2, float s) 
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The write's inverse: the rows of the slots, in T.  A thread takes 16 bytes of a row of K
-// and of V, so that a warp's stores are whole rows.
+// The write's inverse: the rows of the slots, in T.  D/16 threads a row, each 16 bytes of
+// every 1/2 (16-bit T) or 1/4 (fp32) of it, K and V, so that each of a warp's stores is whole
+// runs of 128 or 64 bytes and a thread has 8 or 16 loads in flight.
 template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kFp4Threads)
     gather_cache_fp4_kernel(T* key, T* value, const unsigned char* k_cache, const unsigned char* v_cache,
                             const int64_t* slot_mapping, int rows, int num_kv_heads, long long num_blocks,
                             float k_scale, float v_scale, unsigned* err) {
-  constexpr int kDims = 16 / sizeof(T);  // a thread's
+  constexpr int kDims = 16 / sizeof(T), TR = D / 16, N = 16 / kDims;  // dims of 16 bytes, threads a row, parts a thread
   using Codes = std::conditional_t<kDims == 8, uint32_t, uint16_t>;
   griddep_wait();
   griddep_launch_dependents();
-  int row, c, off;
+  int row, part, off;
   long long tile;
-  if (!locate_row<D, BS, D / kDims>(slot_mapping, rows, num_kv_heads, num_blocks, err, row, c, tile, off)) return;
-  const int g = c * kDims / 16, at = fp4::code_at<D>(off, c * kDims / 2);
-  const uint32_t kc = *reinterpret_cast<const Codes*>(k_cache + tile + at);
-  const uint32_t vc = *reinterpret_cast<const Codes*>(v_cache + tile + at);
-  const uint32_t ks = k_cache[tile + fp4::k_scale_at<D, BS>(off, g)];
-  const uint32_t vs = v_cache[tile + fp4::v_scale_at<D, BS>(off, g)];
-  const long long to = (long long)row * D + c * kDims;
-  *reinterpret_cast<uint4*>(key + to) = widen16<T>(kc, fp4::e4m3x2_to_f16x2(ks | ks << 8), k_scale);
-  *reinterpret_cast<uint4*>(value + to) = widen16<T>(vc, fp4::e4m3x2_to_f16x2(vs | vs << 8), v_scale);
+  if (!locate_row<D, BS, TR>(slot_mapping, rows, num_kv_heads, num_blocks, err, row, part, tile, off)) return;
+  uint32_t kc[N], vc[N], ks[N], vs[N];
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    const int c = part + TR * x, g = c * kDims / 16, at = fp4::code_at<D>(off, c * kDims / 2);
+    kc[x] = *reinterpret_cast<const Codes*>(k_cache + tile + at);
+    vc[x] = *reinterpret_cast<const Codes*>(v_cache + tile + at);
+    ks[x] = k_cache[tile + fp4::k_scale_at<D, BS>(off, g)];
+    vs[x] = v_cache[tile + fp4::v_scale_at<D, BS>(off, g)];
+  }
+  const long long to = (long long)row * D + part * kDims;
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    *reinterpret_cast<uint4*>(key + to + TR * kDims * x) =
+        widen16<T>(kc[x], fp4::e4m3x2_to_f16x2(ks[x] | ks[x] << 8), k_scale);
+    *reinterpret_cast<uint4*>(value + to + TR * kDims * x) =
+        widen16<T>(vc[x], fp4::e4m3x2_to_f16x2(vs[x] | vs[x] << 8), v_scale);
+  }
 }
 
 // Whole blocks into a 16-bit pool (k [.., D/8, BS, 8], v [.., D, BS]).  64 threads take a tile
@@ -182,10 +194,11 @@ __global__ void __launch_bounds__(kFp4Threads)
 // 16 bytes at a time.  K: a thread takes 8 dims of a token, consecutive threads consecutive
 // tokens; V: two dims of 8 tokens, their nibbles interleaved so that the conversion gives token
 // pairs.  Every store instruction fills whole 32-byte sectors.
-constexpr int kExpandHeads = 4, kExpandThreads = 64 * kExpandHeads;
+constexpr int kExpandHeads = 2, kExpandThreads = 64 * kExpandHeads;
 
+// (12 CTAs of an SM against the 8 that ptxas chose: 1793 blocks x 4 heads 14.5 -> 13.4 us.)
 template <typename T, int D, int BS>
-__global__ void __launch_bounds__(kExpandThreads)
+__global__ void __launch_bounds__(kExpandThreads, 12)
     expand_blocks_fp4_kernel(T* k_out, T* v_out, const unsigned char* k_cache, const unsigned char* v_cache,
                              const int64_t* src_dst, int num_kv_heads, long long num_out_blocks, long long num_blocks,
                              float k_scale, float v_scale, unsigned* err) {
@@ -276,8 +289,8 @@ cudaError_t gather_t(void* key, void* value, const unsigned char* kc, const unsi
                      cudaStream_t stream) {
   return for_shape(head_size, block_size, [&](auto d, auto bs) {
     constexpr int D = decltype(d)::value, BS = decltype(bs)::value;
-    return launch_pdl(gather_cache_fp4_kernel<T, D, BS>, dim3(row_blocks(rows, D * sizeof(T) / 16)), dim3(kFp4Threads),
-                      0, stream, static_cast<T*>(key), static_cast<T*>(value), kc, vc, slots, rows, hkv, (long long)nb,
+    return launch_pdl(gather_cache_fp4_kernel<T, D, BS>, dim3(row_blocks(rows, D / 16)), dim3(kFp4Threads), 0,
+                      stream, static_cast<T*>(key), static_cast<T*>(value), kc, vc, slots, rows, hkv, (long long)nb,
                       ks, vs, err);
   });
 }
