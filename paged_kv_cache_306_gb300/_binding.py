@@ -429,11 +429,33 @@ def pa_fp4_tile_bytes(head_size, block_size):
 
 @functools.lru_cache(maxsize=None)
 def _fp4_torch():
-    """What the FP4 calls take from torch on every call, looked up once.  These calls run in a
-    few microseconds on the GPU, so their checks and marshalling are kept as short."""
+    """What the FP4 calls take from torch on every call, looked up once."""
     import torch
     codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
     return torch.uint8, torch.int32, torch.int64, codes, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+@functools.lru_cache(maxsize=None)
+def _fp4_calls():
+    """The extension that checks and marshals the FP4 calls without Python's and ctypes' share of
+    their time (csrc/fp4_calls.cpp), or None where it was not built.  It returns -1 for a call it
+    does not take; the Python code below then takes it, or says what is wrong with it."""
+    import importlib.machinery
+    import importlib.util
+    from . import build
+    path = build.calls_path()
+    if path is None or not os.path.exists(path):
+        return None
+    lib = load()
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_fp4_calls", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fp4_calls", loader, origin=path))
+        loader.exec_module(m)
+    except ImportError:
+        return None
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.pa_reshape_and_cache_fp4, lib.pa_gather_cache_fp4, lib.pa_expand_blocks_fp4, lib.pa_decode_fp4)))
+    return m
 
 
 def _need_here(name, t, dtype=None, dims=None):
@@ -491,18 +513,33 @@ def _fp4_rows(call, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale
 
 def pa_reshape_and_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None):
     """Quantise key/value [T, Hkv, D] into the FP4 pools through slot_mapping (int64 [T])."""
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.rows(False, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream)
+        if st >= 0:
+            return check(st)
     _fp4_rows(load().pa_reshape_and_cache_fp4, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream)
 
 
 def pa_gather_cache_fp4(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream=None):
     """Read the rows of slot_mapping (int64 [T]) back into key/value [T, Hkv, D] (fp32, fp16
     or bf16); the rows of a negative slot stay as they are."""
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.rows(True, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream)
+        if st >= 0:
+            return check(st)
     _fp4_rows(load().pa_gather_cache_fp4, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream)
 
 
 def pa_expand_blocks_fp4(k_out, v_out, k_cache, v_cache, src_dst, k_scale, v_scale, stream=None):
     """Read whole FP4 blocks back into the 16-bit pools k_out [NB', Hkv, D/8, bs, 8] and v_out
     [NB', Hkv, D, bs]: src_dst is int64 [n, 2] of (FP4 block, 16-bit block)."""
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.expand(k_out, v_out, k_cache, v_cache, src_dst, k_scale, v_scale, stream)
+        if st >= 0:
+            return check(st)
     u8, _, i64, codes, current, raw_stream = _fp4_torch()
     dt, dev = k_out.dtype, k_out.get_device()
     if not (dev >= 0 and dev == current() and k_out.is_contiguous()
@@ -551,6 +588,14 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_s
     and none is given, or too small a one, one is taken from torch's allocator.
     Returns the workspace tensor used (or None).
     """
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.decode(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len, k_scale, v_scale,
+                          workspace, stream)
+        if st == PA_OK:
+            return workspace
+        if st > 0 and st != PA_ERR_WORKSPACE:
+            check(st)
     u8, i32, _, codes, current, raw_stream = _fp4_torch()
     dt, dev = q.dtype, q.get_device()
     if not (dev >= 0 and dev == current() and q.dim() == 3 and q.is_contiguous()

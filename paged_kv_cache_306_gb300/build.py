@@ -4,7 +4,9 @@
 
 Each translation unit is compiled in parallel, then linked into
 paged_kv_cache_306_gb300/_build/libpa.so.  Rebuilds only when a source or header
-is newer than the library.
+is newer than the library.  Beside it goes the CPython extension that marshals the
+FP4 calls (csrc/fp4_calls.cpp), built for the Python and torch at hand; without
+their headers it is left out, and the binding takes its ctypes path.
 """
 import argparse
 import concurrent.futures as cf
@@ -12,6 +14,8 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,38 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr"]
 
 
+def calls_path():
+    """Where the FP4 calls' extension for this Python and torch lies (built or not); None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return os.path.join(OUT_DIR, f"_fp4_calls-{torch.__version__}-{sys.version_info[0]}{sys.version_info[1]}.so")
+
+
+def _build_calls(out):
+    """Compile the FP4 calls' extension; returns an error text, or None."""
+    import torch
+    t = os.path.dirname(torch.__file__)
+    py = sysconfig.get_paths()["include"]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    gxx = shutil.which("g++")
+    for need in (gxx, os.path.join(py, "Python.h"), os.path.join(t, "include", "ATen", "core", "Tensor.h")):
+        if not need or not os.path.exists(need):
+            return f"{need or 'g++'} not found"
+    lib = os.path.join(t, "lib")
+    cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-I", py,
+           "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", cuda, os.path.join(CSRC, "fp4_calls.cpp"), "-o", out + ".tmp", "-L", lib, "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        return r.stderr
+    os.replace(out + ".tmp", out)
+    return None
+
+
 def _nvcc():
     for c in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if c and os.path.exists(c):
@@ -37,6 +73,9 @@ def _stale():
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
+    calls = calls_path()
+    if calls and not os.path.exists(calls) and not os.path.exists(calls + ".failed"):
+        return True
     deps = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -55,13 +94,25 @@ def build(force=False, verbose=False, extra_flags=()):
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
     objs = []
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    calls = calls_path()
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        made = ex.submit(_build_calls, calls) if calls else None
         for src, obj, r in ex.map(lambda s: _compile(nvcc, s, list(extra_flags)), SOURCES):
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
             if verbose and r.stderr:
                 print(r.stderr)
             objs.append(obj)
+        failed = made.result() if made else None
+    if calls:
+        mark = calls + ".failed"
+        for f in (mark, calls) if failed else (mark,):
+            if os.path.exists(f):
+                os.remove(f)
+        if failed:  # the binding works without it, a few microseconds a call slower
+            with open(mark, "w") as f:
+                f.write(failed)
+            print(f"FP4 calls' extension not built ({failed.strip().splitlines()[-1][:200]}): the ctypes path is used")
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)

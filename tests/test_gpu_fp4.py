@@ -639,3 +639,76 @@ def test_a_serving_run_over_an_fp4_cache():
             ref = oracle.decode(q, *pools64(), table, lens, scale, "f64", q_dtype="f16")
             assert (np.abs(as_f64(got) - ref) - half_ulp(ref, "f16")).max() <= TOL["f16"]
     bm.close()
+
+
+# --- the binding ----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("path", ["extension", "ctypes"])
+def test_both_marshalling_paths_check_and_compute_alike(path, monkeypatch):
+    """The compiled marshalling and the Python one: the same results, the same refusals."""
+    import paged_kv_cache_306_gb300 as pa
+    from paged_kv_cache_306_gb300 import _binding as B
+    if path == "extension":
+        assert B._fp4_calls() is not None, "the extension was not built"
+    else:
+        monkeypatch.setattr(B, "_fp4_calls", lambda: None)
+    rng = rng_of("paths")
+    NB, Hkv, D, bs, T = 12, 2, 128, 16, 30
+    key, k64 = store(rng.standard_normal((T, Hkv, D)), "bf16")
+    rows = cuda(key, "bf16")
+    kt = torch.zeros(NB, Hkv, fp4.tile_bytes(D, bs), dtype=torch.uint8, device="cuda")
+    vt = torch.zeros_like(kt)
+    slots = cuda(np.arange(T, dtype=np.int64))
+    back = torch.zeros_like(rows), torch.zeros_like(rows)
+    pa.pa_reshape_and_cache_fp4(rows, rows, kt, vt, slots, KS, VS)
+    pa.pa_gather_cache_fp4(*back, kt, vt, slots, KS, VS)
+    for got, s in zip(back, (KS, VS)):
+        assert np.array_equal(as_f64(got), rounded(fp4.values(*fp4.quantise(k64, s), s), "bf16"))
+    ko = torch.zeros(NB, Hkv, D // 8, bs, 8, dtype=torch.bfloat16, device="cuda")
+    vo = torch.zeros(NB, Hkv, D, bs, dtype=torch.bfloat16, device="cuda")
+    pairs = cuda(np.array([[0, 3], [1, 4]], np.int64))
+    pa.pa_expand_blocks_fp4(ko, vo, kt, vt, pairs, KS, VS)
+    assert torch.equal(vo[3].permute(2, 0, 1), back[1][:16])
+    q = cuda(store(rng.standard_normal((1, 4, D)), "f16")[0], "f16")
+    table, lens, out = cuda(np.array([[0, 1]], np.int32)), cuda(np.array([T], np.int32)), torch.empty_like(q)
+    ws = pa.pa_decode_fp4(out, q, kt, vt, table, lens, 0.1, 32, KS, VS)
+    again = torch.empty_like(out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert pa.pa_decode_fp4(again, q, kt, vt, table, lens, 0.1, 32, KS, VS, ws, side) is ws
+    side.synchronize()
+    assert same_bytes(out, again)
+    long = torch.zeros(1, 2000, dtype=torch.int32, device="cuda")
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    grown = pa.pa_decode_fp4(again, q, kt, vt, long, lens, 0.1, 32000, KS, VS, small)   # too small a workspace
+    assert grown is not small and grown.numel() >= pa.pa_decode_fp4_workspace_size(1, 4, 2, D, 32000, 16) > 16
+    no_error()
+
+    def refused(status, f, *a):
+        with pytest.raises(pa.PAError) as e:
+            f(*a)
+        assert e.value.status == status, str(e.value)
+    bad, unsupported = B.PA_ERR_INVALID_ARG, B.PA_ERR_UNSUPPORTED
+    for f in (pa.pa_reshape_and_cache_fp4, pa.pa_gather_cache_fp4):
+        refused(bad, f, rows.cpu(), rows, kt, vt, slots, KS, VS)
+        refused(bad, f, rows, rows.half(), kt, vt, slots, KS, VS)                     # two row types
+        refused(bad, f, rows, rows[:, :, ::2], kt, vt, slots, KS, VS)                 # not contiguous
+        refused(bad, f, rows, rows, kt, vt, slots[:-1].contiguous(), KS, VS)          # a slot short
+        refused(bad, f, rows, rows, kt, vt, slots.int(), KS, VS)
+        refused(bad, f, rows, rows, kt, vt[:-1].contiguous(), slots, KS, VS)          # pools of two sizes
+        refused(bad, f, rows, rows, kt.float(), vt, slots, KS, VS)
+        refused(bad, f, rows[:, :1].contiguous(), rows[:, :1].contiguous(), kt, vt, slots, KS, VS)   # heads
+        refused(bad, f, rows[..., :64].contiguous(), rows[..., :64].contiguous(), kt[..., :1000].contiguous(),
+                vt[..., :1000].contiguous(), slots, KS, VS)
+        refused(bad, f, rows, rows, kt, vt, slots, 0.0, VS)
+        refused(unsupported, f, rows.to(torch.float64), rows.to(torch.float64), kt, vt, slots, KS, VS)
+    refused(bad, pa.pa_expand_blocks_fp4, ko, vo.half(), kt, vt, pairs, KS, VS)
+    refused(bad, pa.pa_expand_blocks_fp4, ko[:, :, :, :8].contiguous(), vo, kt, vt, pairs, KS, VS)
+    refused(unsupported, pa.pa_expand_blocks_fp4, ko.float(), vo.float(), kt, vt, pairs, KS, VS)
+    refused(bad, pa.pa_decode_fp4, out, q.bfloat16(), kt, vt, table, lens, 0.1, 32, KS, VS)
+    refused(bad, pa.pa_decode_fp4, out, q, kt, vt, table, lens, 0.1, 33, KS, VS)      # longer than the table
+    refused(bad, pa.pa_decode_fp4, out, q, kt, vt, table.long(), lens, 0.1, 32, KS, VS)
+    refused(bad, pa.pa_decode_fp4, out, q, kt, vt, table, lens, float("nan"), 32, KS, VS)
+    refused(bad, pa.pa_decode_fp4, out[:, :2].contiguous(), q, kt, vt, table, lens, 0.1, 32, KS, VS)
+    refused(unsupported, pa.pa_decode_fp4, out.float(), q.float(), kt, vt, table, lens, 0.1, 32, KS, VS)
+    no_error()
