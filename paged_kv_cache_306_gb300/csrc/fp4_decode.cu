@@ -45,10 +45,10 @@ constexpr float kSlack = 8.f;         // how far weights may exceed 1, in log2 u
 // NT: 8-column tiles of query heads (a unit has up to 8 NT heads).
 template <int D, int NT>
 struct Fp4Shape {
-  static constexpr int kWarps = NT == 1 ? 12 : 8;
+  static constexpr int kWarps = NT == 1 || D == 64 ? 12 : 8;
   static constexpr int kRows = 8 * NT;
   static constexpr int kStage = 2 * kChunk * (D / 2 + D / 16);
-  static constexpr int kStages = (NT == 1 ? 2 : 4) * (128 / D);
+  static constexpr int kStages = D == 64 ? 4 : NT == 1 ? 2 : 4;
   static constexpr int kPiece = kRows * D * 4;                  // an unnormalised partial output
   static constexpr int kFirst = kWarps * kStages * kStage;      // [warps]: the piece a warp starts with
   static constexpr int kMl = kFirst + kWarps * kPiece;          // [2 warps][rows]: (m, l)
@@ -64,7 +64,7 @@ struct Fp4Shape {
 };
 
 constexpr uint64_t kFp4WaitNs = 1000000000ull;  // 1 s, then PA_DEVERR_TIMEOUT
-constexpr int kMergeBatch = 4;                  // pieces of other CTAs loaded at once
+constexpr int kMergeBatch = 8;                  // pieces of other CTAs loaded at once
 constexpr int kBegins = 1 << 30;  // beside a unit's number: the piece holds its segment's first chunk
 
 __device__ __forceinline__ float ex2(float x) {  // |relative error| < 2^-22, 0 below 2^-126
@@ -469,6 +469,13 @@ __device__ __forceinline__ void unit_heads(const Fp4DecodeParams& p, int u, int&
   nh = min(16, kvh * p.group + p.group - h0);
 }
 
+// Warps of each CTA that share `total` chunks.
+template <int WARPS>
+__device__ __forceinline__ int active_warps(int total) {
+  const int grid = static_cast<int>(gridDim.x);
+  return total >= grid * WARPS ? WARPS : (total + grid - 1) / grid;
+}
+
 template <typename T, int D, int BS, int NT>
 __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_kernel(const Fp4DecodeParams p) {
   using Sh = Fp4Shape<D, NT>;
@@ -612,12 +619,14 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     if (tid == WARPS * 32 - 1) s_pre[S] = before;
     __syncthreads();
 
-    // An equal share of the launch's chunks (fewer than 2^31); with fewer chunks than warps, one each.
+    // An equal share of the launch's chunks (fewer than 2^31).  With fewer chunks than the grid has
+    // warps, every CTA puts an equal number of its warps to work, with one chunk each.
     const int total = s_pre[S] * U;
-    const int workers = min(total, static_cast<int>(gridDim.x) * WARPS);
-    const int me = blockIdx.x * WARPS + warp;
+    const int active = active_warps<WARPS>(total);
+    const int workers = min(total, static_cast<int>(gridDim.x) * active);
+    const int me = blockIdx.x * active + warp;
     start = len = 0;
-    if (me < workers) {  // me * total / workers, the odd chunks spread over the grid
+    if (warp < active && me < workers) {  // me * total / workers, the odd chunks spread over the grid
       const int share = total / workers, more = total - share * workers;  // (more < workers <= 16 * SMs)
       start = me * share + me * more / workers;
       len = (me + 1) * share + (me + 1) * more / workers - start;
@@ -838,12 +847,13 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
 
   // The segment's pieces: its first in CTA head (slot 2 head + 1), the others in slots 2 (head + i),
   // the last of them this CTA's own.
-  const int total = s_pre[S] * U, workers = min(total, static_cast<int>(gridDim.x) * WARPS);
+  const int total = s_pre[S] * U, active = active_warps<WARPS>(total);
+  const int workers = min(total, static_cast<int>(gridDim.x) * active);
   const int share = total / workers, more = total - share * workers;
   const int at = s_pre[tail_s] * U + tail_u * (s_pre[tail_s + 1] - s_pre[tail_s]);  // its first chunk
   int head = blockIdx.x;
   for (;;) {  // the last CTA before this one whose first chunk is not past it
-    const int w = max(head - 1 - lane, 0) * WARPS;
+    const int w = max(head - 1 - lane, 0) * active;
     const uint32_t from = __ballot_sync(0xffffffffu, w * share + w * more / workers <= at);
     if (from) {
       head -= __ffs(from);
@@ -948,14 +958,18 @@ cudaError_t launch_shape(int head_size, int block_size, const Fp4DecodeParams& p
 
 }  // namespace
 
-// Chunks a warp should have before another CTA is worth its part of the merging.
-constexpr int kFp4MinChunks = 2;
-
+// CTAs of a launch, from the most chunks it can have.  A CTA gets about four chunks, one for
+// each of its SM's schedulers -- whole segments where they are short, since a segment cut at
+// CTAs' ends costs a wait for the other CTA -- and where that cuts segments into more than 32
+// pieces, rather as many chunks as it has warps.
 int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len) {
-  const int group = num_heads / num_kv_heads, warps = group <= 8 ? Fp4Shape<128, 1>::kWarps : Fp4Shape<128, 2>::kWarps;
-  const long long chunks = (long long)num_seqs * fp4_decode_units(num_heads, num_kv_heads) *
-                           ((max_seq_len + kChunk - 1) / kChunk);
-  const long long want = (chunks + kFp4MinChunks * warps - 1) / (kFp4MinChunks * warps);
+  const long long each = (max_seq_len + kChunk - 1) / kChunk;
+  const long long segs = (long long)num_seqs * fp4_decode_units(num_heads, num_kv_heads), chunks = segs * each;
+  const int warps = num_heads / num_kv_heads <= 8 ? Fp4Shape<128, 1>::kWarps : Fp4Shape<128, 2>::kWarps;
+  const long long per_cta = each <= 8 ? (each + 3) / each * each : 4;
+  long long want = (chunks + per_cta - 1) / per_cta;
+  const long long few = (chunks + warps - 1) / warps;
+  if (want > 32 * segs) want = few > 32 * segs ? few : 32 * segs;
   return static_cast<int>(want < sms ? (want > 0 ? want : 1) : sms);
 }
 
