@@ -515,35 +515,35 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   int cur[NB], nxt[NB];                         // lane i: the tiles of position i of 32 (-1: none)
   bool bad = false;                             // some length is outside the contract
 
-  // Lane i looks up position i of the next 32: its blocks (`have` of them) and their kv head.
-  auto look_up = [&](int positions, int (&id)[NB], int& have, int& head) {
+  // Lane i finds position i of the next 32: where its blocks' numbers are (`have` of them), and their kv head.
+  auto find = [&](int positions, const int32_t*& row, int& have, int& head) {
     int ls = gs, lu = gu, lj = gj + lane;
-    for (int c = s_pre[ls + 1] - s_pre[ls]; lj >= c;) {
-      lj -= c;
-      if (++lu < U) continue;
-      lu = 0;
-      do {
-        if (++ls == S) break;
-        c = s_pre[ls + 1] - s_pre[ls];
-      } while (c == 0);
-      if (ls == S) break;
-    }
     have = head = 0;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) id[b] = 0;
+    row = p.block_tables;
     if (lane < positions) {
+      for (int c = s_pre[ls + 1] - s_pre[ls]; lj >= c;) {
+        lj -= c;
+        if (++lu < U) continue;
+        lu = 0;
+        do {
+          ++ls;
+          c = s_pre[ls + 1] - s_pre[ls];
+        } while (c == 0);
+      }
       int h, c;
       unit_heads(p, lu, head, h, c);
       have = min((s_len[ls] + BS - 1) / BS - lj * NB, NB);
-      const int32_t* row = p.block_tables + (long long)ls * p.max_blocks_per_seq + lj * NB;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (b < have) id[b] = ld_now(row + b);
+      row += (long long)ls * p.max_blocks_per_seq + lj * NB;
     }
-    // the next group starts right after lane 31 (a chunk index past its unit is brought in range there)
+    // the next group, if there is one, starts right after lane 31 (a chunk index past its unit is brought in
+    // range there)
     gs = __shfl_sync(0xffffffffu, ls, 31);
     gu = __shfl_sync(0xffffffffu, lu, 31);
     gj = __shfl_sync(0xffffffffu, lj, 31) + 1;
+  };
+  auto read_blocks = [&](const int32_t* row, int have, int (&id)[NB]) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) id[b] = b < have ? ld_now(row + b) : 0;
   };
   // Blocks to tiles (-1: none); block 0 for one outside the pool.  Whether there was one.
   auto to_tiles = [&](const int (&id)[NB], int have, int head, int (&tile)[NB]) {
@@ -631,7 +631,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       start = me * share + me * more / workers;
       len = (me + 1) * share + (me + 1) * more / workers - start;
     }
-    int id[NB] = {}, have = 0, head = 0;
+    int id[NB], have = 0, head = 0;
+    const int32_t* row = p.block_tables;
     if (len > 0) {
       // The sequence: the last one whose prefix is at most the start, found by the warp together in
       // 32-way steps (empty sequences have their successor's prefix).
@@ -645,17 +646,15 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       u = r / c;
       j = r - u * c;
       gs = s, gu = u, gj = j;
-      look_up(len, id, have, head);
+      find(len, row, have, head);
     }
+    read_blocks(row, have, id);
     int now_len[PER], now_id[NB] = {};
     if (!waited) {  // what has to read the same
       griddep_wait();
 #pragma unroll
       for (int k = 0; k < PER; ++k) now_len[k] = tid * PER + k < S ? ld_now(p.seq_lens + tid * PER + k) : 0;
-      if (len > 0) {
-        gs = s, gu = u, gj = j;
-        look_up(len, now_id, have, head);
-      }
+      read_blocks(row, have, now_id);
     }
     // the first chunks and the query rows are asked for in the meantime (every tile lies in the pool)
     bad_id = to_tiles(id, have, head, cur);
@@ -693,7 +692,9 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     int group = 0;
     auto look_up_next = [&](int positions) {
       int id[NB], have, head;
-      look_up(positions, id, have, head);
+      const int32_t* row;
+      find(positions, row, have, head);
+      read_blocks(row, have, id);
       if (to_tiles(id, have, head, nxt)) set_error(p.err, kErrBlockId);
     };
     if (len > 32) look_up_next(len - 32);
