@@ -487,7 +487,12 @@ PA_API pa_status pa_copy_blocks_fp4(void* k_cache, void* v_cache, const int64_t*
                                     int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
                                     void* stream);
 
-/* Workspace bytes of pa_decode_fp4 (0 for arguments it would reject, or when it needs none). */
+/*
+ * Workspace bytes of pa_decode_fp4: 0 for arguments it would reject, or when it needs
+ * none (few enough tokens for one CTA).  The workspace needs no initialisation.  A call
+ * uses it until its work on the GPU is done: calls that may overlap need one each, calls
+ * and graph replays in order on one stream can share it.
+ */
 PA_API size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                            int max_seq_len, int block_size);
 
@@ -497,8 +502,17 @@ PA_API size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_
  * fp32, the softmax weights are rounded once to fp16; out is rounded once to q_dtype.
  * Conditions on sizes, tables and lengths as in pa_decode (no caller partitions); a
  * sequence whose length lies outside [1, max_seq_len] is recorded as
- * PA_DEVERR_SEQ_LEN and its rows of out are zero.  Deterministic: equal arguments
- * give equal bits, whatever the physical placement of the blocks.
+ * PA_DEVERR_SEQ_LEN and its rows of out are zero.  num_blocks * num_kv_heads must stay
+ * below 2^31 (PA_ERR_UNSUPPORTED otherwise).  Deterministic: equal arguments give equal
+ * bits, whatever the physical placement of the blocks.
+ *
+ * One kernel per 1024 sequences.  It may start while the previous kernel in the stream
+ * finishes; what it reads of seq_lens and block_tables before that is read again after
+ * it, and only the later values count.  A sequence spread over several CTAs is merged by
+ * the one that holds its end, which waits for the others, about 1 s at most
+ * (PA_DEVERR_TIMEOUT; after one, a captured call must not be replayed on that workspace
+ * before its last num_SMs * 8 bytes have been cleared).  pa_set_test_wait_limit makes
+ * these waits run out too.
  */
 PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
                                const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,

