@@ -149,8 +149,8 @@ struct Fp4Math {
   uint32_t qb[KS][NT][2];
   float acc[KS][NT][4];
   float lacc[NT][4];  // the weights' sums of heads 8n + 2 t4 + {0, 1} (twice): a product with ones
-  // of those heads: the reference m of the exponents, kRaise - m hs, the score above which m moves, hs
-  float m_[NT][2], off_[NT][2], lim_[NT][2], hs_[NT][2];
+  // of those heads: the reference m of the exponents, the score above which m moves, hs
+  float m_[NT][2], lim_[NT][2], hs_[NT][2];
   int g, t4;
   int k_at, ks_at, v_at[2], vs_at;  // this lane's places in a sub-tile (fp4::code_at and its scales')
 
@@ -177,10 +177,7 @@ struct Fp4Math {
     for (int n = 0; n < NT; ++n) {
       lacc[n][0] = lacc[n][1] = lacc[n][2] = lacc[n][3] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m_[n][c] = lim_[n][c] = kNoScore;  // the first chunk sets them
-        off_[n][c] = INFINITY;
-      }
+      for (int c = 0; c < 2; ++c) m_[n][c] = lim_[n][c] = kNoScore;  // the first chunk sets them
     }
   }
 
@@ -241,7 +238,7 @@ struct Fp4Math {
             const float2 v = unpack2<T>(qb[k][n][i]);
             qb[k][n][i] = pack2<__half>(v.x * up, v.y * up);
           }
-        const float down = mag * __uint_as_float((127 - e) << 23);
+        const float down = fminf(mag * __uint_as_float((127 - e) << 23), 0x1p127f);  // (inf * 0 would be NaN)
         hs_[n][0] = __shfl_sync(0xffffffffu, down, 8 * t4);  // heads 2 t4 and 2 t4 + 1
         hs_[n][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
       }
@@ -358,7 +355,8 @@ struct Fp4Math {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          sc[mt][n][c] = ex2(fmaf(sc[mt][n][c], hs_[n][c & 1], off_[n][c & 1]));
+          // the difference first: exact where it counts, and never above kSlack whatever the scores' size
+          sc[mt][n][c] = ex2(fmaf(sc[mt][n][c] - m_[n][c & 1], hs_[n][c & 1], kRaise));
         }
     if (part) mask(sc, tok, rem, 0.f);
     // rounded to fp16 (11 bits, as the operands are fp16); their sums are of what was rounded
@@ -417,11 +415,9 @@ struct Fp4Math {
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float off = fmaf(-v, hs_[n][c], kRaise);
-        f[c] = ex2(off - off_[n][c]);
+        f[c] = ex2((m_[n][c] - v) * hs_[n][c]);  // (at first m is kNoScore, and there is nothing to bring)
         m_[n][c] = v;
-        off_[n][c] = off;
-        lim_[n][c] = v + __fdividef(kSlack, hs_[n][c]);  // (hs 0: infinity)
+        lim_[n][c] = __fadd_rd(v, __fdividef(kSlack, hs_[n][c]));  // (hs 0: infinity)
         lacc[n][c] *= f[c];
         lacc[n][c + 2] *= f[c];
       }
@@ -462,7 +458,7 @@ struct Fp4Math {
         for (int k = 0; k < KS; k += 2)
           o[((2 * n + c) * (KS / 2) + k / 2) * 32 + ((4 * g + t4) ^ (k / 2))] =
               make_float4(acc[k][n][c], acc[k][n][c + 2], acc[k + 1][n][c], acc[k + 1][n][c + 2]);
-        if (g == 0) ml[8 * n + 2 * t4 + c] = make_float2(-off_[n][c], lacc[n][c]);
+        if (g == 0) ml[8 * n + 2 * t4 + c] = make_float2(m_[n][c] * hs_[n][c], lacc[n][c]);
       }
   }
   // Dims 4 i .. 4 i + 3 of head r of a piece.

@@ -593,6 +593,28 @@ def test_decode_scales_of_any_sign(scale):
     c.check(out)
 
 
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** 10, -2.0 ** 24, 2.0 ** 40, 2.0 ** 63])
+def test_scores_of_any_size_leave_the_largest(q_dtype, scale):
+    """q of -1, 0 and 1 and scales sf of 1: every score is a sum of at most 128 codes, exact in fp32, and
+    two that differ do so by 1/2 at least, 2^9 and more after the softmax's scale.  So the answer is the mean of the
+    V rows whose score is the largest (the smallest for a negative scale), wherever their pieces are."""
+    c = Case([1, 65, 3000, 20000], 2, 2, 128, 16, q_dtype, scale)
+    (kc, kf), vp = c.pools
+    kf[...] = 0x38                                            # sf = 1
+    rng = rng_of("largest", scale)
+    c.q = store(rng.integers(-1, 2, size=c.q.shape).astype(np.float64), q_dtype)[0]
+    c.k = fp4.pack(kc, kf, "k")
+    c.scale = scale / KS
+    out = c.run()
+    no_error()
+    k64, v64 = fp4.f64_pools(c.k, c.v, 128, 16, KS, VS)
+    args = (c.table, np.array(c.lens, np.int32), c.scale, "f64")
+    ref, mass = (oracle.decode(c.q, k64, v, *args, q_dtype=q_dtype) for v in (v64, np.abs(np.nan_to_num(v64))))
+    bound = (np.array(c.lens)[:, None, None] / 8 + 64) * 2.0 ** -22 * mass     # sums in fp32
+    assert (np.abs(as_f64(out) - ref) - bound - half_ulp(np.abs(ref) + bound, q_dtype)).max() <= 0
+
+
 # --- as they are used together ------------------------------------------------------------------------
 
 def test_a_serving_run_over_an_fp4_cache():
