@@ -550,6 +550,8 @@ def pa_expand_blocks_fp4(k_out, v_out, k_cache, v_cache, src_dst, k_scale, v_sca
         _fp4_refuse(("k_out", k_out, None, 5), ("v_out", v_out, dt, 4), ("k_cache", k_cache, u8, 3),
                     ("v_cache", v_cache, u8, 3), ("src_dst", src_dst, i64, None))
     nbo, hkv, d, bs = v_out.shape
+    if src_dst.dim() != 2 or src_dst.shape[1] != 2:
+        raise PAError(PA_ERR_INVALID_ARG, "src_dst must be [pairs, 2]")
     if k_out.shape != (nbo, hkv, d // 8, bs, 8):
         raise PAError(PA_ERR_INVALID_ARG, f"k_out must be [{nbo}, {hkv}, {d // 8}, {bs}, 8]")
     nb, h, tile = k_cache.shape
@@ -557,7 +559,7 @@ def pa_expand_blocks_fp4(k_out, v_out, k_cache, v_cache, src_dst, k_scale, v_sca
         raise PAError(PA_ERR_INVALID_ARG, f"block size {bs} in the 16-bit pools, another in the FP4 pools")
     code = codes[dt] if dt in codes else dtype_code(dt)
     st = load().pa_expand_blocks_fp4(k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                     src_dst.data_ptr(), src_dst.numel() // 2, hkv, d, bs, nbo, nb, code, float(k_scale),
+                                     src_dst.data_ptr(), src_dst.shape[0], hkv, d, bs, nbo, nb, code, float(k_scale),
                                      float(v_scale),
                                      raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
@@ -569,10 +571,12 @@ def pa_copy_blocks_fp4(k_cache, v_cache, src_dst, head_size, stream=None):
     import torch
     for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         _need_here(n, t, torch.uint8, 3)
-    _need_here("src_dst", src_dst, torch.int64)
+    _need_here("src_dst", src_dst, torch.int64, 2)
+    if src_dst.shape[1] != 2:
+        raise PAError(PA_ERR_INVALID_ARG, "src_dst must be [pairs, 2]")
     nb, hkv, tile = k_cache.shape
     bs = _fp4_tile(nb, hkv, tile, v_cache.shape, hkv, head_size)
-    check(load().pa_copy_blocks_fp4(_ptr(k_cache), _ptr(v_cache), _ptr(src_dst), src_dst.numel() // 2, hkv, head_size,
+    check(load().pa_copy_blocks_fp4(_ptr(k_cache), _ptr(v_cache), _ptr(src_dst), src_dst.shape[0], hkv, head_size,
                                     bs, nb, _stream(stream)))
 
 

@@ -136,14 +136,14 @@ PyObject* expand(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* stream = nullptr;
     if (!row_code(ko->scalar_type(), &code) || vo->scalar_type() != ko->scalar_type() || ko->size(0) != blocks ||
         ko->size(1) != heads || ko->size(2) != dims / 8 || ko->size(3) != size || ko->size(4) != 8 ||
-        pairs->scalar_type() != at::kLong || heads > kIntMax || !pools(*k, *v, heads, dims, &bs) || bs != size ||
+        pairs->scalar_type() != at::kLong || pairs->dim() != 2 || pairs->size(1) != 2 || heads > kIntMax || !pools(*k, *v, heads, dims, &bs) || bs != size ||
         !as_float(a[5], &ks) || !as_float(a[6], &vs) || !as_stream(a[7], dev, &stream))
       return status(-1);
     pa_status st;
     void *kp = ko->data_ptr(), *vp = vo->data_ptr(), *kc = k->data_ptr(), *vc = v->data_ptr();
     const auto* sd = static_cast<const int64_t*>(pairs->data_ptr());
     Py_BEGIN_ALLOW_THREADS;
-    st = g_expand(kp, vp, kc, vc, sd, pairs->numel() / 2, static_cast<int>(heads), static_cast<int>(dims), bs, blocks,
+    st = g_expand(kp, vp, kc, vc, sd, pairs->size(0), static_cast<int>(heads), static_cast<int>(dims), bs, blocks,
                   k->size(0), code, ks, vs, stream);
     Py_END_ALLOW_THREADS;
     return status(st);

@@ -143,6 +143,32 @@ def test_write_reports_a_slot_beyond_the_pool_and_writes_the_others():
         assert np.array_equal(got.cpu().numpy(), fp4.pack(*logical, of))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_rows_that_start_on_16_bytes(dtype):
+    """Row arrays on a 16-byte boundary that is none of 32 bytes are read by narrower loads: same bytes."""
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("offset", dtype)
+    T, Hkv, D, bs = 50, 3, 128, 16
+    key, value = (store(rng.standard_normal((T, Hkv, D)), dtype)[0] for _ in range(2))
+    slots = cuda(rng.permutation(64)[:T].astype(np.int64))
+    got = []
+    for off in (0, 16):
+        rows = []
+        for x in (key, value):
+            t = cuda(x, dtype)
+            n = off // t.element_size()
+            flat = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+            flat[n:] = t.view(-1)
+            rows.append(flat[n:].view(T, Hkv, D))
+            assert rows[-1].data_ptr() % 32 == off
+        pools = [torch.zeros(4, Hkv, fp4.tile_bytes(D, bs), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        pa.pa_reshape_and_cache_fp4(*rows, *pools, slots, KS, VS)
+        got.append(pools)
+    no_error()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 # --- the reads back -----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -449,6 +475,83 @@ def test_a_captured_call_follows_its_inputs():
         c.check(out)
 
 
+def test_two_captured_steps_share_a_workspace_and_pools():
+    """A step (write, block copy, decode, reads back) captured twice, for batches of different shapes, on one
+    workspace and one pair of pools; replayed in turn on a side stream with new rows, slots and lengths."""
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("steps")
+    Hkv, D, bs, NB = 2, 128, 16, 600
+    kt = torch.full((NB, Hkv, fp4.tile_bytes(D, bs)), 0xFF, dtype=torch.uint8, device="cuda")
+    vt = torch.full_like(kt, 0xFF)
+    logical = [fp4.unpack(x.cpu().numpy(), D, bs, of) for x, of in ((kt, "k"), (vt, "v"))]
+    first = [store(rng.standard_normal((NB * bs, Hkv, D)), "f16") for _ in range(2)]
+    every = np.arange(NB * bs, dtype=np.int64)
+    pa.pa_reshape_and_cache_fp4(cuda(first[0][0], "f16"), cuda(first[1][0], "f16"), kt, vt, cuda(every), KS, VS)
+    for rows, lg, s in zip(first, logical, (KS, VS)):
+        fp4.write(rows[1], lg, every, s)
+    shapes = [(4, 8, 2100), (2, 2, 4000)]       # sequences, heads, longest
+    ws = torch.empty(max(pa.pa_decode_fp4_workspace_size(S, H, Hkv, D, L, bs) for S, H, L in shapes), dtype=torch.uint8,
+                     device="cuda")
+    f16, i64 = dict(dtype=torch.float16, device="cuda"), dict(dtype=torch.int64, device="cuda")
+    steps = []
+    for S, H, L in shapes:
+        t = dict(key=torch.zeros(S, Hkv, D, **f16), value=torch.zeros(S, Hkv, D, **f16), slots=torch.full((S,), -1, **i64),
+                 pairs=torch.zeros(1, 2, **i64), q=torch.zeros(S, H, D, **f16), out=torch.zeros(S, H, D, **f16),
+                 table=torch.zeros(S, L // bs + 1, dtype=torch.int32, device="cuda"),
+                 lens=torch.ones(S, dtype=torch.int32, device="cuda"), rk=torch.zeros(S, Hkv, D, **f16),
+                 rv=torch.zeros(S, Hkv, D, **f16), ko=torch.zeros(2, Hkv, D // 8, bs, 8, **f16),
+                 vo=torch.zeros(2, Hkv, D, bs, **f16), expand=torch.zeros(1, 2, **i64))
+
+        def step(t=t, L=L):
+            pa.pa_copy_blocks_fp4(kt, vt, t["pairs"], D)
+            pa.pa_reshape_and_cache_fp4(t["key"], t["value"], kt, vt, t["slots"], KS, VS)
+            pa.pa_decode_fp4(t["out"], t["q"], kt, vt, t["table"], t["lens"], 0.09, L, KS, VS, ws)
+            pa.pa_gather_cache_fp4(t["rk"], t["rv"], kt, vt, t["slots"], KS, VS)
+            pa.pa_expand_blocks_fp4(t["ko"], t["vo"], kt, vt, t["expand"], KS, VS)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        steps.append((t, g))
+    side = torch.cuda.Stream()
+    for rep in range(6):
+        i = rep % 2
+        (S, H, L), (t, g) = shapes[i], steps[i]
+        c = Case([int(x) for x in rng.integers(1, L, S - 1)] + [L - rep], H // Hkv, Hkv, D, bs, "f16", rep)
+        need = [-(-x // bs) for x in c.lens]
+        perm = rng.permutation(NB - 2)[:sum(need)].astype(np.int32) + 2
+        c.table = np.zeros((S, L // bs + 1), np.int32)
+        for s in range(S):
+            c.table[s, :need[s]] = perm[sum(need[:s]):sum(need[:s + 1])]
+        slots = np.array([c.table[s, (x - 1) // bs] * bs + (x - 1) % bs for s, x in enumerate(c.lens)], np.int64)
+        new = [store(rng.standard_normal((S, Hkv, D)), "f16") for _ in range(2)]
+        src = int(perm[0])
+        for lg, rows, sc in zip(logical, new, (KS, VS)):
+            for part in lg:
+                part[rep % 2] = part[src]
+            fp4.write(rows[1], lg, slots, sc)
+        for n, v in (("key", cuda(new[0][0], "f16")), ("value", cuda(new[1][0], "f16")), ("slots", cuda(slots)),
+                     ("pairs", cuda(np.array([[src, rep % 2]], np.int64))), ("q", cuda(c.q, "f16")),
+                     ("table", cuda(c.table)), ("lens", cuda(np.array(c.lens, np.int32))),
+                     ("expand", cuda(np.array([[src, 1]], np.int64)))):
+            t[n].copy_(v)
+        t["out"].fill_(math.nan)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            g.replay()
+        side.synchronize()
+        no_error()
+        c.scale, c.max_len = 0.09, L
+        c.k, c.v = fp4.pack(*logical[0], "k"), fp4.pack(*logical[1], "v")
+        assert np.array_equal(kt.cpu().numpy(), c.k) and np.array_equal(vt.cpu().numpy(), c.v)
+        c.check(t["out"])
+        for got, rows, sc in ((t["rk"], new[0], KS), (t["rv"], new[1], VS)):
+            assert np.array_equal(as_f64(got), rounded(fp4.values(*fp4.quantise(rows[1], sc), sc), "f16"))
+        assert np.array_equal(as_f64(t["vo"][1]).transpose(0, 2, 1),
+                              rounded(fp4.pool_values(c.v[src:src + 1], D, bs, "v", VS), "f16")[0])
+
+
 def test_lengths_and_tables_written_right_before_the_call():
     """The kernel may look at both while the previous kernel still runs: what that one writes must count."""
     cases = [Case(lens, 4, 2, 128, 16, "f16", i, extra=0) for i, lens in
@@ -582,6 +685,20 @@ def test_a_nan_in_the_cache_reaches_its_own_rows_only():
     bad[2, :3, 80:96] = True
     assert torch.equal(torch.isnan(out), bad)
     assert torch.equal(out[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("wrong", [math.nan, math.inf])
+def test_a_query_that_is_no_number_spoils_its_own_rows_only(q_dtype, wrong):
+    c = Case([300, 40, 9000], 3, 2, 128, 16, q_dtype)
+    t = c.upload()
+    t["q"][0, 1, 77] = t["q"][2, 5, 0] = wrong
+    out = c.run(t)
+    no_error()
+    assert not math.isnan(wrong) or (torch.isnan(out[0, 1]).all() and torch.isnan(out[2, 5]).all())
+    ref = cuda(c.reference()[0]).to(out.dtype)
+    out[0, 1], out[2, 5] = ref[0, 1], ref[2, 5]
+    c.check(out)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.09, 3.0e-5])
@@ -744,6 +861,8 @@ def test_both_marshalling_paths_check_and_compute_alike(path, monkeypatch):
         refused(bad, f, rows, rows, kt, vt, slots, 0.0, VS)
         refused(unsupported, f, rows.to(torch.float64), rows.to(torch.float64), kt, vt, slots, KS, VS)
     refused(bad, pa.pa_expand_blocks_fp4, ko, vo.half(), kt, vt, pairs, KS, VS)
+    refused(bad, pa.pa_expand_blocks_fp4, ko, vo, kt, vt, pairs.view(-1), KS, VS)                    # no pairs
+    refused(bad, pa.pa_copy_blocks_fp4, kt, vt, pairs.view(-1), D)
     refused(bad, pa.pa_expand_blocks_fp4, ko[:, :, :, :8].contiguous(), vo, kt, vt, pairs, KS, VS)
     refused(unsupported, pa.pa_expand_blocks_fp4, ko.float(), vo.float(), kt, vt, pairs, KS, VS)
     refused(bad, pa.pa_decode_fp4, out, q.bfloat16(), kt, vt, table, lens, 0.1, 32, KS, VS)
