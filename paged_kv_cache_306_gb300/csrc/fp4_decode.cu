@@ -37,8 +37,8 @@
 //
 // Measured on a GB300 (fp16, 128 dims, 16-token blocks unless said; floor: the bytes at the
 // measured copy rate): 64 sequences of 512-4096 tokens, 28/4 heads, 23.4 us (floor 12.6);
-// 16 x 2048 tokens, 32/32 heads, 32.6 us (22.3); 4 x 47K-131K tokens, 32/8 heads, bf16,
-// 71.1 us (60.5); one sequence of 100 tokens 3.1 us, what its launch, three dependent loads
+// 16 x 2048 tokens, 32/32 heads, 32.5 us (22.3); 4 x 32K-131K tokens, 32/8 heads, bf16,
+// 72.1 us (60.5); one sequence of 100 tokens 3.1 us, what its launch, three dependent loads
 // and one chunk take.  About 5 us of the larger calls are the schedule (1.2), the first
 // copies (1), and the merging of pieces with the waits for the slowest warp and CTA (3).
 #include <math.h>
