@@ -853,8 +853,9 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   }
   if (!publish && tail_s < 0) return;  // (the same for all threads of the CTA)
   __syncthreads();
+  // The barrier orders the CTA's pieces before this thread's release, which covers what it has observed so:
+  // no fence of its own (with one: 2 to 7% on calls of 6 to 10 us).
   if (publish && tid == (WARPS - 1) * 32) {  // (not the warp that waits below)
-    __threadfence();
     st_release(p.part_tag + blockIdx.x, p.tag);
   }
   if (tail_s < 0) return;
@@ -880,8 +881,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     const uint64_t t0 = global_timer_ns(), limit = p.test_wait_ns ? p.test_wait_ns : kFp4WaitNs;
     const uint64_t want = p.test_wait_ns ? ~p.tag : p.tag;  // (the test's wait: for what nobody publishes)
     for (int c = head + lane; c < static_cast<int>(blockIdx.x); c += 32)
-      while (ld_acquire(p.part_tag + c) != want)
-        if (global_timer_ns() - t0 > limit) {
+      for (unsigned tries = 1; ld_acquire(p.part_tag + c) != want; ++tries)
+        if (tries % 16 == 0 && global_timer_ns() - t0 > limit) {
           set_error(p.err, kErrTimeout);
           break;
         }
