@@ -8,7 +8,9 @@
 // How it maps to the GPU.
 //   * Work: a segment is (sequence, head unit), cut into chunks of 32 tokens.  All
 //     chunks of the launch are laid end to end; the grid is at most one CTA per SM and
-//     every warp of it takes one equal run of chunks, crossing segments.  12 warps (up to
+//     every warp of it takes one equal run of chunks, crossing segments; where segments are
+//     short, the CTAs' shares are rounded to whole segments (the rule and why: at kExtraRounds'
+//     use; 30 sequences of 300-500 tokens, 32/8 heads, 10.3 -> 7.8 us).  12 warps (up to
 //     168 registers each): 16 of 128 registers measured 3-7% slower, 10 and 13 12%.
 //   * Copies: each warp has its own ring of stages in shared memory, filled by asynchronous
 //     16-byte copies (cp.async) of its own lanes: a chunk is one or two blocks of K and of V,
@@ -38,7 +40,7 @@
 // Measured on a GB300 (fp16, 128 dims, 16-token blocks unless said; floor: the bytes at the
 // measured copy rate): 64 sequences of 512-4096 tokens, 28/4 heads, 23.4 us (floor 12.6);
 // 16 x 2048 tokens, 32/32 heads, 32.5 us (22.3); 4 x 32K-131K tokens, 32/8 heads, bf16,
-// 72.1 us (60.5); one sequence of 100 tokens 3.1 us, what its launch, three dependent loads
+// 71.7 us (60.5); one sequence of 100 tokens 3.1 us, what its launch, three dependent loads
 // and one chunk take.  About 5 us of the larger calls are the schedule (1.2), the first
 // copies (1), and the merging of pieces with the waits for the slowest warp and CTA (3).
 #include <math.h>
@@ -73,8 +75,8 @@ struct Fp4Shape {
   static constexpr int kFactor = kRun + (kWarps + 1) * kRows * 8; // [2 warps][rows]: a piece's weight in its run
   static constexpr int kSeg = kFactor + 2 * kWarps * kRows * 4; // [2 warps] int2: (sequence or -1, unit and kBegins)
   static constexpr int kLen = kSeg + 2 * kWarps * 8;            // [seqs]
-  static constexpr int kPre = kLen + kMaxSeqsPerLaunch * 4;     // [seqs + 1], then the scan's warp sums
-  static constexpr int kBytes = kPre + (kMaxSeqsPerLaunch + 1 + kWarps + 3) * 4;
+  static constexpr int kPre = kLen + kMaxSeqsPerLaunch * 4;     // [seqs + 1], then the scan's warp sums and maxima
+  static constexpr int kBytes = kPre + (kMaxSeqsPerLaunch + 1 + 2 * kWarps + 3) * 4;
   static_assert(kStages >= 2 && kPiece <= kStages * kStage, "a warp's last piece takes its ring's place");
   static_assert(kStage % 128 == 0 && kMl % 16 == 0, "alignment");
   static_assert(kWarps <= 31 && kBytes <= 227 * 1024, "a bit per warp; shared memory per CTA");
@@ -82,6 +84,7 @@ struct Fp4Shape {
 
 constexpr uint64_t kFp4WaitNs = 1000000000ull;  // 1 s, then PA_DEVERR_TIMEOUT
 constexpr int kMergeBatch = 8;                  // pieces of other CTAs loaded at once
+constexpr int kExtraRounds = 2;                 // chunks of a warp that are worth not cutting segments at CTAs' ends
 constexpr int kBegins = 1 << 30;  // beside a unit's number: the piece holds its segment's first chunk
 
 __device__ __forceinline__ float ex2(float x) {  // |relative error| < 2^-22, 0 below 2^-126
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   int2* s_seg = reinterpret_cast<int2*>(smem + Sh::kSeg);
   int* s_len = reinterpret_cast<int*>(smem + Sh::kLen);
   int* s_pre = reinterpret_cast<int*>(smem + Sh::kPre);
-  int* s_sum = s_pre + kMaxSeqsPerLaunch + 1;
+  int *s_sum = s_pre + kMaxSeqsPerLaunch + 1, *s_most = s_sum + WARPS;
 
   if (lane < 2) s_seg[2 * warp + lane] = make_int2(-1, 0);  // no piece
   griddep_launch_dependents();
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
 
   bool bad_id = false;
   for (bool waited = false;; waited = true) {
-    int count[PER], sum = 0;
+    int count[PER], sum = 0, most = 0;
     bad = false;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -613,16 +616,19 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       if (i < S) s_len[i] = L;
       count[k] = (L + kChunk - 1) / kChunk;
       sum += count[k];
+      most = max(most, count[k]);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += x;
     }
-    if (lane == 31) s_sum[warp] = incl;
+    if (lane == 31) s_sum[warp] = incl, s_most[warp] = most;
     bad = __syncthreads_or(bad);
     int before = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
+    most = __reduce_max_sync(0xffffffffu, lane < WARPS ? s_most[lane] : 0);
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int i = tid * PER + k;
@@ -632,30 +638,62 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     if (tid == WARPS * 32 - 1) s_pre[S] = before;
     __syncthreads();
 
-    // An equal share of the launch's chunks (fewer than 2^31).  With fewer chunks than the grid has
-    // warps, every CTA puts an equal number of its warps to work, with one chunk each.
-    const int total = s_pre[S] * U;
-    const int active = active_warps<WARPS>(total);
-    const int workers = min(total, static_cast<int>(gridDim.x) * active);
-    const int me = blockIdx.x * active + warp;
+    // The sequence of a chunk: the last one whose prefix is at most the chunk, found by the warp together
+    // in 32-way steps (empty sequences have their successor's prefix).
+    auto sequence_of = [&](int chunk) {
+      int s = 0;
+      for (int step = S > 32 ? (S + 31) / 32 : 1;; step = 1) {
+        const int i = s + lane * step;
+        s += (31 - __clz(__ballot_sync(0xffffffffu, i < S && s_pre[min(i, S)] * U <= chunk))) * step;
+        if (step == 1) return s;
+      }
+    };
+    // A share of the launch's chunks (fewer than 2^31).
+    const int total = s_pre[S] * U, grid = static_cast<int>(gridDim.x);
     start = len = 0;
-    if (warp < active && me < workers) {  // me * total / workers, the odd chunks spread over the grid
-      const int share = total / workers, more = total - share * workers;  // (more < workers <= 16 * SMs)
-      start = me * share + me * more / workers;
-      len = (me + 1) * share + (me + 1) * more / workers - start;
+    const int per_cta = total / grid, rest = total - per_cta * grid;
+    // Where segments are short, a CTA's chunks start where a segment does: no segment is cut at CTAs' ends, which
+    // saves the wait for another CTA (about 2 us) and costs longer runs in some CTAs: at most `most` chunks more,
+    // whole segments where segments are alike.  It is done where that makes the longest run of a warp at most two
+    // chunks longer, and one in the second case (a chunk takes a warp about 1 us).  Measured with and without:
+    // 64 sequences of 50-120 tokens, 32/8 heads, 6.4 and 8.8 us; 100 of 200-300 11.1 and 13.5; 210 of 497-774, 64/8
+    // heads, 35.0 and 36.7; one of 1000, 8/8 heads, three chunks a warp against one, would be 7.1 against 5.9.
+    const int share = per_cta + (rest > 0);
+    auto rounds = [](int chunks) { return (chunks + WARPS - 1) / WARPS; };
+    if (rounds(share + most) <= rounds(share) + kExtraRounds &&
+        rounds(share <= most ? most : (share + most - 1) / most * most) < rounds(share) + kExtraRounds) {
+      auto bound = [&](int cta) {
+        const int chunk = cta * per_cta + min(cta, rest);
+        if (chunk >= total) return total;
+        const int s = sequence_of(chunk);
+        const unsigned c = s_pre[s + 1] - s_pre[s], in = chunk - s_pre[s] * U;
+        return chunk - static_cast<int>(in % c);
+      };
+      const int from = bound(blockIdx.x), chunks = bound(blockIdx.x + 1) - from;
+      if (chunks <= WARPS) {
+        start = from + warp;
+        len = warp < chunks;
+      } else {
+        start = from + warp * chunks / WARPS;
+        len = from + (warp + 1) * chunks / WARPS - start;
+      }
+    } else {
+      // Equal shares.  With fewer chunks than the grid has warps, every CTA puts an equal number of its warps
+      // to work, with one chunk each.
+      const int active = active_warps<WARPS>(total);
+      const int workers = min(total, grid * active);
+      const int me = blockIdx.x * active + warp;
+      if (warp < active && me < workers) {  // me * total / workers, the odd chunks spread over the grid
+        const int each = total / workers, more = total - each * workers;  // (more < workers <= 16 * SMs)
+        start = me * each + me * more / workers;
+        len = (me + 1) * each + (me + 1) * more / workers - start;
+      }
     }
     int id[NB], have = 0, head = 0;
     const int32_t* row = p.block_tables;
     if (len > 0) {
-      // The sequence: the last one whose prefix is at most the start, found by the warp together in
-      // 32-way steps (empty sequences have their successor's prefix).
-      s = 0;
-      for (int step = S > 32 ? (S + 31) / 32 : 1;; step = 1) {
-        const int i = s + lane * step;
-        s += (31 - __clz(__ballot_sync(0xffffffffu, i < S && s_pre[min(i, S)] * U <= start))) * step;
-        if (step == 1) break;
-      }
-      const int c = s_pre[s + 1] - s_pre[s], r = start - s_pre[s] * U;
+      s = sequence_of(start);
+      const unsigned c = s_pre[s + 1] - s_pre[s], r = start - s_pre[s] * U;
       u = r / c;
       j = r - u * c;
       gs = s, gu = u, gj = j;

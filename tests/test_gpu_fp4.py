@@ -339,6 +339,18 @@ def test_decode_many_sequences(S, G, Hkv, D, bs):
     c.check(out)
 
 
+@pytest.mark.parametrize("S", [1, 7, 30, 200])
+@pytest.mark.parametrize("longest", [20, 60, 200, 500, 900])
+@pytest.mark.parametrize("G,Hkv,D,bs", [(4, 2, 128, 16), (10, 3, 64, 32)])
+def test_decode_batches_of_short_sequences(S, longest, G, Hkv, D, bs):
+    """Segments from much shorter to much longer than a CTA's share: whole ones a CTA, or cut at CTAs' ends."""
+    lens = [int(x) for x in rng_of("short", S, longest, G).integers(1, longest + 1, S)]
+    c = Case(lens, G, Hkv, D, bs, "f16", longest)
+    out = c.run()
+    no_error()
+    c.check(out)
+
+
 def test_decode_with_a_loose_length_bound():
     """max_seq_len far above the lengths: the tables are wide, the sequences short."""
     c = Case([5, 40, 100], 4, 2, 128, 16, "f16")
