@@ -607,6 +607,68 @@ def test_calls_on_two_streams_with_their_own_workspaces():
         c.check(o)
 
 
+def test_two_host_threads_with_streams_of_their_own():
+    """Writes, reads and decodes from two threads at once, each on its own stream, pools and workspaces."""
+    import threading
+    import paged_kv_cache_306_gb300 as pa
+    cases = [Case([1200, 33, 700], 4, 2, 128, 16, "f16", "a"), Case([60, 2500], 4, 2, 64, 32, "bf16", "b")]
+    ts = [c.upload() for c in cases]
+    rows, failed = [], []
+    for c, t in zip(cases, ts):     # every row read back and written again
+        slots = cuda(np.arange(len(c.k) * c.bs, dtype=np.int64))
+        rows.append((slots, *(torch.empty(len(slots), c.Hkv, c.D, device="cuda") for _ in range(2))))
+    outs = [torch.full_like(t["q"], math.nan) for t in ts]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                slots, k, v = rows[i]
+                for _ in range(25):
+                    pa.pa_gather_cache_fp4(k, v, ts[i]["k"], ts[i]["v"], slots, KS, VS)
+                    pa.pa_reshape_and_cache_fp4(k, v, ts[i]["k"], ts[i]["v"], slots, KS, VS)
+                    cases[i].run(ts[i], out=outs[i])
+            stream.synchronize()
+        except Exception as e:      # reported by the main thread
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    no_error()
+    for c, o, t in zip(cases, outs, ts):
+        c.k, c.v = t["k"].cpu().numpy(), t["v"].cpu().numpy()
+        c.check(o)
+
+
+def test_many_kv_heads():
+    import paged_kv_cache_306_gb300 as pa
+    rng = rng_of("heads")
+    T, Hkv, D, bs, NB = 20, 1001, 64, 16, 3
+    (key, k64), (value, v64) = (store(rng.standard_normal((T, Hkv, D)), "bf16") for _ in range(2))
+    kt = torch.zeros(NB, Hkv, fp4.tile_bytes(D, bs), dtype=torch.uint8, device="cuda")
+    vt = torch.zeros_like(kt)
+    slots = np.concatenate([np.arange(32, 48), np.arange(4)]).astype(np.int64)    # blocks 2 and 0
+    pa.pa_reshape_and_cache_fp4(cuda(key, "bf16"), cuda(value, "bf16"), kt, vt, cuda(slots), KS, VS)
+    rk, rv = torch.empty(2, T, Hkv, D, device="cuda")
+    pa.pa_gather_cache_fp4(rk, rv, kt, vt, cuda(slots), KS, VS)
+    want = [rounded(fp4.values(*fp4.quantise(x, s), s), "f32") for x, s in ((k64, KS), (v64, VS))]
+    assert np.array_equal(as_f64(rk), want[0]) and np.array_equal(as_f64(rv), want[1])
+    ko = torch.zeros(2, Hkv, D // 8, bs, 8, dtype=torch.float16, device="cuda")
+    vo = torch.zeros(2, Hkv, D, bs, dtype=torch.float16, device="cuda")
+    pa.pa_expand_blocks_fp4(ko, vo, kt, vt, cuda(np.array([[2, 1]], np.int64)), KS, VS)
+    assert np.array_equal(as_f64(vo[1]).transpose(2, 0, 1), rounded(want[1][:16], "f16"))
+    c = Case([T], 1, Hkv, D, bs, "bf16", "heads", extra=1)
+    c.table = np.array([[2, 0]], np.int32)
+    c.k, c.v = kt.cpu().numpy(), vt.cpu().numpy()
+    out = c.run()
+    no_error()
+    c.check(out)
+
+
 def test_pools_past_32_bit_offsets():
     """Blocks at the end of pools of more than 4 GiB each: the write, both reads and decode."""
     import paged_kv_cache_306_gb300 as pa
