@@ -1218,6 +1218,14 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   }
   const int len = static_cast<int>(end - start);
   if (len <= 0) {
+    // This warp's slot may lie between the first and the last piece of the segment at `start`: it is marked as
+    // holding none, since a call replayed from a graph carries the same epoch, and an earlier replay over other
+    // lengths may have left a piece there.  (Slots grow with the warp and the segment: no piece uses this one.)
+    if (lane == 0 && start < T_all) {
+      int s, u, j;
+      locate(start, s_pre, S, U, s, u, j);
+      p.part_tag[(long long)w + seg_id(s, u, shared && j < shared_len(s) ? 0 : 1)] = make_int2(-1, 0);
+    }
     if (p.fused) write_tokens();
     return;
   }
@@ -1431,7 +1439,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
 // (M, L, O) with the same rule; the row is O / L.  Slots whose tag is not (their
 // segment, this launch's epoch) weigh nothing and are never read into a sum:
 // when the grid has more warps than blocks of work, a warp with an empty range
-// leaves its slot inside a segment's range unwritten.  A piece whose rows saw no
+// has a slot inside a segment's range, and writes a tag of no segment there.  A piece whose rows saw no
 // block (a member that holds fewer shared blocks than the piece covers) has
 // m = -inf and weighs nothing too.
 constexpr int kMergeRows = 8;
