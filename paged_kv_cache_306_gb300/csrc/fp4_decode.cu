@@ -3,7 +3,9 @@
 // What is computed: for a sequence s and the query heads that share a kv head,
 //     out = s_v sum_t p_t (code sf)_t / sum_t p_t,  p_t = 2^(hs q . (code sf)_t - m),
 // with hs = scale s_k log2 e and a running maximum m (one pass over the tokens).
-// Pieces of a sequence done apart are merged with M = max m_i, weights 2^(m_i - M).
+// With m = hs m': pieces of a sequence done apart are merged with M' = max m'_i and factors
+// 2^(hs (m'_i - M')): like a weight's exponent, the difference first, so that scores of any size
+// leave the largest however the work is cut (hs m' itself may be past fp32's largest number).
 //
 // How it maps to the GPU.
 //   * Work: a segment is (sequence, head unit), cut into chunks of 32 tokens.  All
@@ -70,10 +72,11 @@ struct Fp4Shape {
   static constexpr int kStages = D == 64 ? 4 : NT == 1 ? 2 : 4;
   static constexpr int kPiece = kRows * D * 4;                  // an unnormalised partial output
   static constexpr int kFirst = kWarps * kStages * kStage;      // [warps]: the piece a warp starts with
-  static constexpr int kMl = kFirst + kWarps * kPiece;          // [2 warps][rows]: (m, l)
-  static constexpr int kRun = kMl + 2 * kWarps * kRows * 8;     // [warps + 1][rows]: a run's (M, W), by its first warp
-  static constexpr int kFactor = kRun + (kWarps + 1) * kRows * 8; // [2 warps][rows]: a piece's weight in its run
-  static constexpr int kSeg = kFactor + 2 * kWarps * kRows * 4; // [2 warps] int2: (sequence or -1, unit and kBegins)
+  static constexpr int kMl = kFirst + kWarps * kPiece;          // [2 warps][rows]: (m', l)
+  static constexpr int kRun = kMl + 2 * kWarps * kRows * 8;     // [warps + 1][rows]: a run's (M', W), by its first warp
+  static constexpr int kFactor = kRun + (kWarps + 1) * kRows * 8; // [2 warps][rows]: a piece's hs, then its weight in its run
+  static constexpr int kHs = kFactor + 2 * kWarps * kRows * 4;  // [rows]: hs of the run that warp 0 does not begin
+  static constexpr int kSeg = kHs + kRows * 4;                  // [2 warps] int2: (sequence or -1, unit and kBegins)
   static constexpr int kLen = kSeg + 2 * kWarps * 8;            // [seqs]
   static constexpr int kPre = kLen + kMaxSeqsPerLaunch * 4;     // [seqs + 1], then the scan's warp sums and maxima
   static constexpr int kBytes = kPre + (kMaxSeqsPerLaunch + 1 + 2 * kWarps + 3) * 4;
@@ -452,7 +455,7 @@ struct Fp4Math {
 
   // A piece in shared memory: vectors of 4 dims, [head parts (n, c)][vectors of D/8 dims][lane ^ vector],
   // so that neither the lanes that write nor those that read a head's row meet in a bank.
-  __device__ __forceinline__ void store_piece(float4* o, float2* ml) const {
+  __device__ __forceinline__ void store_piece(float4* o, float2* ml, float* hs) const {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -461,7 +464,10 @@ struct Fp4Math {
         for (int k = 0; k < KS; k += 2)
           o[((2 * n + c) * (KS / 2) + k / 2) * 32 + ((4 * g + t4) ^ (k / 2))] =
               make_float4(acc[k][n][c], acc[k][n][c + 2], acc[k + 1][n][c], acc[k + 1][n][c + 2]);
-        if (g == 0) ml[8 * n + 2 * t4 + c] = make_float2(m_[n][c] * hs_[n][c], lacc[n][c]);
+        if (g == 0) {
+          ml[8 * n + 2 * t4 + c] = make_float2(m_[n][c], lacc[n][c]);
+          hs[8 * n + 2 * t4 + c] = hs_[n][c];
+        }
       }
   }
   // Dims 4 i .. 4 i + 3 of head r of a piece.
@@ -508,6 +514,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   float2* s_ml = reinterpret_cast<float2*>(smem + Sh::kMl);
   float2* s_run = reinterpret_cast<float2*>(smem + Sh::kRun);
   float* s_factor = reinterpret_cast<float*>(smem + Sh::kFactor);
+  float* s_hs = reinterpret_cast<float*>(smem + Sh::kHs);
   int2* s_seg = reinterpret_cast<int2*>(smem + Sh::kSeg);
   int* s_len = reinterpret_cast<int*>(smem + Sh::kLen);
   int* s_pre = reinterpret_cast<int*>(smem + Sh::kPre);
@@ -785,7 +792,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
         // a piece that ends its segment but did not begin it can only be this warp's first (entry
         // 2 warp), the other kind only its last (entry 2 warp + 1)
         const int e = 2 * warp + (ends ? 0 : 1);
-        math.store_piece(piece(e), s_ml + e * Sh::kRows);
+        math.store_piece(piece(e), s_ml + e * Sh::kRows, s_factor + e * Sh::kRows);
         if (lane == 0) s_seg[e] = make_int2(s, u | (j0 == 0 ? kBegins : 0));
       }
       if (last) break;
@@ -816,7 +823,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     ends = stops != 0;
     return ends ? __ffs(stops) - 1 : 31 - __clz(finals);
   };
-  // Every (piece, head)'s factor in its run, and the run's (M, W) beside its first piece.
+  // Every (piece, head)'s factor in its run, and the run's (M', W) beside its first piece.  (hs is the same in
+  // every piece of a head's segment.)
   for (int i = tid; i < 2 * WARPS * Sh::kRows; i += WARPS * 32) {
     const int e = i / Sh::kRows, r = i % Sh::kRows, w = e >> 1;
     if (!(((e & 1 ? finals : firsts) >> w) & 1u)) continue;
@@ -825,15 +833,17 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
     bool ends = true;
     const int w1 = e & 1 ? run_end(w, ends) : w;
     auto ml = [&](int x) { return s_ml[(2 * x + (ends && x == w1 ? 0 : 1)) * Sh::kRows + r]; };
-    float M = -INFINITY, W = 0.f;
+    const float hs = s_factor[i];
+    float M = kNoScore, W = 0.f;
 #pragma unroll 4
     for (int x = w0; x <= w1; ++x) M = fmaxf(M, ml(x).x);
     if (w == w0) {
 #pragma unroll 4
-      for (int x = w0; x <= w1; ++x) W = fmaf(ex2(ml(x).x - M), ml(x).y, W);
+      for (int x = w0; x <= w1; ++x) W = fmaf(ex2((ml(x).x - M) * hs), ml(x).y, W);
       s_run[(e & 1 ? w : WARPS) * Sh::kRows + r] = make_float2(M, W);  // (a first piece alone: warp 0's)
+      if (!before) s_hs[r] = hs;
     }
-    s_factor[i] = ex2(s_ml[i].x - M);
+    s_factor[i] = ex2((s_ml[i].x - M) * hs);
   }
   __syncthreads();
   // A warp takes a head of a run, a lane D/32 dims.
@@ -929,10 +939,11 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   unit_heads(p, tail_u, kvh, h0, nh);
   auto slot = [&](int i) { return i == 0 ? 2 * head + 1 : 2 * (head + i); };
   for (int r = warp; r < nh; r += WARPS) {  // a warp per query head, 32 pieces at a time
-    float M = -INFINITY, W = 0.f, O[C] = {};
+    const float hs = s_hs[r];
+    float M = kNoScore, W = 0.f, O[C] = {};
     for (int i0 = 0; i0 < pieces; i0 += 32) {
       const int cnt = min(32, pieces - i0);
-      float2 ml = make_float2(-INFINITY, 0.f);
+      float2 ml = make_float2(kNoScore, 0.f);
       if (lane < cnt) ml = __ldcg(p.part_ml + slot(i0 + lane) * 16 + r);
       Vec o[kMergeBatch];
       auto load = [&](int i1) {
@@ -945,7 +956,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       float top = fmaxf(ml.x, M);
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float keep = ex2(M - top), f = ex2(ml.x - top);
+      const float keep = ex2((M - top) * hs), f = ex2((ml.x - top) * hs);
       float w = f * ml.y;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) w += __shfl_xor_sync(0xffffffffu, w, x);

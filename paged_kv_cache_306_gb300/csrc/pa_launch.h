@@ -231,7 +231,7 @@ struct Fp4DecodeParams {
   float out_scale;              // v_scale
   // the workspace (null when the grid is one CTA): two pieces per CTA, 16 rows each
   float* part_o;                // [2 grid, 16, D]: unnormalised partial outputs
-  float2* part_ml;              // [2 grid, 16]: (maximum in log2 units, sum)
+  float2* part_ml;              // [2 grid, 16]: (maximum, before the softmax's scale; sum)
   uint64_t* part_tag;           // [grid]: `tag` once the CTA's piece of a segment that goes on is there
   uint64_t tag;                 // this launch's own
   unsigned long long test_wait_ns;  // > 0 only in the timeout-path test (see pa_set_test_wait_limit)
