@@ -511,8 +511,9 @@ PA_API size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_
  * it, and only the later values count.  A sequence spread over several CTAs is merged by
  * the one that holds its end, which waits for the others, about 1 s at most
  * (PA_DEVERR_TIMEOUT; after one, a captured call must not be replayed on that workspace
- * before its last num_SMs * 8 bytes have been cleared).  pa_set_test_wait_limit makes
- * these waits run out too.
+ * before the workspace's first num_SMs * 8 bytes have been cleared: they hold the tags of
+ * all calls, and a piece that came late would leave its tag there).  pa_set_test_wait_limit
+ * makes these waits run out too.
  */
 PA_API pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const void* v_cache,
                                const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,

@@ -123,11 +123,13 @@ pa_status check_fp4_rows(const void* key, const void* value, const void* k_cache
 }
 
 // How one pa_decode_fp4 call is cut into launches, and its workspace: nothing when a
-// launch is one CTA, else room for two pieces per CTA.
+// launch is one CTA, else a tag per SM and room for two pieces per CTA.  The tags come
+// first, in as many bytes for every shape, so that neither a larger workspace nor one
+// that shapes share moves them or puts other data in their place.
 struct Fp4Plan {
   int chunk;  // sequences per launch
   int grid;
-  size_t off_ml, off_tag, bytes;
+  size_t off_o, off_ml, bytes;
 };
 
 pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len,
@@ -145,11 +147,11 @@ pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_
   if (chunk < 1) chunk = 1;
   pl->chunk = static_cast<int>(chunk);
   pl->grid = pa::fp4_decode_grid(sms, pl->chunk, num_heads, num_kv_heads, max_seq_len);
-  pl->off_ml = pl->off_tag = pl->bytes = 0;
+  pl->off_o = pl->off_ml = pl->bytes = 0;
   if (pl->grid > 1) {
-    pl->off_ml = (size_t)pl->grid * 2 * 16 * head_size * sizeof(float);
-    pl->off_tag = pl->off_ml + (size_t)pl->grid * 2 * 16 * 2 * sizeof(float);
-    pl->bytes = pl->off_tag + (size_t)pl->grid * sizeof(uint64_t);
+    pl->off_o = ((size_t)sms * sizeof(uint64_t) + 127) / 128 * 128;
+    pl->off_ml = pl->off_o + (size_t)pl->grid * 2 * 16 * head_size * sizeof(float);
+    pl->bytes = pl->off_ml + (size_t)pl->grid * 2 * 16 * 2 * sizeof(float);
   }
   return PA_OK;
 }
@@ -834,9 +836,9 @@ pa_status pa_decode_fp4(void* out, const void* q, const void* k_cache, const voi
   if (st != PA_OK) return st;
   if (pl.bytes) {
     char* ws = static_cast<char*>(workspace);
-    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_tag = reinterpret_cast<uint64_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
     p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
-    p.part_tag = reinterpret_cast<uint64_t*>(ws + pl.off_tag);
   }
   p.k_cache = k_cache;
   p.v_cache = v_cache;
