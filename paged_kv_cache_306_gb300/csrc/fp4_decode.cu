@@ -85,6 +85,9 @@ struct Fp4Shape {
   static_assert(kWarps <= 31 && kBytes <= 227 * 1024, "a bit per warp; shared memory per CTA");
 };
 
+// n tokens in pieces of `size`, for any int n >= 0.
+__host__ __device__ constexpr int pieces_of(int n, int size) { return static_cast<int>((static_cast<unsigned>(n) + size - 1) / size); }
+
 constexpr uint64_t kFp4WaitNs = 1000000000ull;  // 1 s, then PA_DEVERR_TIMEOUT
 constexpr int kMergeBatch = 8;                  // pieces of other CTAs loaded at once
 constexpr int kExtraRounds = 2;                 // chunks of a warp that are worth not cutting segments at CTAs' ends
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       }
       int h, c;
       unit_heads(p, lu, head, h, c);
-      have = min((s_len[ls] + BS - 1) / BS - lj * NB, NB);
+      have = min(pieces_of(s_len[ls], BS) - lj * NB, NB);
       row += (long long)ls * p.max_blocks_per_seq + lj * NB;
     }
     // the next group, if there is one, starts right after lane 31 (a chunk index past its unit is brought in
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
   int L = 0, n = 0, h0 = 0, nh = 0, kvh = 0;  // the current segment
   auto fetch_q = [&]() {
     L = s_len[s];
-    n = (L + kChunk - 1) / kChunk;
+    n = pieces_of(L, kChunk);
     unit_heads(p, u, kvh, h0, nh);
     math.load_q(static_cast<const T*>(p.q) + ((long long)s * p.num_heads + h0) * D, nh);
   };
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT>::kWarps * 32, 1) decode_fp4_ke
       const int L = out ? 0 : lens[k];
       bad |= out && i < S;
       if (i < S) s_len[i] = L;
-      count[k] = (L + kChunk - 1) / kChunk;
+      count[k] = pieces_of(L, kChunk);
       sum += count[k];
       most = max(most, count[k]);
     }
@@ -1027,7 +1030,7 @@ cudaError_t launch_shape(int head_size, int block_size, const Fp4DecodeParams& p
 // CTAs' ends costs a wait for the other CTA -- and where that cuts segments into more than 32
 // pieces, rather as many chunks as it has warps.
 int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len) {
-  const long long each = (max_seq_len + kChunk - 1) / kChunk;
+  const long long each = pieces_of(max_seq_len, kChunk);
   const long long segs = (long long)num_seqs * fp4_decode_units(num_heads, num_kv_heads), chunks = segs * each;
   const int warps = num_heads / num_kv_heads <= 8 ? Fp4Shape<128, 1>::kWarps : Fp4Shape<128, 2>::kWarps;
   const long long per_cta = each <= 8 ? (each + 3) / each * each : 4;
