@@ -146,7 +146,7 @@ pa_status make_fp4_plan(int num_seqs, int num_heads, int num_kv_heads, int head_
   if (chunk > 0x7fffffffLL / per_seq) chunk = 0x7fffffffLL / per_seq;
   if (chunk < 1) chunk = 1;
   pl->chunk = static_cast<int>(chunk);
-  pl->grid = pa::fp4_decode_grid(sms, pl->chunk, num_heads, num_kv_heads, max_seq_len);
+  pl->grid = pa::fp4_decode_grid(sms, pl->chunk, num_heads, num_kv_heads, head_size, max_seq_len);
   pl->off_o = pl->off_ml = pl->bytes = 0;
   if (pl->grid > 1) {
     pl->off_o = ((size_t)sms * sizeof(uint64_t) + 127) / 128 * 128;

@@ -1029,10 +1029,12 @@ cudaError_t launch_shape(int head_size, int block_size, const Fp4DecodeParams& p
 // each of its SM's schedulers -- whole segments where they are short, since a segment cut at
 // CTAs' ends costs a wait for the other CTA -- and where that cuts segments into more than 32
 // pieces, rather as many chunks as it has warps.
-int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len) {
+int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len) {
   const long long each = pieces_of(max_seq_len, kChunk);
   const long long segs = (long long)num_seqs * fp4_decode_units(num_heads, num_kv_heads), chunks = segs * each;
-  const int warps = num_heads / num_kv_heads <= 8 ? Fp4Shape<128, 1>::kWarps : Fp4Shape<128, 2>::kWarps;
+  const bool one = num_heads / num_kv_heads <= 8;
+  const int warps = head_size == 64 ? (one ? Fp4Shape<64, 1>::kWarps : Fp4Shape<64, 2>::kWarps)
+                                    : (one ? Fp4Shape<128, 1>::kWarps : Fp4Shape<128, 2>::kWarps);
   const long long per_cta = each <= 8 ? (each + 3) / each * each : 4;
   long long want = (chunks + per_cta - 1) / per_cta;
   const long long few = (chunks + warps - 1) / warps;

@@ -240,7 +240,7 @@ inline int fp4_decode_units(int num_heads, int num_kv_heads) {
   return num_kv_heads * ((num_heads / num_kv_heads + 15) / 16);
 }
 // CTAs of a launch of num_seqs sequences.
-int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int max_seq_len);
+int fp4_decode_grid(int sms, int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len);
 cudaError_t launch_decode_fp4(bool q_is_bf16, int head_size, int block_size, const Fp4DecodeParams& p, int grid,
                               cudaStream_t stream, int* launches);
 

@@ -55,3 +55,12 @@ def test_a_sequence_under_the_longest_bound(L, bound):
     assert np.isfinite(got).all()
     # one more rounding: fp16, half a step of 2^-11
     assert (np.abs(got - want) <= want * (2.0 ** -11 + (2.0 ** -4 if L > 1 << 20 else 2.0 ** -18))).all()
+
+
+def test_the_grid_counts_the_warps_of_the_kernel_that_runs():
+    """Head size 64 has 12 warps a CTA whatever the group: one long segment of 1200 chunks is 100 CTAs, for 8 query
+    heads a kv head and for 16 (head size 128: 8 warps with 9 and more heads)."""
+    import paged_kv_cache_306_gb300 as pa
+    size = pa.pa_decode_fp4_workspace_size
+    assert size(1, 16, 1, 64, 38400, 16) == size(1, 8, 1, 64, 38400, 16)
+    assert size(1, 16, 1, 128, 25600, 16) == size(1, 8, 1, 128, 38400, 16)
