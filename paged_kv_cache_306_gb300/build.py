@@ -11,6 +11,7 @@ their headers it is left out, and the binding takes its ctypes path.
 import argparse
 import concurrent.futures as cf
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -31,12 +32,20 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 
 def calls_path():
-    """Where the FP4 calls' extension for this Python and torch lies (built or not); None without torch."""
+    """Where the FP4 calls' extension for this Python, torch and source lies (built or not); None without torch.
+
+    The extension calls the library through the prototypes it was compiled with, so its name carries a digest of
+    them: one that was compiled from another header, by this environment or another, is never loaded."""
     try:
         import torch
     except ImportError:
         return None
-    return os.path.join(OUT_DIR, f"_fp4_calls-{torch.__version__}-{sys.version_info[0]}{sys.version_info[1]}.so")
+    h = hashlib.sha256()
+    for f in (os.path.join(CSRC, "fp4_calls.cpp"), os.path.join(INCLUDE, "pa.h")):
+        with open(f, "rb") as src:
+            h.update(src.read())
+    return os.path.join(OUT_DIR, f"_fp4_calls-{torch.__version__}-{sys.version_info[0]}{sys.version_info[1]}-"
+                                 f"{h.hexdigest()[:12]}.so")
 
 
 def _build_calls(out):
