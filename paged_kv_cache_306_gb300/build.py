@@ -5,8 +5,10 @@
 Each translation unit is compiled in parallel, then linked into
 paged_kv_cache_306_gb300/_build/libpa.so.  Rebuilds only when a source or header
 is newer than the library.  Beside it goes the CPython extension that marshals the
-FP4 calls (csrc/fp4_calls.cpp), built for the Python and torch at hand; without
-their headers it is left out, and the binding takes its ctypes path.
+FP4 calls (csrc/fp4_calls.cpp), built for the Python and torch at hand, by itself where
+only it is missing; without a compiler or their headers it is left out, and the binding
+takes its ctypes path.  A build that failed leaves its message beside it and is tried
+again when the library is rebuilt, or by the command above.
 """
 import argparse
 import concurrent.futures as cf
@@ -53,7 +55,10 @@ def _build_calls(out):
     import torch
     t = os.path.dirname(torch.__file__)
     py = sysconfig.get_paths()["include"]
-    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    try:
+        cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    except RuntimeError as e:
+        return str(e)
     gxx = shutil.which("g++")
     for need in (gxx, os.path.join(py, "Python.h"), os.path.join(t, "include", "ATen", "core", "Tensor.h")):
         if not need or not os.path.exists(need):
@@ -82,11 +87,38 @@ def _stale():
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    calls = calls_path()
-    if calls and not os.path.exists(calls) and not os.path.exists(calls + ".failed"):
-        return True
     deps = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _calls_missing():
+    calls = calls_path()
+    return bool(calls) and not os.path.exists(calls)
+
+
+def _make_calls():
+    """Build the FP4 calls' extension, or leave the reason beside its place."""
+    calls = calls_path()
+    mark = calls + ".failed"
+    os.makedirs(OUT_DIR, exist_ok=True)
+    failed = _build_calls(calls)
+    # what earlier sources left of this environment's extension
+    for end in ("", ".failed"):
+        for f in glob.glob(glob.escape(calls.rsplit("-", 1)[0]) + "*.so" + end):
+            if f != calls or failed:
+                os.remove(f)
+    if failed:
+        with open(mark, "w") as f:
+            f.write(failed)
+
+
+def _report_calls():
+    """Say so where the binding works without the extension, a few microseconds a call slower."""
+    mark = (calls_path() or "") + ".failed"
+    if os.path.exists(mark):
+        with open(mark) as f:
+            why = f.read().strip().splitlines() or ["no message"]
+        print(f"FP4 calls' extension not built ({why[-1][:200]}): the ctypes path is used")
 
 
 def _compile(nvcc, src, extra):
@@ -96,39 +128,38 @@ def _compile(nvcc, src, extra):
     return src, obj, r
 
 
-def build(force=False, verbose=False, extra_flags=()):
-    """Compile and link libpa.so; return its path."""
-    if not force and not _stale():
-        return LIB
+def build(force=False, verbose=False, extra_flags=(), retry=False):
+    """Compile and link libpa.so; return its path.  retry: the FP4 calls' extension even if it failed before."""
+    stale = force or _stale()
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        made = None
+        if calls_path() and (stale or _calls_missing() and (retry or not os.path.exists(calls_path() + ".failed"))):
+            made = ex.submit(_make_calls)
+        if stale:
+            _build_lib(verbose, extra_flags)
+        if made:
+            made.result()
+    _report_calls()
+    return LIB
+
+
+def _build_lib(verbose, extra_flags):
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
     objs = []
-    calls = calls_path()
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        made = ex.submit(_build_calls, calls) if calls else None
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         for src, obj, r in ex.map(lambda s: _compile(nvcc, s, list(extra_flags)), SOURCES):
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
             if verbose and r.stderr:
                 print(r.stderr)
             objs.append(obj)
-        failed = made.result() if made else None
-    if calls:
-        mark = calls + ".failed"
-        for f in (mark, calls) if failed else (mark,):
-            if os.path.exists(f):
-                os.remove(f)
-        if failed:  # the binding works without it, a few microseconds a call slower
-            with open(mark, "w") as f:
-                f.write(failed)
-            print(f"FP4 calls' extension not built ({failed.strip().splitlines()[-1][:200]}): the ctypes path is used")
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
@@ -138,4 +169,4 @@ if __name__ == "__main__":
     ap.add_argument("--ptxas-info", action="store_true", help="print registers/spills per kernel")
     a = ap.parse_args()
     extra = ["-Xptxas", "-v"] if a.ptxas_info else []
-    print(build(force=a.force or a.ptxas_info, verbose=a.verbose or a.ptxas_info, extra_flags=extra))
+    print(build(force=a.force or a.ptxas_info, verbose=a.verbose or a.ptxas_info, extra_flags=extra, retry=True))
