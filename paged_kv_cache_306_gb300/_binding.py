@@ -467,6 +467,13 @@ def _need_here(name, t, dtype=None, dims=None):
                                           f"cuda:{torch.cuda.current_device()}")
 
 
+def _fp4_bound(max_seq_len):
+    """max_seq_len, refused where C's int cannot hold it: ctypes would cut off its upper bits."""
+    if not -0x80000000 <= max_seq_len <= 0x7fffffff:
+        raise PAError(PA_ERR_INVALID_ARG, f"max_seq_len {max_seq_len} is past 32 bits")
+    return max_seq_len
+
+
 def _fp4_refuse(*needs):
     """Raise the error of the first of needs (name, tensor, dtype, dims) that does not hold."""
     for n in needs:
@@ -581,7 +588,8 @@ def pa_copy_blocks_fp4(k_cache, v_cache, src_dst, head_size, stream=None):
 
 
 def pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size):
-    return load().pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size)
+    return load().pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, _fp4_bound(max_seq_len),
+                                               block_size)
 
 
 def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len, k_scale, v_scale,
@@ -600,6 +608,7 @@ def pa_decode_fp4(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_s
             return workspace
         if st > 0 and st != PA_ERR_WORKSPACE:
             check(st)
+    _fp4_bound(max_seq_len)
     u8, i32, _, codes, current, raw_stream = _fp4_torch()
     dt, dev = q.dtype, q.get_device()
     if not (dev >= 0 and dev == current() and q.dim() == 3 and q.is_contiguous()

@@ -64,3 +64,22 @@ def test_the_grid_counts_the_warps_of_the_kernel_that_runs():
     size = pa.pa_decode_fp4_workspace_size
     assert size(1, 16, 1, 64, 38400, 16) == size(1, 8, 1, 64, 38400, 16)
     assert size(1, 16, 1, 128, 25600, 16) == size(1, 8, 1, 128, 38400, 16)
+
+
+@pytest.mark.parametrize("path", ["extension", "ctypes"])
+@pytest.mark.parametrize("bound", [(1 << 32) + 40, 1 << 31, -(1 << 31) - 1, (1 << 32) + 40000])
+def test_a_length_bound_past_32_bits_is_refused(path, bound, monkeypatch):
+    """2^32 + 40 is not 40."""
+    import paged_kv_cache_306_gb300 as pa
+    from paged_kv_cache_306_gb300 import _binding as B
+    if path == "ctypes":
+        monkeypatch.setattr(B, "_fp4_calls", lambda: None)
+    q = torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda")
+    pool = torch.zeros(4, 1, pa.pa_fp4_tile_bytes(64, 16), dtype=torch.uint8, device="cuda")
+    table, lens = torch.zeros(1, 3, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(pa.PAError) as e:
+        pa.pa_decode_fp4(torch.empty_like(q), q, pool, pool, table, lens, 0.1, bound, 0.5, 0.5)
+    assert e.value.status == B.PA_ERR_INVALID_ARG
+    with pytest.raises(pa.PAError):
+        pa.pa_decode_fp4_workspace_size(1, 2, 1, 64, bound, 16)
+    assert pa.pa_get_device_error() == 0
