@@ -165,7 +165,8 @@ PA_API int pa_decode_plan_partition(int num_seqs, int num_heads, int num_kv_head
  * PA_PARTITION_AUTO; it is resolved as pa_decode_plan_partition does).  Zero
  * when no split is made.  The workspace holds per-partition maxima, sums and
  * partial outputs in fp32; its contents need no initialisation and are
- * meaningless between calls.
+ * meaningless between calls.  A captured call may be replayed over other lengths
+ * and tables (within its max_seq_len) on the workspace it was captured with.
  */
 PA_API size_t pa_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                 int max_seq_len, int block_size, int partition_size,
@@ -440,7 +441,10 @@ PA_API pa_status pa_decode_noalloc(void* out, const void* q, const void* k_cache
  * For every call: head_size is 64 or 128 and block_size 16 or 32
  * (PA_ERR_UNSUPPORTED otherwise); k_scale and v_scale lie in [2^-64, 2^64]
  * (PA_ERR_INVALID_ARG otherwise); slots, block tables, alignment, errors and
- * streams as in the calls above.
+ * streams as in the calls above.  The calls that do a whole step (pa_decode_step) or
+ * read shared prefixes once (pa_decode_shared), and pa_prefill, take no FP4 pools: a
+ * step over them is a block copy, a write and a decode, forked sequences each read their
+ * prefix, and pa_prefill reads blocks that pa_expand_blocks_fp4 has converted.
  */
 
 /* Bytes of one (block, kv head) tile of an FP4 pool; 0 for unsupported sizes. */
@@ -499,7 +503,8 @@ PA_API size_t pa_decode_fp4_workspace_size(int num_seqs, int num_heads, int num_
 /*
  * pa_decode over FP4 pools: q and out have q_dtype (PA_F16 or PA_BF16), K and V read
  * back as code * sf * s, exactly.  Scores, softmax statistics and the weighted sum are
- * fp32, the softmax weights are rounded once to fp16; out is rounded once to q_dtype.
+ * fp32, the softmax weights are rounded once to fp16 (for bf16 queries too; one below
+ * 2^-32 of the largest vanishes); out is rounded once to q_dtype.
  * Conditions on sizes, tables and lengths as in pa_decode (no caller partitions); a
  * sequence whose length lies outside [1, max_seq_len] is recorded as
  * PA_DEVERR_SEQ_LEN and its rows of out are zero.  num_blocks * num_kv_heads must stay

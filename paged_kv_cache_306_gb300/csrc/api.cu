@@ -239,7 +239,8 @@ pa_status make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size
 }
 
 // A fresh tag for every launch, so a launch never mistakes a partial slot left by
-// an earlier launch for its own.  The sequence starts at a random point, so tags
+// an earlier launch for its own.  (A call replayed from a graph keeps its tag: there
+// the kernel leaves no slot of a segment unwritten, see its warps without work.)  The sequence starts at a random point, so tags
 // left in a reused buffer by another process are as unlikely to match.  Zero is
 // never used.
 unsigned next_epoch() {

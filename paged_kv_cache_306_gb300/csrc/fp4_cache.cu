@@ -1,10 +1,12 @@
 // fp4_cache.cu -- the FP4 pools' quantising write and the two reads back (see fp4.cuh).
 //
 // All three move 9/16 byte of a pool per element and 2 or 4 bytes of rows, once each, and are
-// bound by DRAM where they are large.  Measured on a GB300: write of 65536 tokens x 8 heads x
-// 128 dims 58.9 us from bf16 (5.8 TB/s; the quotients still share the time), 91 us from fp32
-// (6.7 TB/s); read back 56 us as bf16 (6.1 TB/s), 93 us as fp32 (6.6 TB/s); 8192 blocks of 16
-// tokens x 8 heads expanded in 110 us (6.3 TB/s).  A call for 64 tokens takes 1.8 us.
+// bound by DRAM where they are large.  Measured on a GB300, calls in a graph: write of 65536
+// tokens x 8 heads x 128 dims 58.8 us from bf16 (5.9 TB/s; the quotients still share the time),
+// 89.5 us from fp32 (6.9 TB/s); read back 55.5 us as bf16 (6.2 TB/s), 93.0 us as fp32 (6.6 TB/s);
+// 8192 blocks of 16 tokens x 8 heads expanded in 111.6 us (6.2 TB/s).  A write of 64 tokens takes
+// 2.0 us, a read 1.9 us; a write of 8192 tokens x 4 heads from fp16 4.8 us (floor 3.2): 1024 CTAs
+// on 912 places, so a second wave of 112.
 #include "fp4.cuh"
 #include "pa_launch.h"
 
@@ -116,8 +118,8 @@ __device__ __forceinline__ bool locate_row(const int64_t* slot_mapping, int rows
   return true;
 }
 
-// (16-bit rows: six CTAs of an SM in 42 registers a thread hide the loads, 62.9 -> 58.9 us for 65536
-// tokens x 8 heads x 128 dims; fp32 rows are 32 registers a thread and slow down below 50.)
+// (16-bit rows: six CTAs of an SM, in 40 registers a thread and a word spilled, hide the loads, 62.9 ->
+// 58.9 us for 65536 tokens x 8 heads x 128 dims; fp32 rows are 32 registers a thread and slow down below 50.)
 template <typename T, int D, int BS, bool kWide>
 __global__ void __launch_bounds__(kFp4Threads, sizeof(T) == 2 ? 6 : 1)
     reshape_and_cache_fp4_kernel(const T* key, const T* value, unsigned char* k_cache, unsigned char* v_cache,

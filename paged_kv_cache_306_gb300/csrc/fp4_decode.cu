@@ -60,7 +60,7 @@ constexpr int kChunk = 32;            // tokens
 constexpr float kNoScore = -1e30f;    // below every score (|score| < 2^35)
 // Weights are taken 2^7 times as large (it cancels in the normalised sum) and may grow by another
 // 2^8 before the reference moves: up to 2^15, inside fp16, while a weight of 2^-21 of the largest
-// score's still has all 11 bits.
+// score's still has all 11 bits, and one below 2^-32 of it vanishes.
 constexpr float kRaise = 7.f, kSlack = 8.f;
 
 // NT: 8-column tiles of query heads (a unit has up to 8 NT heads).
@@ -210,7 +210,8 @@ struct Fp4Math {
 
   // scale_log2 may be negative: its sign goes into q, so that the largest score is the
   // largest exponent.  bf16 heads become fp16 with a power of two taken from the head's
-  // largest |q| (every element keeps its 8 bits), put back by hs_.
+  // largest |q|, put back by hs_.  An element down to 2^-30 of the largest keeps its 8 bits; a
+  // smaller one lands among fp16's subnormals and is off by at most 2^-25, 2^-38 of the largest.
   __device__ __forceinline__ void scale_q(float scale_log2) {
     const float mag = fabsf(scale_log2);
     if (scale_log2 < 0.f) {
@@ -480,7 +481,10 @@ struct Fp4Math {
   }
 };
 
-// Head unit u: its kv head, first query head and number of them.
+// Head unit u: its kv head, first query head and number of them.  Past 16 heads a kv head's heads are
+// units of 16 and a rest, each of which reads and widens all of K and V for itself, with 16 columns: a rest of
+// one head costs nearly what 16 do (16 sequences of 2048 tokens, 4 kv heads of 128 dims: 8 heads each 11.0 us, 9 to
+// 16 12.8, 17 17.7, 32 18.4, 33 22.3; of 64 dims 9.5, 10.5 to 11.1, 13.9, 14.3, 16.6).
 __device__ __forceinline__ void unit_heads(const Fp4DecodeParams& p, int u, int& kvh, int& h0, int& nh) {
   if (p.group <= 16) {
     kvh = u;

@@ -66,7 +66,7 @@ struct DecodeParams {
   int max_seq_len;
   int part_blocks;              // blocks per caller partition; a huge value when none
   int num_slots;                // partial-result slots in the workspace
-  unsigned epoch;               // distinguishes this launch's partial slots from stale ones
+  unsigned epoch;               // distinguishes this launch's partial slots from those of other launches
   float scale_log2;             // scale * k_scale * log2(e)
   float out_scale;              // v_scale: a quantised cache's V reads back as code * v_scale
   // The fused step (pa_decode_step): the new token of each sequence s (rows s of
