@@ -12,6 +12,7 @@ again when the library is rebuilt, or by the command above.
 """
 import argparse
 import concurrent.futures as cf
+import contextlib
 import glob
 import hashlib
 import os
@@ -106,7 +107,8 @@ def _make_calls():
     for end in ("", ".failed"):
         for f in glob.glob(glob.escape(calls.rsplit("-", 1)[0]) + "*.so" + end):
             if f != calls or failed:
-                os.remove(f)
+                with contextlib.suppress(FileNotFoundError):  # (another process builds too)
+                    os.remove(f)
     if failed:
         with open(mark, "w") as f:
             f.write(failed)
@@ -114,9 +116,9 @@ def _make_calls():
 
 def _report_calls():
     """Say so where the binding works without the extension, a few microseconds a call slower."""
-    mark = (calls_path() or "") + ".failed"
-    if os.path.exists(mark):
-        with open(mark) as f:
+    calls = calls_path()
+    if calls and os.path.exists(calls + ".failed"):
+        with open(calls + ".failed") as f:
             why = f.read().strip().splitlines() or ["no message"]
         print(f"FP4 calls' extension not built ({why[-1][:200]}): the ctypes path is used")
 

@@ -91,3 +91,11 @@ def test_what_older_sources_left_goes(built, tree):
     os.utime(tree / "include" / "pa.h", (0, 0))
     pa_build.build()
     assert os.path.exists(pa_build.calls_path()) and not os.path.exists(old)
+
+
+def test_without_torch_there_is_no_extension_to_report(built, tree, monkeypatch, capsys):
+    monkeypatch.setattr(pa_build, "calls_path", lambda: None)
+    monkeypatch.chdir(tree)
+    (tree / ".failed").write_text("another program's file")
+    pa_build.build()
+    assert built == [] and not capsys.readouterr().out
