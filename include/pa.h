@@ -87,6 +87,12 @@ typedef enum {
 
 typedef enum { PA_F32 = 0, PA_F16 = 1, PA_BF16 = 2, PA_FP8_E4M3 = 3 } pa_dtype;
 
+/* Which dims of a row turn together (pa_rope): i and i + rotary_dim / 2, or 2 i and 2 i + 1. */
+typedef enum { PA_ROPE_HALVES = 0, PA_ROPE_PAIRS = 1 } pa_rope_layout;
+
+/* How pa_rope_frequencies stretches the frequencies for contexts longer than a model's own. */
+typedef enum { PA_ROPE_PLAIN = 0, PA_ROPE_LINEAR = 1, PA_ROPE_BANDS = 2, PA_ROPE_YARN = 3 } pa_rope_scaling;
+
 /* partition_size values for pa_decode.  The kernels cut sequences wherever their
  * load-balanced schedule needs to (every warp streams an equal share of all blocks)
  * and merge the pieces, so no caller partition is ever needed for speed: AUTO means
@@ -381,6 +387,113 @@ PA_API pa_status pa_prefill(void* out, const void* q, const void* k_cache, const
                             const int32_t* query_start_loc, int num_seqs, int num_query_tokens, int max_seq_len,
                             int num_heads, int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
                             float scale, pa_dtype dtype, void* stream);
+
+/*
+ * Decode whose scores are capped, biased or masked (the pages' attention is plain softmax; models
+ * built on it change the scores in these three ways).  pa_decode_scaled, but
+ * for the query at position p = seq_lens[s] - 1 of sequence s and its head h
+ *     out[s, h, :] = sum_t softmax_t(z_t) V_s[t, :]  over max(0, p - window + 1) <= t <= p,
+ *     x_t = scale * <q[s, h, :], K_s[t, :]>,
+ *     z_t = (softcap > 0 ? softcap * tanh(x_t / softcap) : x_t) - alibi_slopes[h] * (p - t)
+ *
+ * softcap       0 (none), or in [2^-64, 2^64]
+ * alibi_slopes  fp32 [num_heads], finite, 4-byte aligned; NULL: no bias.  The bias is
+ *               computed in fp32.
+ * window        positions the query sees, its own among them; 0: all
+ *
+ * Nothing before the window is read: block-table entries of blocks that end before it
+ * may hold anything (their blocks may have been freed), as may the slots before it in its
+ * first block.  Everything else as in pa_decode_scaled (q_dtype, cache_dtype, scales), without caller
+ * partitions; the workspace is pa_decode_masked_workspace_size bytes.  fp32 caches and 16-bit caches
+ * with one query head per kv head take the tanh in full fp32 accuracy, the others to
+ * 2^-21 of softcap.  With softcap 0, alibi_slopes NULL and window 0 the result is
+ * pa_decode_scaled's up to fp32 rounding.
+ */
+PA_API size_t pa_decode_masked_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                              int max_seq_len, int block_size, int window, pa_dtype cache_dtype);
+PA_API pa_status pa_decode_masked(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                  int num_seqs, int max_seq_len, int num_heads, int num_kv_heads, int head_size,
+                                  int block_size, int64_t num_blocks, float scale, float softcap,
+                                  const float* alibi_slopes, int window, void* workspace, size_t workspace_bytes,
+                                  pa_dtype q_dtype, pa_dtype cache_dtype, float k_scale, float v_scale, void* stream);
+
+/*
+ * Chunked prefill with the same changes of the scores, and a prefix that every row sees:
+ * pa_prefill, but the row at position p of sequence s attends, with z_t as in
+ * pa_decode_masked and |p - t| for p - t, to
+ *     max(0, p - window + 1) <= t <= max(p, min(prefix_lens[s], seq_lens[s]) - 1)
+ *
+ * prefix_lens  int32 [num_seqs], 4-byte aligned: the sequence's first prefix_lens[s] positions are
+ *              seen by rows before them too (their K/V must be in the cache: the chunk, or an
+ *              earlier one, holds them); below 1 none; NULL: none anywhere
+ * scale        positive (PA_ERR_INVALID_ARG otherwise)
+ * softcap, alibi_slopes, window as in pa_decode_masked, the tanh to 2^-21 of softcap.
+ *
+ * Block-table entries of blocks that end before the window of the sequence's first row may hold
+ * anything.  As in pa_prefill, an infinity or NaN in the V of a position that some row of a
+ * sequence's chunk sees may reach rows that do not see it.
+ */
+PA_API pa_status pa_prefill_masked(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                                   const int32_t* query_start_loc, const int32_t* prefix_lens, int num_seqs,
+                                   int num_query_tokens, int max_seq_len, int num_heads, int num_kv_heads,
+                                   int head_size, int block_size, int64_t num_blocks, float scale, float softcap,
+                                   const float* alibi_slopes, int window, pa_dtype dtype, void* stream);
+
+/*
+ * Rotary positions, the step between a layer's projections and the calls above: the token at
+ * position p turns pair i of the first rotary_dim dims of each of its q and key heads,
+ *     x' = amplitude * (x cos a - y sin a),  y' = amplitude * (x sin a + y cos a),  a = p * inv_freq[i],
+ * the pair (x, y) being dims (i, i + rotary_dim / 2) for PA_ROPE_HALVES and (2 i, 2 i + 1) for
+ * PA_ROPE_PAIRS; the other dims are copied.  Angles are exact to 2^-52 of themselves, whatever
+ * the position; cosines, sines and products are fp32, and each element is rounded once
+ * (an FP8 code from the fp32 value).
+ *
+ * q, key, value  rows [num_tokens] of num_heads, num_kv_heads and num_kv_heads heads of head_size
+ *                dims; *_stride elements lie between a token's row and the next, so that all
+ *                three may be views of one projection's rows.  A stride is a multiple of 16 bytes.
+ * q_out          [num_tokens, num_heads, head_size]; may be q itself (q_stride then being a
+ *                row's elements), else it overlaps no input.  Every token's q is turned, padding tokens' too.
+ * positions      int64 [num_tokens], any values
+ * inv_freq       double [rotary_dim / 2] in device memory, finite: radians per position
+ *                (pa_rope_frequencies computes them)
+ * head_size 64 or 128; rotary_dim a multiple of 16 (PA_ERR_UNSUPPORTED otherwise); rows fp32,
+ * fp16 or bf16.
+ *
+ * pa_rope writes the keys to key_out [num_tokens, num_kv_heads, head_size] (which may be key, as q_out
+ * q): for FP4 pools, or rows kept elsewhere.
+ * pa_rope_and_cache writes keys and values into the pools as pa_reshape_and_cache_scaled does (slots, padding,
+ * dtypes, scales and errors as there), in the same kernel.
+ */
+PA_API pa_status pa_rope(void* q_out, void* key_out, const void* q, const void* key, int64_t q_stride,
+                         int64_t key_stride, const int64_t* positions, const double* inv_freq, int64_t num_tokens,
+                         int num_heads, int num_kv_heads, int head_size, int rotary_dim, pa_rope_layout layout,
+                         float amplitude, pa_dtype dtype, void* stream);
+PA_API pa_status pa_rope_and_cache(void* q_out, const void* q, const void* key, const void* value, int64_t q_stride,
+                                   int64_t key_stride, int64_t value_stride, void* k_cache, void* v_cache,
+                                   const int64_t* positions, const int64_t* slot_mapping, const double* inv_freq,
+                                   int64_t num_tokens, int num_heads, int num_kv_heads, int head_size, int rotary_dim,
+                                   int block_size, int64_t num_blocks, pa_rope_layout layout, float amplitude,
+                                   pa_dtype key_dtype, pa_dtype cache_dtype, float k_scale, float v_scale,
+                                   void* stream);
+
+/*
+ * The frequencies of pa_rope, on the host (both outputs are host memory; no CUDA call):
+ * inv_freq[i], i < rotary_dim / 2, from f_i = base^(-2 i / rotary_dim), and the amplitude.
+ *   PA_ROPE_PLAIN   f_i
+ *   PA_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   PA_ROPE_BANDS   by the turns n_i = original_len f_i / 2 pi that the pair makes over the original
+ *                   length: f_i / factor where n_i <= low, f_i where n_i >= high, and between them the
+ *                   mix (1 - g) f_i / factor + g f_i with g = (n_i - low) / (high - low)
+ *   PA_ROPE_YARN    the mix linear in i ("YaRN: Efficient Context Window Extension of Large Language
+ *                   Models", §3.2), from the whole pair at or below the one that makes `high` turns to the
+ *                   one at or above that which makes `low`; amplitude 0.1 ln(factor) + 1
+ * The amplitude is 1 but for PA_ROPE_YARN.  Arguments that a scaling does not name are not looked at.
+ */
+PA_API pa_status pa_rope_frequencies(double* inv_freq, float* amplitude, int rotary_dim, double base,
+                                     pa_rope_scaling scaling, double factor, double original_len, double low,
+                                     double high);
 
 /*
  * Decode with no allocation anywhere: the same computation, arguments and

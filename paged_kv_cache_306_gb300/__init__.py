@@ -8,7 +8,9 @@ cache variant of both (``pa_reshape_and_cache_scaled``, ``pa_decode_scaled``), a
 held in 4 bits (``pa_reshape_and_cache_fp4``, ``pa_gather_cache_fp4``,
 ``pa_expand_blocks_fp4``, ``pa_decode_fp4``), the
 three fused into one generation step (``pa_decode_step``), chunked prefill
-(``pa_prefill``) and the host-side block manager that produces block tables, slots and copy-on-write
+(``pa_prefill``), decode and prefill with capped, biased or masked scores
+(``pa_decode_masked``, ``pa_prefill_masked``), rotary positions alone and with the write
+(``pa_rope``, ``pa_rope_and_cache``, ``pa_rope_frequencies``) and the host-side block manager that produces block tables, slots and copy-on-write
 pairs (``BlockManager``, ``include/pa_block_manager.h``).  This package is the
 thin Python binding; PyTorch supplies device memory and streams only.
 """
@@ -30,12 +32,16 @@ from ._binding import (  # noqa: F401
     PARTITION_AUTO,
     PARTITION_NONE,
     PAError,
+    ROPE_HALVES,
+    ROPE_PAIRS,
     load,
     pa_copy_blocks,
     pa_copy_blocks_fp4,
     pa_decode,
     pa_decode_fp4,
     pa_decode_fp4_workspace_size,
+    pa_decode_masked,
+    pa_decode_masked_workspace_size,
     pa_decode_scaled,
     pa_decode_shared,
     pa_decode_shared_workspace_size,
@@ -48,9 +54,13 @@ from ._binding import (  # noqa: F401
     pa_gather_cache_fp4,
     pa_get_device_error,
     pa_prefill,
+    pa_prefill_masked,
     pa_launch_count,
     pa_reshape_and_cache,
     pa_reshape_and_cache_fp4,
     pa_set_test_wait_limit,
     pa_reshape_and_cache_scaled,
+    pa_rope,
+    pa_rope_and_cache,
+    pa_rope_frequencies,
 )

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(PKG, "_build", "libpa.so")
 (PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_ALIGNMENT, PA_ERR_WORKSPACE, PA_ERR_CUDA,
  PA_ERR_OUT_OF_BLOCKS) = range(7)
 PA_F32, PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2, 3
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+ROPE_SCALINGS = {None: 0, "linear": 1, "bands": 2, "yarn": 3}
 PARTITION_NONE = 0
 PARTITION_AUTO = -1
 DEVICE_ERRORS = {0: "none", 1: "block id outside the pool", 2: "seq_len outside [1, max_seq_len]",
@@ -91,6 +93,21 @@ def load():
                                   P]
     for f in (lib.pa_reshape_and_cache_fp4, lib.pa_gather_cache_fp4, lib.pa_expand_blocks_fp4,
               lib.pa_copy_blocks_fp4, lib.pa_decode_fp4):
+        f.restype = i32
+    # capped, biased and masked attention; rotary positions
+    lib.pa_decode_masked_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32]
+    lib.pa_decode_masked_workspace_size.restype = sz
+    lib.pa_decode_masked.argtypes = [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i64, f32, f32, P, i32, P, sz,
+                                     i32, i32, f32, f32, P]
+    lib.pa_prefill_masked.argtypes = [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32, i32, i64, f32, f32, P,
+                                      i32, i32, P]
+    lib.pa_rope.argtypes = [P, P, P, P, i64, i64, P, P, i64, i32, i32, i32, i32, i32, f32, i32, P]
+    lib.pa_rope_and_cache.argtypes = [P, P, P, P, i64, i64, i64, P, P, P, P, P, i64, i32, i32, i32, i32, i32, i64, i32,
+                                      f32, i32, i32, f32, f32, P]
+    f64 = ctypes.c_double
+    lib.pa_rope_frequencies.argtypes = [P, P, i32, f64, i32, f64, f64, f64, f64]
+    for f in (lib.pa_decode_masked, lib.pa_prefill_masked, lib.pa_rope, lib.pa_rope_and_cache,
+              lib.pa_rope_frequencies):
         f.restype = i32
     # host-side block manager (include/pa_block_manager.h)
     lib.pa_bm_create.argtypes = [i64, i32, ctypes.POINTER(P)]
@@ -417,6 +434,195 @@ def pa_prefill(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc
     check(load().pa_prefill(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                             block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc), S, T, max_seq_len, H, hkv,
                             D, bs, nb, float(scale), dtype_code(dt), _stream(stream)))
+
+
+# --- capped, biased and masked attention -----------------------------------------------------------
+
+def _int32(name, x):
+    """x, refused where C's int cannot hold it: ctypes would cut off its upper bits."""
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} {x} is past 32 bits")
+    return x
+
+
+def _masked_pools(q, out, k_cache, v_cache):
+    """The checks of q, out and the pools; returns (num_blocks, kv heads, block size)."""
+    _need_here("q", q, None, 3)
+    _need_here("out", out, q.dtype, 3)
+    _need_here("k_cache", k_cache, None, 5)
+    _need_here("v_cache", v_cache, k_cache.dtype, 4)
+    if out.shape != q.shape:
+        raise PAError(PA_ERR_INVALID_ARG, "out and q differ in shape")
+    nb, hkv, d, bs = v_cache.shape
+    x = 16 // k_cache.element_size()
+    if d != q.shape[2] or k_cache.shape != (nb, hkv, d // x, bs, x):
+        raise PAError(PA_ERR_INVALID_ARG, f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not "
+                                          f"hold rows of {q.shape[2]} dims")
+    return nb, hkv, bs
+
+
+def _masked_tables(q, block_tables, seq_lens, alibi_slopes):
+    import torch
+    _need_here("block_tables", block_tables, torch.int32, 2)
+    _need_here("seq_lens", seq_lens, torch.int32, 1)
+    if block_tables.shape[0] != seq_lens.shape[0]:
+        raise PAError(PA_ERR_INVALID_ARG, "block_tables and seq_lens must have one row per sequence")
+    if alibi_slopes is not None:
+        _need_here("alibi_slopes", alibi_slopes, torch.float32, 1)
+        if alibi_slopes.shape[0] != q.shape[1]:
+            raise PAError(PA_ERR_INVALID_ARG, "alibi_slopes must have one entry per query head")
+
+
+def pa_decode_masked_workspace_size(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, window,
+                                    cache_dtype):
+    return load().pa_decode_masked_workspace_size(num_seqs, num_heads, num_kv_heads, head_size,
+                                                  _int32("max_seq_len", max_seq_len), block_size,
+                                                  _int32("window", window),
+                                                  cache_dtype if isinstance(cache_dtype, int) else dtype_code(cache_dtype))
+
+
+def pa_decode_masked(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len, softcap=0.0,
+                     alibi_slopes=None, window=0, k_scale=1.0, v_scale=1.0, workspace=None, stream=None):
+    """Decode attention whose scores are capped at +-softcap by a tanh (0: not), lowered by
+    alibi_slopes[h] (fp32 [H], or None) per position of distance, and limited to the last
+    `window` positions (0: all); writes out [S, H, D].  Pools as in pa_decode_scaled.
+
+    max_seq_len is a host-side bound on seq_lens.  When the call needs a workspace and
+    none is given, or too small a one, one is taken from torch's allocator.  Returns the
+    workspace tensor used (or None).
+    """
+    nb, hkv, bs = _masked_pools(q, out, k_cache, v_cache)
+    _masked_tables(q, block_tables, seq_lens, alibi_slopes)
+    S, H, D = q.shape
+    if seq_lens.shape[0] != S:
+        raise PAError(PA_ERR_INVALID_ARG, "q must have one row per sequence")
+    cc = dtype_code(k_cache.dtype)
+    lib = load()
+    need = pa_decode_masked_workspace_size(S, H, hkv, D, max_seq_len, bs, window, cc)
+    if workspace is not None:
+        _need_here("workspace", workspace)
+    workspace = _workspace(need, workspace, q.device, stream)
+    check(lib.pa_decode_masked(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                               block_tables.shape[1], _ptr(seq_lens), S, max_seq_len, H, hkv, D, bs, nb, float(scale),
+                               float(softcap), _ptr(alibi_slopes), window, _ptr(workspace),
+                               workspace.nbytes if workspace is not None else 0, dtype_code(q.dtype), cc,
+                               float(k_scale), float(v_scale), _stream(stream)))
+    return workspace
+
+
+def pa_prefill_masked(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, max_seq_len,
+                      softcap=0.0, alibi_slopes=None, window=0, prefix_lens=None, stream=None):
+    """Chunked prefill (pa_prefill) with scores changed as in pa_decode_masked; prefix_lens
+    (int32 [S], or None): the leading positions of each sequence that all of its rows see,
+    those before them too."""
+    import torch
+    nb, hkv, bs = _masked_pools(q, out, k_cache, v_cache)
+    _masked_tables(q, block_tables, seq_lens, alibi_slopes)
+    _need_here("query_start_loc", query_start_loc, torch.int32, 1)
+    T, H, D = q.shape
+    S = seq_lens.shape[0]
+    if k_cache.dtype != q.dtype:
+        raise PAError(PA_ERR_INVALID_ARG, f"q has dtype {q.dtype}, the pools {k_cache.dtype}")
+    if query_start_loc.shape[0] != S + 1:
+        raise PAError(PA_ERR_INVALID_ARG, "query_start_loc must have num_seqs + 1 entries")
+    if prefix_lens is not None:
+        _need_here("prefix_lens", prefix_lens, torch.int32, 1)
+        if prefix_lens.shape[0] != S:
+            raise PAError(PA_ERR_INVALID_ARG, "prefix_lens must have one entry per sequence")
+    check(load().pa_prefill_masked(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                   block_tables.shape[1], _ptr(seq_lens), _ptr(query_start_loc), _ptr(prefix_lens), S,
+                                   T, _int32("max_seq_len", max_seq_len), H, hkv, D, bs, nb, float(scale),
+                                   float(softcap), _ptr(alibi_slopes), _int32("window", window), dtype_code(q.dtype),
+                                   _stream(stream)))
+
+
+# --- rotary positions ------------------------------------------------------------------------------
+
+def pa_rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=0, low=1.0, high=32.0):
+    """inv_freq (float64 [rotary_dim / 2], on the CPU: move it to the GPU once) and the amplitude for
+    pa_rope and pa_rope_and_cache.  scaling: None, "linear", "bands" (by turns over original_len: low and
+    high, often 1 and 4) or "yarn" (low and high often 1 and 32)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise PAError(PA_ERR_INVALID_ARG, f"unknown scaling {scaling!r}")
+    inv_freq = torch.empty(max(0, _int32("rotary_dim", rotary_dim)) // 2, dtype=torch.float64)
+    amplitude = ctypes.c_float(1.0)
+    check(load().pa_rope_frequencies(ctypes.c_void_p(inv_freq.data_ptr()), ctypes.byref(amplitude), rotary_dim,
+                                     float(base), ROPE_SCALINGS[scaling], float(factor), float(original_len),
+                                     float(low), float(high)))
+    return inv_freq, amplitude.value
+
+
+def _rope_rows(name, t, dtype, heads=None):
+    """The stride (in elements) from one token's row of t [T, heads, D] to the next, the row itself contiguous."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} must be on the current CUDA device")
+    if t.dtype != dtype or t.dim() != 3 or (heads is not None and t.shape[1:] != heads):
+        raise PAError(PA_ERR_INVALID_ARG, f"{name} is {t.dtype} {tuple(t.shape)}: {dtype} [T, heads, D] is expected")
+    T, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise PAError(PA_ERR_INVALID_ARG, f"a token's row of {name} must be contiguous")
+    return t.stride(0) if T > 1 else h * d
+
+
+def _rope_args(q_out, q, key, positions, inv_freq):
+    """The checks that both rope calls make; returns (q stride, key stride)."""
+    import torch
+    sq = _rope_rows("q", q, q.dtype)
+    T, H, D = q.shape
+    sk = _rope_rows("key", key, q.dtype)
+    if key.shape[0] != T or key.shape[2] != D:
+        raise PAError(PA_ERR_INVALID_ARG, "q and key differ in tokens or head size")
+    _need_here("q_out", q_out, q.dtype, 3)
+    if q_out.shape != q.shape:
+        raise PAError(PA_ERR_INVALID_ARG, "q_out and q differ in shape")
+    _need_here("positions", positions, torch.int64, 1)
+    if positions.shape[0] != T:
+        raise PAError(PA_ERR_INVALID_ARG, "positions must have one entry per token")
+    _need_here("inv_freq", inv_freq, torch.float64, 1)
+    return sq, sk
+
+
+def pa_rope(q_out, key_out, q, key, positions, inv_freq, layout=ROPE_HALVES, amplitude=1.0, stream=None):
+    """Rotary positions: q [T, H, D] and key [T, Hkv, D] (rows may lie apart, as views of one projection's)
+    turned by positions (int64 [T]) times inv_freq (float64 [rotary dims / 2]) into q_out and key_out
+    (contiguous; may be q and key themselves)."""
+    sq, sk = _rope_args(q_out, q, key, positions, inv_freq)
+    _need_here("key_out", key_out, q.dtype, 3)
+    if key_out.shape != key.shape:
+        raise PAError(PA_ERR_INVALID_ARG, "key_out and key differ in shape")
+    T, H, D = q.shape
+    check(load().pa_rope(_ptr(q_out), _ptr(key_out), _ptr(q), _ptr(key), sq, sk, _ptr(positions), _ptr(inv_freq), T, H,
+                         key.shape[1], D, 2 * inv_freq.shape[0], layout, float(amplitude), dtype_code(q.dtype),
+                         _stream(stream)))
+
+
+def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, layout=ROPE_HALVES,
+                      amplitude=1.0, k_scale=1.0, v_scale=1.0, stream=None):
+    """pa_rope, but the turned keys go into the paged pools with the values, through slot_mapping
+    (int64 [T]), as pa_reshape_and_cache_scaled writes them."""
+    import torch
+    sq, sk = _rope_args(q_out, q, key, positions, inv_freq)
+    sv = _rope_rows("value", value, q.dtype, key.shape[1:])
+    T, H, D = q.shape
+    hkv = key.shape[1]
+    if value.shape[0] != T:
+        raise PAError(PA_ERR_INVALID_ARG, "key and value differ in tokens")
+    _need_here("k_cache", k_cache, None, 5)
+    _need_here("v_cache", v_cache, k_cache.dtype, 4)
+    nb, h, d, bs = v_cache.shape
+    x = 16 // k_cache.element_size()
+    if h != hkv or d != D or k_cache.shape != (nb, h, d // x, bs, x):
+        raise PAError(PA_ERR_INVALID_ARG, f"k_cache {tuple(k_cache.shape)} and v_cache {tuple(v_cache.shape)} do not "
+                                          f"hold {hkv} heads of {D} dims")
+    _need_here("slot_mapping", slot_mapping, torch.int64, 1)
+    if slot_mapping.shape[0] != T:
+        raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must have one entry per token")
+    check(load().pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(key), _ptr(value), sq, sk, sv, _ptr(k_cache),
+                                   _ptr(v_cache), _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), T, H, hkv, D,
+                                   2 * inv_freq.shape[0], bs, nb, layout, float(amplitude), dtype_code(q.dtype),
+                                   dtype_code(k_cache.dtype), float(k_scale), float(v_scale), _stream(stream)))
 
 
 # --- FP4 pools -----------------------------------------------------------------------------------

@@ -190,7 +190,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 // kMaxSeqsPerLaunch sequences.  Partial slots: one per warp plus one per segment,
 // the most pieces a launch can leave (pieces start at warp or segment boundaries).
 pa_status make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len, int block_size,
-                    int partition_size, pa_dtype dtype, DecodePlan* pl, bool shared = false) {
+                    int partition_size, pa_dtype dtype, DecodePlan* pl, bool shared = false, bool masked = false) {
   const int group = num_heads / num_kv_heads;
   pl->members = shared ? shared_members(dtype, num_heads, num_kv_heads) : 0;
   if (pl->members && (max_seq_len + block_size - 1) / block_size >= (1 << pa::kInfoOffBits))
@@ -207,7 +207,8 @@ pa_status make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size
   if (chunk > 0x7fffffffLL / unit_cost) chunk = 0x7fffffffLL / unit_cost;
   if (chunk < 1) chunk = 1;
   pl->chunk = static_cast<int>(chunk);
-  const int ctas = pa::decode_ctas_per_sm(static_cast<int>(dtype), head_size, block_size, pl->kind);
+  const int ctas = masked ? pa::decode_masked_ctas_per_sm(static_cast<int>(dtype), head_size, block_size, pl->kind)
+                          : pa::decode_ctas_per_sm(static_cast<int>(dtype), head_size, block_size, pl->kind);
   const int sms = sm_count();
   if (ctas <= 0 || sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device (SM count %d, CTAs per SM %d)", sms, ctas);
   const int warps = pa::decode_warps_for(elem_bytes(dtype), head_size, block_size, pl->kind);
@@ -236,6 +237,30 @@ pa_status make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size
   if (pl->members) off = align256(off + (size_t)chunk * 2 * sizeof(int));
   pl->bytes = off;
   return PA_OK;
+}
+
+// What pa_decode_masked and pa_prefill_masked add to a call.
+struct ScoreMod {
+  float softcap;        // 0: none
+  const float* slopes;  // null: none
+  int window;           // 0: none
+};
+
+// The tokens that a window leaves of max_seq_len, rounded up to the blocks they may lie in.
+int windowed_len(int max_seq_len, int window, int block_size) {
+  if (window <= 0) return max_seq_len;
+  const long long n = (((long long)window + block_size - 2) / block_size + 1) * block_size;
+  return n < max_seq_len ? static_cast<int>(n) : max_seq_len;
+}
+
+// A cap is 0 or in a range in which cap * log2(e) and 1 / cap are ordinary fp32 numbers.
+bool softcap_ok(float cap) { return cap == 0.f || (cap >= 0x1p-64f && cap <= 0x1p64f); }
+
+// The factor that brings q.k to the argument of the kernels' softmax, or, capped, of their tanh:
+// s / cap for the CUDA-core kernels, 2 log2(e) s / cap for the tensor-core ones.
+double score_factor(double scale, float softcap, bool tensor_cores) {
+  constexpr double kLog2e = 1.4426950408889634;
+  return softcap == 0.f ? scale * kLog2e : scale / softcap * (tensor_cores ? 2 * kLog2e : 1.0);
 }
 
 // A fresh tag for every launch, so a launch never mistakes a partial slot left by
@@ -303,6 +328,28 @@ cudaError_t launch_decode(int dtype, int head_size, int block_size, const Decode
     case PA_F32: return launch_decode_f32(head_size, block_size, p, kind, grid, stream, launches);
     case PA_F16: return launch_decode_f16(head_size, block_size, p, kind, grid, stream, launches);
     case PA_BF16: return launch_decode_bf16(head_size, block_size, p, kind, grid, stream, launches);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+int decode_masked_ctas_per_sm(int dtype, int head_size, int block_size, DecodeKind kind) {
+  switch (dtype) {
+    case PA_F32: return decode_masked_ctas_per_sm_f32(head_size, block_size, kind);
+    case PA_F16: return decode_masked_ctas_per_sm_f16(head_size, block_size, kind);
+    case PA_BF16: return decode_masked_ctas_per_sm_bf16(head_size, block_size, kind);
+    case PA_FP8_E4M3: return decode_masked_ctas_per_sm_fp8(false, head_size, block_size, kind);
+    default: return 0;
+  }
+}
+
+cudaError_t launch_decode_masked(int dtype, int head_size, int block_size, const DecodeMaskedParams& p, DecodeKind kind,
+                                 int grid, cudaStream_t stream, int* launches) {
+  if (dtype >= 16)  // as in launch_decode
+    return launch_decode_masked_fp8(dtype - 16 == PA_BF16, head_size, block_size, p, kind, grid, stream, launches);
+  switch (dtype) {
+    case PA_F32: return launch_decode_masked_f32(head_size, block_size, p, kind, grid, stream, launches);
+    case PA_F16: return launch_decode_masked_f16(head_size, block_size, p, kind, grid, stream, launches);
+    case PA_BF16: return launch_decode_masked_bf16(head_size, block_size, p, kind, grid, stream, launches);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -446,9 +493,11 @@ static pa_status decode_impl(void* out, const void* q, const void* k_cache, cons
                              size_t workspace_bytes, pa_dtype q_dtype, pa_dtype dtype, float k_scale, float v_scale,
                              void* stream, const void* new_key = nullptr, const void* new_value = nullptr,
                              const int64_t* copy_pairs = nullptr, int64_t num_copies = 0,
-                             const int32_t* prefix_group = nullptr, const int32_t* prefix_blocks = nullptr) {
+                             const int32_t* prefix_group = nullptr, const int32_t* prefix_blocks = nullptr,
+                             const ScoreMod* mod = nullptr) {
   // new_key != nullptr: the fused step (pa_decode_step), already validated there.
   // `dtype` is the cache dtype from here on; q and out have q_dtype.
+  // mod != nullptr: pa_decode_masked, its own arguments already validated there.
   pa_status st = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, dtype);
   if (st != PA_OK) return st;
   if (dtype == PA_FP8_E4M3) {
@@ -477,14 +526,15 @@ static pa_status decode_impl(void* out, const void* q, const void* k_cache, cons
   if (prefix_group && (!aligned(prefix_group, 4) || !aligned(prefix_blocks, 4)))
     return fail(PA_ERR_ALIGNMENT, "prefix_group and prefix_blocks need 4-byte alignment");
   DecodePlan pl;
-  st = make_plan(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, partition_size, dtype, &pl,
-                 prefix_group != nullptr);
+  st = make_plan(num_seqs, num_heads, num_kv_heads, head_size,
+                 mod ? windowed_len(max_seq_len, mod->window, block_size) : max_seq_len, block_size, partition_size,
+                 dtype, &pl, prefix_group != nullptr, mod != nullptr);
   if (st != PA_OK) return st;
   if (!workspace || workspace_bytes < pl.bytes)
     return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", pl.bytes, workspace ? workspace_bytes : 0);
   if (!aligned(workspace, 16)) return fail(PA_ERR_ALIGNMENT, "workspace needs 16-byte alignment");
 
-  pa::DecodeParams p{};
+  pa::DecodeMaskedParams p{};  // (its own members stay unused without mod)
   char* ws = static_cast<char*>(workspace);
   p.part_tag = reinterpret_cast<int2*>(ws + pl.off_tag);
   p.part_ml = reinterpret_cast<float*>(ws + pl.off_ml);
@@ -514,6 +564,14 @@ static pa_status decode_impl(void* out, const void* q, const void* k_cache, cons
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * k_scale * 1.4426950408889634);
   p.out_scale = v_scale;
   p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
+  if (mod) {
+    p.scale_log2 = static_cast<float>(score_factor(static_cast<double>(scale) * k_scale, mod->softcap,
+                                                   pl.kind != pa::DecodeKind::kSimt));
+    if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale / softcap is not finite");
+    p.cap_log2 = static_cast<float>(mod->softcap * 1.4426950408889634);
+    p.slopes = mod->slopes;
+    p.window = mod->window;
+  }
 
   if (p.fused && num_copies > 0) {  // the copy-on-write copies: their own kernel, before any token lands
     int n = 0;
@@ -542,8 +600,10 @@ static pa_status decode_impl(void* out, const void* q, const void* k_cache, cons
     }
     p.epoch = next_epoch();
     int n = 0;
-    const cudaError_t ce = pa::launch_decode(launch_dtype, head_size, block_size, p, pl.kind, pl.grid,
-                                             static_cast<cudaStream_t>(stream), &n);
+    const auto cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t ce =
+        mod ? pa::launch_decode_masked(launch_dtype, head_size, block_size, p, pl.kind, pl.grid, cs, &n)
+            : pa::launch_decode(launch_dtype, head_size, block_size, p, pl.kind, pl.grid, cs, &n);
     g_launches.fetch_add(n, std::memory_order_relaxed);
     if (ce != cudaSuccess) return cuda_fail(ce, "decode launch");
   }
@@ -652,11 +712,47 @@ pa_status pa_decode_shared(void* out, const void* q, const void* key, const void
                      prefix_group, prefix_blocks);
 }
 
-pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
-                     const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
-                     const int32_t* query_start_loc, int num_seqs, int num_query_tokens, int max_seq_len,
-                     int num_heads, int num_kv_heads, int head_size, int block_size, int64_t num_blocks, float scale,
-                     pa_dtype dtype, void* stream) {
+static pa_status check_mod(float softcap, const float* slopes, int window) {
+  if (!softcap_ok(softcap)) return fail(PA_ERR_INVALID_ARG, "softcap must be 0 or in [2^-64, 2^64]");
+  if (slopes && !aligned(slopes, 4)) return fail(PA_ERR_ALIGNMENT, "alibi_slopes need 4-byte alignment");
+  if (window < 0) return fail(PA_ERR_INVALID_ARG, "window %d < 0", window);
+  return PA_OK;
+}
+
+size_t pa_decode_masked_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size, int max_seq_len,
+                                       int block_size, int window, pa_dtype cache_dtype) {
+  if (check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, cache_dtype) != PA_OK ||
+      window < 0 || num_seqs == 0)
+    return 0;
+  DecodePlan pl;
+  if (make_plan(num_seqs, num_heads, num_kv_heads, head_size, windowed_len(max_seq_len, window, block_size), block_size,
+                PA_PARTITION_NONE, cache_dtype, &pl, false, true) != PA_OK)
+    return 0;
+  return pl.bytes;
+}
+
+pa_status pa_decode_masked(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                           int max_seq_len, int num_heads, int num_kv_heads, int head_size, int block_size,
+                           int64_t num_blocks, float scale, float softcap, const float* alibi_slopes, int window,
+                           void* workspace, size_t workspace_bytes, pa_dtype q_dtype, pa_dtype cache_dtype,
+                           float k_scale, float v_scale, void* stream) {
+  if (!elem_bytes(q_dtype)) return fail(PA_ERR_INVALID_ARG, "unknown query dtype %d", static_cast<int>(q_dtype));
+  const pa_status st = check_mod(softcap, alibi_slopes, window);
+  if (st != PA_OK) return st;
+  const ScoreMod mod{softcap, alibi_slopes, window};
+  return decode_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, max_seq_len,
+                     num_heads, num_kv_heads, head_size, block_size, num_blocks, scale, PA_PARTITION_NONE, workspace,
+                     workspace_bytes, q_dtype, cache_dtype, k_scale, v_scale, stream, nullptr, nullptr, nullptr, 0,
+                     nullptr, nullptr, &mod);
+}
+
+static pa_status prefill_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                              const int32_t* query_start_loc, int num_seqs, int num_query_tokens, int max_seq_len,
+                              int num_heads, int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                              float scale, pa_dtype dtype, void* stream, const ScoreMod* mod = nullptr,
+                              const int32_t* prefix_lens = nullptr) {
   pa_status st = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, max_seq_len, block_size, dtype);
   if (st != PA_OK) return st;
   if (dtype != PA_F16 && dtype != PA_BF16) return fail(PA_ERR_UNSUPPORTED, "prefill runs on fp16 and bf16 caches");
@@ -677,7 +773,7 @@ pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* 
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4))
     return fail(PA_ERR_ALIGNMENT, "q/out/caches need 16-byte, tables and lengths 4-byte alignment");
-  pa::PrefillParams p{};
+  pa::PrefillMaskedParams p{};  // (its own members stay unused without mod)
   st = device_error_ptr(&p.err);
   if (st != PA_OK) return st;
   p.out = out;
@@ -693,18 +789,212 @@ pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* 
   p.max_seq_len = max_seq_len;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
+  if (mod) {
+    p.scale_log2 = static_cast<float>(score_factor(scale, mod->softcap, true));
+    if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale / softcap is not finite");
+    p.cap_log2 = static_cast<float>(mod->softcap * 1.4426950408889634);
+    p.slopes = mod->slopes;
+    p.window = mod->window;
+  }
   for (int c0 = 0; c0 < num_seqs; c0 += pa::kMaxSeqsPerLaunch) {
     p.num_seqs = num_seqs - c0 < pa::kMaxSeqsPerLaunch ? num_seqs - c0 : pa::kMaxSeqsPerLaunch;
     p.block_tables = block_tables + (size_t)c0 * max_blocks_per_seq;
     p.seq_lens = seq_lens + c0;
     p.query_start_loc = query_start_loc + c0;  // offsets stay absolute rows of q and out
+    p.prefix_lens = prefix_lens ? prefix_lens + c0 : nullptr;
     int n = 0;
-    const cudaError_t ce = pa::launch_prefill(static_cast<int>(dtype), head_size, block_size, p,
-                                              static_cast<cudaStream_t>(stream), &n);
+    const auto cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t ce =
+        mod ? pa::launch_prefill_masked(static_cast<int>(dtype), head_size, block_size, p, cs, &n)
+            : pa::launch_prefill(static_cast<int>(dtype), head_size, block_size, p, cs, &n);
     g_launches.fetch_add(n, std::memory_order_relaxed);
     if (ce != cudaSuccess) return cuda_fail(ce, "prefill launch");
   }
   return PA_OK;
+}
+
+pa_status pa_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                     const int32_t* query_start_loc, int num_seqs, int num_query_tokens, int max_seq_len,
+                     int num_heads, int num_kv_heads, int head_size, int block_size, int64_t num_blocks, float scale,
+                     pa_dtype dtype, void* stream) {
+  return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
+                      num_query_tokens, max_seq_len, num_heads, num_kv_heads, head_size, block_size, num_blocks, scale,
+                      dtype, stream);
+}
+
+pa_status pa_prefill_masked(void* out, const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                            const int32_t* query_start_loc, const int32_t* prefix_lens, int num_seqs,
+                            int num_query_tokens, int max_seq_len, int num_heads, int num_kv_heads, int head_size,
+                            int block_size, int64_t num_blocks, float scale, float softcap, const float* alibi_slopes,
+                            int window, pa_dtype dtype, void* stream) {
+  const pa_status st = check_mod(softcap, alibi_slopes, window);
+  if (st != PA_OK) return st;
+  if (!(scale > 0.f)) return fail(PA_ERR_INVALID_ARG, "scale must be positive");
+  if (prefix_lens && !aligned(prefix_lens, 4)) return fail(PA_ERR_ALIGNMENT, "prefix_lens need 4-byte alignment");
+  const ScoreMod mod{softcap, alibi_slopes, window};
+  return prefill_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
+                      num_query_tokens, max_seq_len, num_heads, num_kv_heads, head_size, block_size, num_blocks, scale,
+                      dtype, stream, &mod, prefix_lens);
+}
+
+// --- rotary positions ------------------------------------------------------------------------
+
+pa_status pa_rope_frequencies(double* inv_freq, float* amplitude, int rotary_dim, double base, pa_rope_scaling scaling,
+                              double factor, double original_len, double low, double high) {
+  if (!inv_freq || !amplitude) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (rotary_dim < 2 || rotary_dim % 2) return fail(PA_ERR_INVALID_ARG, "rotary_dim %d must be positive and even", rotary_dim);
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(PA_ERR_INVALID_ARG, "base must be finite and above 1");
+  if (scaling != PA_ROPE_PLAIN && scaling != PA_ROPE_LINEAR && scaling != PA_ROPE_BANDS && scaling != PA_ROPE_YARN)
+    return fail(PA_ERR_INVALID_ARG, "unknown scaling %d", static_cast<int>(scaling));
+  if (scaling != PA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(PA_ERR_INVALID_ARG, "factor must be finite and at least 1");
+  if (scaling == PA_ROPE_BANDS || scaling == PA_ROPE_YARN) {
+    if (!(original_len >= 1.0) || !std::isfinite(original_len))
+      return fail(PA_ERR_INVALID_ARG, "original_len must be finite and at least 1");
+    if (!(low > 0.0) || !(high > low) || !std::isfinite(high))
+      return fail(PA_ERR_INVALID_ARG, "low and high must be finite with 0 < low < high");
+  }
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const int pairs = rotary_dim / 2;
+  // YaRN: the pair that makes `turns` turns over the original length, as a real index
+  auto pair_of = [&](double turns) { return rotary_dim * std::log(original_len / (turns * kTwoPi)) / (2.0 * std::log(base)); };
+  double lo = 0.0, hi = 1.0;
+  if (scaling == PA_ROPE_YARN) {
+    lo = std::fmax(std::floor(pair_of(high)), 0.0);
+    hi = std::fmin(std::ceil(pair_of(low)), rotary_dim - 1.0);
+    if (hi <= lo) hi = lo + 0.001;
+  }
+  *amplitude = scaling == PA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  for (int i = 0; i < pairs; ++i) {
+    const double f = std::pow(base, -2.0 * i / rotary_dim);
+    double keep = 1.0;  // the share of the unscaled frequency
+    if (scaling == PA_ROPE_LINEAR) keep = 0.0;
+    else if (scaling == PA_ROPE_BANDS) keep = std::fmin(std::fmax((original_len * f / kTwoPi - low) / (high - low), 0.0), 1.0);
+    else if (scaling == PA_ROPE_YARN) keep = 1.0 - std::fmin(std::fmax((i - lo) / (hi - lo), 0.0), 1.0);
+    inv_freq[i] = keep * f + (1.0 - keep) * (scaling == PA_ROPE_PLAIN ? f : f / factor);
+  }
+  return PA_OK;
+}
+
+// What pa_rope and pa_rope_and_cache share.
+static pa_status check_rope(int64_t num_tokens, int num_heads, int num_kv_heads, int head_size, int rotary_dim,
+                            pa_rope_layout layout, float amplitude, pa_dtype dtype) {
+  if (dtype != PA_F32 && dtype != PA_F16 && dtype != PA_BF16)
+    return fail(PA_ERR_UNSUPPORTED, "rows are fp32, fp16 or bf16 (dtype %d)", static_cast<int>(dtype));
+  if (num_tokens < 0 || num_tokens > 0x7fffffffLL) return fail(PA_ERR_INVALID_ARG, "num_tokens %lld", (long long)num_tokens);
+  if (num_heads < 1 || num_kv_heads < 1) return fail(PA_ERR_INVALID_ARG, "num_heads and num_kv_heads must be positive");
+  if (num_heads > 65535 || num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "more than 65535 heads");
+  if (head_size != 64 && head_size != 128) return fail(PA_ERR_UNSUPPORTED, "head_size %d not in {64, 128}", head_size);
+  if (rotary_dim < 2 || rotary_dim > head_size || rotary_dim % 2)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d must be even and in [2, head_size]", rotary_dim);
+  if (rotary_dim % 16) return fail(PA_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16", rotary_dim);
+  if (layout != PA_ROPE_HALVES && layout != PA_ROPE_PAIRS)
+    return fail(PA_ERR_INVALID_ARG, "unknown layout %d", static_cast<int>(layout));
+  if (!std::isfinite(amplitude)) return fail(PA_ERR_INVALID_ARG, "amplitude is not finite");
+  return PA_OK;
+}
+
+// A row stride: at least the row, in whole 16-byte pieces.
+static pa_status check_stride(const char* name, int64_t stride, int64_t row, pa_dtype dtype) {
+  if (stride < row) return fail(PA_ERR_INVALID_ARG, "%s_stride %lld is below a token's %lld elements", name,
+                                (long long)stride, (long long)row);
+  if (stride > (1ll << 31)) return fail(PA_ERR_UNSUPPORTED, "%s_stride %lld is past 2^31", name, (long long)stride);
+  if (stride % (16 / elem_bytes(dtype)))
+    return fail(PA_ERR_ALIGNMENT, "%s_stride %lld is not a multiple of 16 bytes", name, (long long)stride);
+  return PA_OK;
+}
+
+static pa_status launch_rope(pa::RopeParams& p, pa_dtype dtype, int cache_dtype, int head_size, pa_rope_layout layout,
+                             void* stream) {
+  pa_status st = device_error_ptr(&p.err);
+  if (st != PA_OK) return st;
+  const int sms = sm_count();
+  if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
+  int n = 0;
+  const cudaError_t ce = pa::launch_rope(static_cast<int>(dtype), cache_dtype, head_size, layout == PA_ROPE_PAIRS, p, sms,
+                                         static_cast<cudaStream_t>(stream), &n);
+  g_launches.fetch_add(n, std::memory_order_relaxed);
+  return ce == cudaSuccess ? PA_OK : cuda_fail(ce, "rope launch");
+}
+
+pa_status pa_rope(void* q_out, void* key_out, const void* q, const void* key, int64_t q_stride, int64_t key_stride,
+                  const int64_t* positions, const double* inv_freq, int64_t num_tokens, int num_heads,
+                  int num_kv_heads, int head_size, int rotary_dim, pa_rope_layout layout, float amplitude,
+                  pa_dtype dtype, void* stream) {
+  pa_status st = check_rope(num_tokens, num_heads, num_kv_heads, head_size, rotary_dim, layout, amplitude, dtype);
+  if (st == PA_OK) st = check_stride("q", q_stride, (int64_t)num_heads * head_size, dtype);
+  if (st == PA_OK) st = check_stride("key", key_stride, (int64_t)num_kv_heads * head_size, dtype);
+  if (st != PA_OK || num_tokens == 0) return st;
+  if (!q_out || !key_out || !q || !key || !positions || !inv_freq) return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q_out, 16) || !aligned(key_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(positions, 8) ||
+      !aligned(inv_freq, 8))
+    return fail(PA_ERR_ALIGNMENT, "q/key and their outputs need 16-byte, positions and inv_freq 8-byte alignment");
+  pa::RopeParams p{};
+  p.q_out = q_out;
+  p.key_out = key_out;
+  p.q = q;
+  p.key = key;
+  p.q_stride = q_stride;
+  p.key_stride = key_stride;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.num_tokens = num_tokens;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.rotary_dim = rotary_dim;
+  p.amplitude = amplitude;
+  return launch_rope(p, dtype, -1, head_size, layout, stream);
+}
+
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* key, const void* value, int64_t q_stride,
+                            int64_t key_stride, int64_t value_stride, void* k_cache, void* v_cache,
+                            const int64_t* positions, const int64_t* slot_mapping, const double* inv_freq,
+                            int64_t num_tokens, int num_heads, int num_kv_heads, int head_size, int rotary_dim,
+                            int block_size, int64_t num_blocks, pa_rope_layout layout, float amplitude,
+                            pa_dtype key_dtype, pa_dtype cache_dtype, float k_scale, float v_scale, void* stream) {
+  pa_status st = check_rope(num_tokens, num_heads, num_kv_heads, head_size, rotary_dim, layout, amplitude, key_dtype);
+  if (st == PA_OK) st = check_stride("q", q_stride, (int64_t)num_heads * head_size, key_dtype);
+  if (st == PA_OK) st = check_stride("key", key_stride, (int64_t)num_kv_heads * head_size, key_dtype);
+  if (st == PA_OK) st = check_stride("value", value_stride, (int64_t)num_kv_heads * head_size, key_dtype);
+  if (st != PA_OK) return st;
+  if (block_size < 1 || num_blocks < 1) return fail(PA_ERR_INVALID_ARG, "block_size and num_blocks must be positive");
+  if (cache_dtype == PA_FP8_E4M3) {
+    if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+      return fail(PA_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
+  } else if (key_dtype != cache_dtype || k_scale != 1.f || v_scale != 1.f) {
+    return fail(PA_ERR_INVALID_ARG, "a 16-bit or fp32 cache takes rows of its own dtype with scales 1");
+  }
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !q || !key || !value || !k_cache || !v_cache || !positions || !slot_mapping || !inv_freq)
+    return fail(PA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(positions, 8) || !aligned(slot_mapping, 8) || !aligned(inv_freq, 8))
+    return fail(PA_ERR_ALIGNMENT, "q/key/value/caches need 16-byte, positions, slot_mapping and inv_freq 8-byte alignment");
+  pa::RopeParams p{};
+  p.q_out = q_out;
+  p.q = q;
+  p.key = key;
+  p.value = value;
+  p.q_stride = q_stride;
+  p.key_stride = key_stride;
+  p.value_stride = value_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.positions = positions;
+  p.slot_mapping = slot_mapping;
+  p.inv_freq = inv_freq;
+  p.num_tokens = num_tokens;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.num_heads = num_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.rotary_dim = rotary_dim;
+  p.amplitude = amplitude;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  return launch_rope(p, key_dtype, static_cast<int>(cache_dtype), head_size, layout, stream);
 }
 
 size_t pa_fp4_tile_bytes(int head_size, int block_size) {

@@ -117,13 +117,14 @@ __device__ __forceinline__ bool wait_stage(uint64_t* bars, uint64_t* never, unsi
   return ok;
 }
 
-// Zero the V columns of tokens >= rem in a stage (only a sequence's last, partial
-// block): those slots may hold anything, and 0 * NaN would poison the sum.
+// Zero the V columns of tokens >= rem, and of those below `from`, in a stage (only a
+// sequence's last, partial block, and the block a window starts in): those slots may hold
+// anything, and 0 * NaN would poison the sum.
 template <typename T, int D, int BS>
-__device__ __forceinline__ void zero_tail_v(unsigned char* vtile, int rem, int lane) {
+__device__ __forceinline__ void zero_outside_v(unsigned char* vtile, int from, int rem, int lane) {
   T* v = reinterpret_cast<T*>(vtile);
   for (int idx = lane; idx < D * BS; idx += 32)
-    if ((idx % BS) >= rem) v[idx] = DType<T>::from_f32(0.f);
+    if ((idx % BS) >= rem || (idx % BS) < from) v[idx] = DType<T>::from_f32(0.f);
   __syncwarp();
 }
 
@@ -168,8 +169,24 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 1 / x by the hardware's approximate reciprocal (1 / inf = 0)
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename T, typename TC, int D, int BS, int NH, bool kEarly>
+//
+// kMod (pa_decode_masked): scores are capped and biased before the softmax, and tokens
+// before the window are hidden (see Scores).
+struct Scores {  // of a block, for kMod; unused otherwise
+  float cap_log2;   // cap * log2(e); 0: no cap
+  int from;         // the block's tokens below this one are hidden
+  float base;       // position of the block's first token less that of the query (<= 0)
+};
+
+template <typename T, typename TC, int D, int BS, int NH, bool kEarly, bool kMod>
 struct MmaMath {
   static constexpr int MT = BS / 16;  // 16-token tiles of a block
   static constexpr int KS = D / 16;   // 16-dim k-steps of S^T, and 16-dim row tiles of O^T
@@ -195,6 +212,7 @@ struct MmaMath {
   uint32_t kf[FM][FK][4], vf[FM][FK][4];  // the block's K and V^T A fragments (kEarly)
   float m_[NH][2], l_[NH][2];  // running max (log2 units) and lane-partial sum of heads 8n + 2t4 + {0, 1}
   float hs_[NH][2];            // score factor (scale * log2 e, over the q scale) of heads 8n + 2t4 + {0, 1}
+  float slope_[kMod ? NH : 1][2];  // kMod: those heads' bias per position of distance, in log2 units
   uint32_t k_lane_off, v_lane_off;
   int g, t4, tok0, tok1;   // tok0 / tok1: tokens of this lane's S^T rows g and g + 8
 
@@ -283,6 +301,17 @@ struct MmaMath {
     }
   }
 
+  // kMod: the biases of query rows 0..nh-1 (slopes: the first row's; null: none).
+  __device__ __forceinline__ void load_slopes(const float* slopes, int nh) {
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int h = 8 * n + 2 * t4 + hh;
+        slope_[kMod ? n : 0][hh] = slopes && h < nh ? __ldg(slopes + h) * kLog2e : 0.f;
+      }
+  }
+
   // Read the block's K and V^T fragments out of the stage (kEarly only).
   __device__ __forceinline__ void fetch(unsigned char* stage, int tile_bytes) {
     if constexpr (kEarly) {
@@ -324,17 +353,17 @@ struct MmaMath {
   // One block: `rem` valid tokens; `live` has bit i set for every member i whose
   // columns take part (all ones outside shared segments).
   __device__ __forceinline__ void block(unsigned char* stage, int tile_bytes, int rem, float scale_log2,
-                                        uint32_t live = 0xffffffffu) {
+                                        uint32_t live, const Scores& ms) {
     if (NH == 1 || nt_ == NH)
-      block_t<NH>(stage, tile_bytes, rem, scale_log2, live);
+      block_t<NH>(stage, tile_bytes, rem, scale_log2, live, ms);
     else
-      block_t<1>(stage, tile_bytes, rem, scale_log2, live);
+      block_t<1>(stage, tile_bytes, rem, scale_log2, live, ms);
   }
 
   // block() over the first NT 8-column tiles.
   template <int NT>
   __device__ __forceinline__ void block_t(unsigned char* stage, int tile_bytes, int rem, float scale_log2,
-                                          uint32_t live) {
+                                          uint32_t live, const Scores& ms) {
     const uint32_t kb = smem_addr(stage), vb = kb + tile_bytes;
     // S^T = K Q^T for the block's BS tokens, the even and the odd 16-dim k-steps in two
     // accumulators (two dependent chains of KS/2 MMAs, added at the end)
@@ -380,6 +409,20 @@ struct MmaMath {
 #pragma unroll
         for (int c = 0; c < 4; ++c) sc[mt][n][c] += so[mt][n][c];
     }
+    if constexpr (kMod) {  // hs_ brings scores to log2 units, or, capped, to 2 log2(e) s / cap
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int tok = 16 * mt + ((c >> 1) ? tok1 : tok0);
+            float v = sc[mt][n][c] * hs_[n][c & 1];
+            // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)); off by 2^-22 of the cap at most
+            if (ms.cap_log2 != 0.f) v = fmaf(-2.f * ms.cap_log2, rcp_approx(1.f + ex2_approx(v)), ms.cap_log2);
+            sc[mt][n][c] = fmaf(slope_[n][c & 1], ms.base + tok, v);
+          }
+    }
     // Online softmax update per head (column), log2 domain; tokens past the sequence
     // (and every token, for a column whose member does not take this block) get -inf.
     bool col_ok[NH][2];
@@ -397,8 +440,8 @@ struct MmaMath {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int tok = 16 * mt + ((c >> 1) ? tok1 : tok0);
-          const float v = sc[mt][n][c] * hs_[n][c & 1];
-          sc[mt][n][c] = (tok < rem && col_ok[n][c & 1]) ? v : -INFINITY;
+          const float v = kMod ? sc[mt][n][c] : sc[mt][n][c] * hs_[n][c & 1];
+          sc[mt][n][c] = (tok < rem && (kMod ? tok >= ms.from : col_ok[n][c & 1])) ? v : -INFINITY;
           mx[n][c & 1] = fmaxf(mx[n][c & 1], sc[mt][n][c]);
         }
       }
@@ -612,7 +655,7 @@ struct MmaMath {
 // --- per-warp math: CUDA cores --------------------------------------------------------------------
 //
 // One query row against the tokens of a block.
-template <typename T, typename TC, int D, int BS>
+template <typename T, typename TC, int D, int BS, bool kMod>
 struct SimtMath {
   static constexpr int kElem = sizeof(TC);
   static constexpr int X = 16 / kElem;
@@ -628,6 +671,7 @@ struct SimtMath {
   float qv[NGH * X];
   float acc[VP];
   float m, lpart;
+  float slope_;  // kMod: the bias per position of distance, in log2 units
   float* pw;  // this warp's BS probabilities in shared memory
   int lane, half, tl, vrow, vchunk;
 
@@ -653,10 +697,12 @@ struct SimtMath {
     for (int k = 0; k < NGH * X; ++k) qv[k] = DType<T>::to_f32(qh[k]);
   }
 
+  __device__ __forceinline__ void load_slopes(const float* slopes, int) { slope_ = slopes ? __ldg(slopes) * kLog2e : 0.f; }
+
   __device__ __forceinline__ void set_columns(int) {}
 
-  __device__ __forceinline__ void block(unsigned char* stage, int tile_bytes, int rem, float scale_log2,
-                                        uint32_t = 0xffffffffu) {
+  __device__ __forceinline__ void block(unsigned char* stage, int tile_bytes, int rem, float scale_log2, uint32_t,
+                                        const Scores& ms) {
     // Scores of this lane's token(s); each half-warp covers half of the head dims.
     float sc[TP];
 #pragma unroll
@@ -671,7 +717,14 @@ struct SimtMath {
         for (int k = 0; k < X; ++k) dot = fmaf(qv[gi * X + k], DType<TC>::to_f32(kv[k]), dot);
       }
       dot += __shfl_xor_sync(0xffffffffu, dot, 16);
-      sc[tp] = tok < rem ? dot * scale_log2 : -INFINITY;
+      if constexpr (kMod) {  // scale_log2 brings scores to log2 units, or, capped, to s / cap (fp32 pools: tanhf's accuracy)
+        float v = dot * scale_log2;
+        if (ms.cap_log2 != 0.f) v = ms.cap_log2 * tanhf(v);
+        v = fmaf(slope_, ms.base + tok, v);
+        sc[tp] = tok < rem && tok >= ms.from ? v : -INFINITY;
+      } else {
+        sc[tp] = tok < rem ? dot * scale_log2 : -INFINITY;
+      }
     }
     float mx = sc[0];
 #pragma unroll
@@ -970,18 +1023,25 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
   __syncthreads();  // s_pre and s_red are rewritten by the prefix sums that follow
 }
 
+// The kernel's parameters: those of pa_decode_masked with kMod.
+template <bool kMod>
+using DecodeArgs = std::conditional_t<kMod, DecodeMaskedParams, DecodeParams>;
+
 // grid = resident CTAs (persistent); kDecodeWarps independent warps per CTA.
 // kMode: 0 = CUDA-core math, 1 or 2 = tensor-core math over 8 or 16 query heads per unit.
-template <typename T, typename TC, int D, int BS, int kMode>
+// kMod: capped or biased scores and windows (pa_decode_masked); no fused step, no shared
+// prefixes.  A window of w tokens leaves each sequence the blocks from (L - w) / BS on: they
+// are its work, and nothing before them is looked up or read.
+template <typename T, typename TC, int D, int BS, int kMode, bool kMod>
 __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
-    decode_kernel(const DecodeParams p) {
+    decode_kernel(const DecodeArgs<kMod> p) {
   using Sh = DecodeShape<TC, D, BS, kMode>;
   constexpr int kDecodeWarps = Sh::kWarps;
   constexpr bool kMma = kMode != 0;
   // Early stage release: 16-bit caches in 8-warp CTAs whose fragments of a block fit in 64 registers.
   constexpr bool kEarly = kMma && sizeof(TC) == 2 && kDecodeWarps == 8 && D * BS <= 128 * 16;
-  using Math = std::conditional_t<kMma, MmaMath<T, TC, D, BS, (kMode > 0 ? kMode : 1), kEarly>,
-                                  SimtMath<T, TC, D, BS>>;
+  using Math = std::conditional_t<kMma, MmaMath<T, TC, D, BS, (kMode > 0 ? kMode : 1), kEarly, kMod>,
+                                  SimtMath<T, TC, D, BS, kMod>>;
   constexpr int TILE = Sh::kTile, STAGES = Sh::kStages;
   extern __shared__ __align__(128) unsigned char smem[];
 
@@ -1018,7 +1078,12 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   // writes, so they are built while the previous kernel in the stream may still be
   // running (see griddep_wait below).
   const int S = p.num_seqs, U = p.units, PB = p.part_blocks;
-  const bool shared = kMma && p.shared;
+  const bool shared = kMma && !kMod && p.shared, fused = !kMod && p.fused;
+  // the first block of a sequence of L tokens that its window reaches
+  auto first_block = [&](int L) {
+    if constexpr (kMod) return p.window > 0 ? max(0, L - p.window) / BS : 0;
+    return 0;
+  };
   {
     constexpr int PER = (kMaxSeqsPerLaunch + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
     int nb[PER], wt[PER];
@@ -1028,7 +1093,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       int L = i < S ? __ldg(p.seq_lens + i) : 0;
       if (L < 1 || L > p.max_seq_len) L = 0;
       if (i < S) s_len[i] = L;
-      nb[k] = (L + BS - 1) / BS;
+      nb[k] = (L + BS - 1) / BS - first_block(L);
     }
     if (shared) {
       shared_layout<PER>(p, s_pre, s_info, s_lead, s_wsum, nb, wt, tid, warp, lane);
@@ -1226,7 +1291,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       locate(start, s_pre, S, U, s, u, j);
       p.part_tag[(long long)w + seg_id(s, u, shared && j < shared_len(s) ? 0 : 1)] = make_int2(-1, 0);
     }
-    if (p.fused) write_tokens();
+    if (fused) write_tokens();
     return;
   }
 
@@ -1248,6 +1313,8 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
         in_shared = j < B;
         if (in_shared) row = s + info_member(s_lead[s]);
         else j = info_off(s_info[s]) + j - B;
+      } else {
+        j += first_block(s_len[s]);
       }
       phys = __ldg(bt + (long long)row * p.max_blocks_per_seq + j);
       if (in_shared) {  // every member that takes this block must hold it at the same place
@@ -1281,7 +1348,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       const int st = k % STAGES;
       unsigned char* dst = ring + st * 2 * TILE;
       const long long tile = (long long)phys * p.num_kv_heads + kvh;
-      const bool with_token = p.fused && (tag >> 30);
+      const bool with_token = fused && (tag >> 30);
       mbar_arrive_expect_tx(
           &bars[st], 2 * TILE + (with_token ? 2 * D * static_cast<int>(sizeof(TC) == 1 ? sizeof(T) : sizeof(TC)) : 0));
       bulk_copy_g2s(dst, static_cast<const unsigned char*>(p.k_cache) + tile * TILE, TILE, &bars[st]);
@@ -1296,7 +1363,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     }
   };
   for (int k = 0; k < STAGES && k < len; ++k) issue(k);
-  if (p.fused) write_tokens();  // while the first stages are in flight
+  if (fused) write_tokens();  // while the first stages are in flight
 
   // The compute cursor walks the same positions in order.  Its segment is
   // (cs, cu, part); cj is the logical block, running from jstart to jend.
@@ -1310,6 +1377,8 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     const int B = shared_len(cs);
     if (cj < B) part = 0;
     else cj = info_off(s_info[cs]) + cj - B;
+  } else {
+    cj += first_block(s_len[cs]);
   }
   int L = 0, nblk = 0, kvh = 0, h0 = 0, nh = 0, seg = 0, jstart = 0, jend = 0, j0 = cj;
   int my_off = 0;          // lane m < cluster size: the first own block of member m (shared part)
@@ -1319,7 +1388,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     L = s_len[cs];
     nblk = (L + BS - 1) / BS;
     unit_heads<kMma>(p, cu, kvh, h0, nh);
-    jstart = 0;
+    jstart = first_block(L);
     jend = nblk;
     direct_ok = true;
     if (shared) {
@@ -1339,6 +1408,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     math.reset();
     math.load_q(static_cast<const T*>(p.q) + ((long long)cs * p.num_heads + h0) * D, nh, p.scale_log2, p.group,
                 (long long)p.num_heads * D);
+    if constexpr (kMod) math.load_slopes(p.slopes ? p.slopes + h0 : nullptr, nh);
   };
   enter();
 
@@ -1347,7 +1417,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     unsigned char* stage = ring + (k % STAGES) * 2 * TILE;
     // valid tokens in this block (>= 1); a shared block is full for every member that takes it
     const int rem = part == 0 ? BS : L - cj * BS;
-    if (p.fused && part != 0 && cj == nblk - 1)  // the sequence's new token: from the step's input, not the pool
+    if (fused && part != 0 && cj == nblk - 1)  // the sequence's new token: from the step's input, not the pool
     {
       if constexpr (sizeof(TC) == 1)
         inject_token_e4m3<T, D, BS>(stage, TILE, side + (k % STAGES) * Sh::kSideStage, (L - 1) % BS,
@@ -1355,7 +1425,13 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       else
         inject_token<TC, D, BS>(stage, TILE, side + (k % STAGES) * Sh::kSideStage, (L - 1) % BS, lane);
     }
-    if (rem < BS) zero_tail_v<TC, D, BS>(stage + TILE, rem, lane);
+    Scores ms{};
+    if constexpr (kMod) {
+      ms.cap_log2 = p.cap_log2;
+      ms.from = p.window > 0 ? L - p.window - cj * BS : 0;  // (below 0 past the window's first block)
+      ms.base = static_cast<float>(cj * BS - (L - 1));
+    }
+    if (rem < BS || ms.from > 0) zero_outside_v<TC, D, BS>(stage + TILE, ms.from, rem, lane);
     if constexpr (Math::kFetch) {  // the block's fragments are in registers: refill the stage now
       math.fetch(stage, TILE);
       __syncwarp();
@@ -1366,7 +1442,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     }
     // the members whose tables hold this block (every column outside shared parts)
     const uint32_t live = (shared && part == 0) ? __ballot_sync(0xffffffffu, cj < my_off) : 0xffffffffu;
-    math.block(stage, TILE, rem, p.scale_log2, live);
+    math.block(stage, TILE, rem, p.scale_log2, live, ms);
     ++cj;
     const bool seg_end = cj == jend, last = k + 1 == len;
     if (seg_end || last) {  // the end of a piece
@@ -1400,7 +1476,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
               ++cs;
             } while (s_pre[cs + 1] == s_pre[cs]);
           }
-          cj = 0;
+          cj = first_block(s_len[cs]);
           if (shared) {
             part = shared_len(cs) > 0 ? 0 : 1;
             cj = part == 0 ? 0 : info_off(s_info[cs]);
@@ -1612,36 +1688,36 @@ constexpr int decode_smem_bytes() {
   return DecodeShape<TC, D, BS, kMode>::kSmemBytes;
 }
 
-template <typename T, typename TC, int D, int BS, int kMode>
+template <typename T, typename TC, int D, int BS, int kMode, bool kMod>
 cudaError_t ensure_smem_attr() {
   static unsigned done = 0;  // bit d: set on device d
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 32 && ((__atomic_load_n(&done, __ATOMIC_ACQUIRE) >> dev) & 1u)) return cudaSuccess;
-  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&decode_kernel<T, TC, D, BS, kMode>),
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&decode_kernel<T, TC, D, BS, kMode, kMod>),
                            cudaFuncAttributeMaxDynamicSharedMemorySize, decode_smem_bytes<TC, D, BS, kMode>());
   if (e == cudaSuccess && dev < 32) __atomic_fetch_or(&done, 1u << dev, __ATOMIC_RELEASE);
   return e;
 }
 
-template <typename T, typename TC, int D, int BS, int kMode>
+template <typename T, typename TC, int D, int BS, int kMode, bool kMod>
 int decode_ctas_per_sm_t() {
-  if (ensure_smem_attr<T, TC, D, BS, kMode>() != cudaSuccess) return 0;
+  if (ensure_smem_attr<T, TC, D, BS, kMode, kMod>() != cudaSuccess) return 0;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, &decode_kernel<T, TC, D, BS, kMode>,
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, &decode_kernel<T, TC, D, BS, kMode, kMod>,
                                                     DecodeShape<TC, D, BS, kMode>::kWarps * 32,
                                                     decode_smem_bytes<TC, D, BS, kMode>()) != cudaSuccess)
     return 0;
   return n;
 }
 
-template <typename T, typename TC, int D, int BS, int kMode>
-cudaError_t launch_decode_t(const DecodeParams& p, int grid, cudaStream_t stream, int* launches) {
+template <typename T, typename TC, int D, int BS, int kMode, bool kMod>
+cudaError_t launch_decode_t(const DecodeArgs<kMod>& p, int grid, cudaStream_t stream, int* launches) {
   *launches = 0;
-  cudaError_t e = ensure_smem_attr<T, TC, D, BS, kMode>();
+  cudaError_t e = ensure_smem_attr<T, TC, D, BS, kMode, kMod>();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_kernel<T, TC, D, BS, kMode>, dim3(grid), dim3(DecodeShape<TC, D, BS, kMode>::kWarps * 32),
+  e = launch_pdl(decode_kernel<T, TC, D, BS, kMode, kMod>, dim3(grid), dim3(DecodeShape<TC, D, BS, kMode>::kWarps * 32),
                  decode_smem_bytes<TC, D, BS, kMode>(), stream, p);
   if (e != cudaSuccess) return e;
   *launches = 1;
@@ -1651,59 +1727,59 @@ cudaError_t launch_decode_t(const DecodeParams& p, int grid, cudaStream_t stream
   const bool wide = (long long)grid * DecodeShape<TC, D, BS, kMode>::kWarps >= 16 * segs;
   if (wide)
     e = launch_pdl(decode_merge_kernel<T, D, (kMode != 0), true>, dim3(static_cast<unsigned>(rows)),
-                   dim3(kMergeRows * 32), 0, stream, p);
+                   dim3(kMergeRows * 32), 0, stream, static_cast<const DecodeParams&>(p));
   else
     e = launch_pdl(decode_merge_kernel<T, D, (kMode != 0), false>,
                    dim3(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows)), dim3(kMergeRows * 32), 0, stream,
-                   p);
+                   static_cast<const DecodeParams&>(p));
   if (e != cudaSuccess) return e;
   *launches = 2;
   return cudaSuccess;
 }
 
 // fp32 caches use the CUDA-core math only; 16-bit and FP8 caches both kinds.
-template <typename T, typename TC, int D, int BS>
+template <typename T, typename TC, int D, int BS, bool kMod>
 int ctas_for(DecodeKind kind) {
   if constexpr (sizeof(T) == 4) {
-    return decode_ctas_per_sm_t<T, TC, D, BS, 0>();
+    return decode_ctas_per_sm_t<T, TC, D, BS, 0, kMod>();
   } else {
     switch (kind) {
-      case DecodeKind::kMma8: return decode_ctas_per_sm_t<T, TC, D, BS, 1>();
-      case DecodeKind::kMma16: return decode_ctas_per_sm_t<T, TC, D, BS, 2>();
-      default: return decode_ctas_per_sm_t<T, TC, D, BS, 0>();
+      case DecodeKind::kMma8: return decode_ctas_per_sm_t<T, TC, D, BS, 1, kMod>();
+      case DecodeKind::kMma16: return decode_ctas_per_sm_t<T, TC, D, BS, 2, kMod>();
+      default: return decode_ctas_per_sm_t<T, TC, D, BS, 0, kMod>();
     }
   }
 }
 
-template <typename T, typename TC, int D, int BS>
-cudaError_t launch_for(const DecodeParams& p, DecodeKind kind, int grid, cudaStream_t s, int* n) {
+template <typename T, typename TC, int D, int BS, bool kMod>
+cudaError_t launch_for(const DecodeArgs<kMod>& p, DecodeKind kind, int grid, cudaStream_t s, int* n) {
   if constexpr (sizeof(T) == 4) {
-    return launch_decode_t<T, TC, D, BS, 0>(p, grid, s, n);
+    return launch_decode_t<T, TC, D, BS, 0, kMod>(p, grid, s, n);
   } else {
     switch (kind) {
-      case DecodeKind::kMma8: return launch_decode_t<T, TC, D, BS, 1>(p, grid, s, n);
-      case DecodeKind::kMma16: return launch_decode_t<T, TC, D, BS, 2>(p, grid, s, n);
-      default: return launch_decode_t<T, TC, D, BS, 0>(p, grid, s, n);
+      case DecodeKind::kMma8: return launch_decode_t<T, TC, D, BS, 1, kMod>(p, grid, s, n);
+      case DecodeKind::kMma16: return launch_decode_t<T, TC, D, BS, 2, kMod>(p, grid, s, n);
+      default: return launch_decode_t<T, TC, D, BS, 0, kMod>(p, grid, s, n);
     }
   }
 }
 
-template <typename T, typename TC>
+template <typename T, typename TC, bool kMod = false>
 int decode_ctas_per_sm_dispatch(int head_size, int block_size, DecodeKind kind) {
-  if (head_size == 64 && block_size == 16) return ctas_for<T, TC, 64, 16>(kind);
-  if (head_size == 64 && block_size == 32) return ctas_for<T, TC, 64, 32>(kind);
-  if (head_size == 128 && block_size == 16) return ctas_for<T, TC, 128, 16>(kind);
-  if (head_size == 128 && block_size == 32) return ctas_for<T, TC, 128, 32>(kind);
+  if (head_size == 64 && block_size == 16) return ctas_for<T, TC, 64, 16, kMod>(kind);
+  if (head_size == 64 && block_size == 32) return ctas_for<T, TC, 64, 32, kMod>(kind);
+  if (head_size == 128 && block_size == 16) return ctas_for<T, TC, 128, 16, kMod>(kind);
+  if (head_size == 128 && block_size == 32) return ctas_for<T, TC, 128, 32, kMod>(kind);
   return 0;
 }
 
-template <typename T, typename TC>
-cudaError_t launch_decode_dispatch(int head_size, int block_size, const DecodeParams& p, DecodeKind kind, int grid,
+template <typename T, typename TC, bool kMod = false>
+cudaError_t launch_decode_dispatch(int head_size, int block_size, const DecodeArgs<kMod>& p, DecodeKind kind, int grid,
                                    cudaStream_t s, int* n) {
-  if (head_size == 64 && block_size == 16) return launch_for<T, TC, 64, 16>(p, kind, grid, s, n);
-  if (head_size == 64 && block_size == 32) return launch_for<T, TC, 64, 32>(p, kind, grid, s, n);
-  if (head_size == 128 && block_size == 16) return launch_for<T, TC, 128, 16>(p, kind, grid, s, n);
-  if (head_size == 128 && block_size == 32) return launch_for<T, TC, 128, 32>(p, kind, grid, s, n);
+  if (head_size == 64 && block_size == 16) return launch_for<T, TC, 64, 16, kMod>(p, kind, grid, s, n);
+  if (head_size == 64 && block_size == 32) return launch_for<T, TC, 64, 32, kMod>(p, kind, grid, s, n);
+  if (head_size == 128 && block_size == 16) return launch_for<T, TC, 128, 16, kMod>(p, kind, grid, s, n);
+  if (head_size == 128 && block_size == 32) return launch_for<T, TC, 128, 32, kMod>(p, kind, grid, s, n);
   return cudaErrorInvalidValue;
 }
 

@@ -94,6 +94,15 @@ struct DecodeParams {
   int members;
 };
 
+// Capped and biased scores, windows (pa_decode_masked).  With a cap, scale_log2 is the
+// factor to the tanh's argument instead: 2 log2(e) scale * k_scale / cap for the
+// tensor-core kernels, scale / cap for the others.
+struct DecodeMaskedParams : DecodeParams {
+  float cap_log2;               // cap * log2(e); 0: no cap
+  const float* slopes;          // [H]: the score of a token at distance n falls by slopes[h] n; null: no bias
+  int window;                   // the last `window` tokens are attended to; 0: all
+};
+
 // Packed per-sequence cluster layout (shared prefixes).  info: bits 0..21 the
 // sequence's shared blocks sh (its own segment starts there), bits 22..26 its
 // member index (0 = the cluster's leader), bits 27..31 the cluster size minus one
@@ -143,6 +152,11 @@ int decode_ctas_per_sm(int dtype, int head_size, int block_size, DecodeKind kind
 cudaError_t launch_decode(int dtype, int head_size, int block_size, const DecodeParams& p, DecodeKind kind,
                           int grid, cudaStream_t stream, int* launches);
 
+// The same for pa_decode_masked.
+int decode_masked_ctas_per_sm(int dtype, int head_size, int block_size, DecodeKind kind);
+cudaError_t launch_decode_masked(int dtype, int head_size, int block_size, const DecodeMaskedParams& p, DecodeKind kind,
+                                 int grid, cudaStream_t stream, int* launches);
+
 // Per-dtype entry points (decode_<dtype>.cu).
 int decode_ctas_per_sm_f32(int head_size, int block_size, DecodeKind kind);
 int decode_ctas_per_sm_f16(int head_size, int block_size, DecodeKind kind);
@@ -157,6 +171,20 @@ cudaError_t launch_decode_bf16(int head_size, int block_size, const DecodeParams
 int decode_ctas_per_sm_fp8(bool q_is_bf16, int head_size, int block_size, DecodeKind kind);
 cudaError_t launch_decode_fp8(bool q_is_bf16, int head_size, int block_size, const DecodeParams& p, DecodeKind kind,
                               int grid, cudaStream_t s, int* n);
+
+// Their capped, biased and windowed forms (decode_masked_<dtype>.cu).
+int decode_masked_ctas_per_sm_f32(int head_size, int block_size, DecodeKind kind);
+int decode_masked_ctas_per_sm_f16(int head_size, int block_size, DecodeKind kind);
+int decode_masked_ctas_per_sm_bf16(int head_size, int block_size, DecodeKind kind);
+int decode_masked_ctas_per_sm_fp8(bool q_is_bf16, int head_size, int block_size, DecodeKind kind);
+cudaError_t launch_decode_masked_f32(int head_size, int block_size, const DecodeMaskedParams& p, DecodeKind kind, int grid,
+                                     cudaStream_t s, int* n);
+cudaError_t launch_decode_masked_f16(int head_size, int block_size, const DecodeMaskedParams& p, DecodeKind kind, int grid,
+                                     cudaStream_t s, int* n);
+cudaError_t launch_decode_masked_bf16(int head_size, int block_size, const DecodeMaskedParams& p, DecodeKind kind, int grid,
+                                      cudaStream_t s, int* n);
+cudaError_t launch_decode_masked_fp8(bool q_is_bf16, int head_size, int block_size, const DecodeMaskedParams& p,
+                                     DecodeKind kind, int grid, cudaStream_t s, int* n);
 
 // Chunked prefill (prefill.cu): causal attention of a chunk of new query tokens
 // per sequence over the paged pool; 16-bit caches.
@@ -182,6 +210,44 @@ struct PrefillParams {
 };
 cudaError_t launch_prefill(int dtype, int head_size, int block_size, const PrefillParams& p, cudaStream_t stream,
                            int* launches);
+
+// pa_prefill_masked (prefill_masked.cu).
+struct PrefillMaskedParams : PrefillParams {
+  float cap_log2;                  // cap * log2(e); 0: no cap (with one, scale_log2 is 2 log2(e) scale / cap)
+  const float* slopes;             // [H]: the score of a key at distance n falls by slopes[h] n; null: no bias
+  int window;                      // a row sees the last `window` positions up to its own; 0: all
+  const int32_t* prefix_lens;      // [S]: positions below it are seen by every row; null: none
+};
+cudaError_t launch_prefill_masked(int dtype, int head_size, int block_size, const PrefillMaskedParams& p,
+                                  cudaStream_t stream, int* launches);
+
+// Rotary positions (rope.cu).
+struct RopeParams {
+  void* q_out;                  // [T, H, D]
+  void* key_out;                // [T, Hkv, D]; unused with a pool
+  const void* q;                // rows of H, Hkv and Hkv heads; *_stride: elements from one token to the next
+  const void* key;
+  const void* value;            // with a pool only
+  long long q_stride, key_stride, value_stride;
+  void* k_cache;
+  void* v_cache;
+  const int64_t* positions;     // [T]
+  const int64_t* slot_mapping;  // [T]; with a pool only
+  const double* inv_freq;       // [rotary_dim / 2]: radians per position
+  unsigned* err;
+  long long num_tokens;
+  long long num_blocks;
+  int block_size;
+  int num_heads;
+  int num_kv_heads;
+  int rotary_dim;
+  float amplitude;
+  float k_scale, v_scale;       // FP8 pools: stored code = E4M3(x / scale)
+  int tile, rows_per;           // tokens, and rows of a token, per CTA: set by launch_rope
+};
+// cache_dtype < 0: rows (key_out) instead of a pool.  head_size 64 or 128.
+cudaError_t launch_rope(int dtype, int cache_dtype, int head_size, bool pairs, RopeParams p, int sms,
+                        cudaStream_t stream, int* launches);
 
 // Write path (cache_ops.cu).
 cudaError_t launch_reshape_and_cache(const void* key, const void* value, void* k_cache, void* v_cache,

@@ -1,0 +1,302 @@
+// rope.cu -- rotary positions on rows of q and k, alone and with the write into the paged pool.
+//
+// What is computed.  A token at position p turns pair i of each head's first rotary_dim
+// dims by the angle p f_i and scales it by A:
+//     x' = A (x cos(p f_i) - y sin(p f_i)),   y' = A (x sin(p f_i) + y cos(p f_i))
+// with the pair (x, y) at dims (i, i + rotary_dim / 2) or (2 i, 2 i + 1); the dims past
+// rotary_dim are copied.  fp32 arithmetic, one rounding at the end (an FP8 code straight
+// from the fp32 value).
+//
+// The angle.  Positions are whole numbers, so the angle is taken in turns and fixed
+// point: with F_i = f_i / 2 pi as a 64-bit fraction of a turn, p F_i mod 2^64 is the
+// product's low word -- the reduction to one turn costs nothing and is exact for every
+// position, and the error is that of F_i alone, |p| 2^-65 turns (plus the rounding of f_i / 2 pi
+// beyond 2^-53 of it).  What is left after the nearest quarter turn lies within 1/8 turn, so as
+// fp32 it is off by at most 2^-28 turns, and sincospif finishes it.  (fp64 per token and pair
+// would be bound by this GPU's fp64 rate; f_i / 2 pi is computed in fp64 once per CTA.)
+//
+// Work.  A unit is two 16-byte pieces of a row: the two halves' pieces of the same pairs,
+// or two neighbouring ones.  A CTA takes `tile` tokens and `rows_per` of a token's rows (its q heads, then
+// its k heads, then its v heads), puts the cosines and sines of its tokens into shared memory, and a
+// thread turns a unit in registers: it reads both pieces before it writes either, so q may be rotated in
+// place.  Key and value units run over 16 tokens with the pieces of a pair of units innermost: the rows are
+// read in whole 32-byte sectors, and consecutive slots of a block are written in whole sectors
+// too, for K (16 bytes a token) and V (one element a token) alike.
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_launch.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTile = 16;  // tokens per CTA at most
+
+// f / 2 pi as a 64-bit fraction of a turn (whole turns drop out).  The quotient is kept as an
+// unevaluated sum hi + lo: 1 / 2 pi to twice the precision of a double.
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  constexpr double kInv2Pi = 0x1.45f306dc9c883p-3;     // 1 / 2 pi, the nearest double
+  constexpr double kInv2PiLo = -0x1.6b01ec5417056p-57;  // 1 / 2 pi - kInv2Pi
+  const double hi = f * kInv2Pi;
+  const double lo = fma(f, kInv2Pi, -hi) + f * kInv2PiLo;
+  const double frac = hi - floor(hi);  // [0, 1]; 1 only by rounding, and then it wraps to 0
+  const uint64_t a = frac >= 1.0 ? 0ull : __double2ull_rz(frac * 0x1p64);
+  return a + static_cast<uint64_t>(__double2ll_rn(lo * 0x1p64));
+}
+
+// cos and sin of `turns` 2^-64 of a turn
+__device__ __forceinline__ float2 cos_sin(uint64_t turns) {
+  const uint64_t up = turns + (1ull << 61);  // the nearest quarter turn is the two highest bits
+  const int quarter = static_cast<int>(up >> 62);
+  const int64_t rest = static_cast<int64_t>((up & ((1ull << 62) - 1))) - (1ll << 61);  // within 1/8 turn
+  float s, c;
+  sincospif(__ll2float_rn(rest) * 0x1p-63f, &s, &c);
+  const float c1 = (quarter & 1) ? s : c, s1 = (quarter & 1) ? c : s;  // a quarter turn: (-s, c)
+  return make_float2((quarter == 1 || quarter == 2) ? -c1 : c1, (quarter == 2 || quarter == 3) ? -s1 : s1);
+}
+
+// X consecutive elements of T (16 bytes) to and from fp32.
+template <typename T, int X>
+__device__ __forceinline__ void widen(const uint4& raw, float (&v)[X]) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = __uint_as_float(raw.x);
+    v[1] = __uint_as_float(raw.y);
+    v[2] = __uint_as_float(raw.z);
+    v[3] = __uint_as_float(raw.w);
+  } else {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2<T>(w[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+template <typename T, int X>
+__device__ __forceinline__ uint4 narrow(const float (&v)[X]) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  else
+    return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+}
+
+// Two E4M3 codes of a / scale and b / scale: the quotients rounded in fp32, the codes to
+// nearest even and at most 448 in size, as the write path stores them.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b, float scale) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3) &
+         0xffffu;
+}
+
+// X (8) elements as E4M3 codes, 8 bytes
+template <int X>
+__device__ __forceinline__ uint2 e4m3_codes8(const float (&v)[X], float scale) {
+  static_assert(X == 8 || X == 4, "a 16-byte piece");
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < X; i += 2) w[i / 4] |= e4m3_pair(v[i], v[i + 1], scale) << (16 * ((i / 2) & 1));
+  return make_uint2(w[0], w[1]);
+}
+
+// T: the rows' type.  TC: the pool's type; void: the turned keys go to rows (key_out) instead,
+// and there are no values.
+template <typename T, typename TC, int D, bool kPairs>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  constexpr bool kPool = !std::is_void<TC>::value;
+  constexpr int E = sizeof(T), X = 16 / E, U = D / (2 * X);  // units per row
+  __shared__ uint64_t s_turn[D / 2];
+  __shared__ __align__(16) float s_cos[kRopeTile][D / 2], s_sin[kRopeTile][D / 2];
+  __shared__ long long s_pos[kRopeTile], s_blk[kRopeTile];
+  __shared__ int s_off[kRopeTile];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, tile = p.tile, H = p.num_heads, Hkv = p.num_kv_heads;
+  const long long t0 = (long long)blockIdx.x * tile;
+  const int ntok = static_cast<int>(min((long long)tile, p.num_tokens - t0));
+  const int r2 = p.rotary_dim / 2;
+  const int rows = H + (kPool ? 2 : 1) * Hkv;  // a token's rows: q heads, k heads, v heads
+  const int row0 = blockIdx.y * p.rows_per, row1 = min(rows, row0 + p.rows_per);
+
+  if (tid < r2) s_turn[tid] = turns_of(__ldg(p.inv_freq + tid));
+  if (tid >= kRopeThreads - kRopeTile) {
+    const int j = tid - (kRopeThreads - kRopeTile);
+    if (j < ntok) {
+      s_pos[j] = __ldg(p.positions + t0 + j);
+      if constexpr (kPool) {
+        const long long slot = __ldg(p.slot_mapping + t0 + j);
+        long long blk = -1;
+        int off = 0;
+        if (slot >= p.num_blocks * p.block_size) {
+          if (blockIdx.y == 0) set_error(p.err, kErrSlot);
+        } else if (slot >= 0) {  // (negative: a padding token)
+          blk = slot / p.block_size;
+          off = static_cast<int>(slot - blk * p.block_size);
+        }
+        s_blk[j] = blk;
+        s_off[j] = off;
+      }
+    }
+  }
+  __syncthreads();
+  if (row0 < H + Hkv)  // (rows of v are not turned)
+    for (int i = tid; i < ntok * r2; i += kRopeThreads) {
+      const int j = i / r2, c = i - j * r2;
+      const float2 cs = cos_sin(static_cast<uint64_t>(s_pos[j]) * s_turn[c]);
+      s_cos[j][c] = cs.x * p.amplitude;
+      s_sin[j][c] = cs.y * p.amplitude;
+    }
+  __syncthreads();
+
+  const int rot_units = p.rotary_dim / (2 * X), half = p.rotary_dim / 2;
+  const int items = (row1 - row0) * tile * U;
+  for (int i = tid; i < items; i += kRopeThreads) {
+    int row = i / (tile * U), k = i - row * (tile * U), j, u;
+    row += row0;
+    if (row < H) {  // q: a row's units side by side
+      u = k % U;
+      j = k / U;
+    } else {        // k and v: two units, the tokens, the other units
+      const int pr = k / (2 * tile);
+      k -= pr * 2 * tile;
+      u = 2 * pr + (k & 1);
+      j = k >> 1;
+    }
+    if (j >= ntok) continue;
+    const long long t = t0 + j;
+    const bool turned = u < rot_units && row < H + Hkv;
+    // the unit's pieces: the first dims of each
+    const int d0 = !kPairs && turned ? u * X : 2 * u * X, d1 = !kPairs && turned ? d0 + half : d0 + X;
+    const T* src;
+    if (row < H) src = static_cast<const T*>(p.q) + t * p.q_stride + row * D;
+    else if (row < H + Hkv) src = static_cast<const T*>(p.key) + t * p.key_stride + (row - H) * D;
+    else src = static_cast<const T*>(p.value) + t * p.value_stride + (row - H - Hkv) * D;
+    long long blk = -1;
+    if constexpr (kPool) {
+      blk = s_blk[j];
+      if (row >= H && blk < 0) continue;  // a padding token's key and value go nowhere
+    }
+    uint4 ra = *reinterpret_cast<const uint4*>(src + d0), rb = *reinterpret_cast<const uint4*>(src + d1);
+    float a[X], b[X];
+    widen<T>(ra, a);
+    widen<T>(rb, b);
+    if (turned) {
+      // pair indices u X .. u X + X - 1 in both layouts
+#pragma unroll
+      for (int e = 0; e < X; ++e) {
+        const float c = s_cos[j][u * X + e], s = s_sin[j][u * X + e];
+        if constexpr (kPairs) {
+          float& x = e < X / 2 ? a[2 * e % X] : b[2 * e % X];
+          float& y = e < X / 2 ? a[(2 * e + 1) % X] : b[(2 * e + 1) % X];
+          const float x0 = x, y0 = y;
+          x = fmaf(x0, c, -(y0 * s));
+          y = fmaf(x0, s, y0 * c);
+        } else {
+          const float x0 = a[e], y0 = b[e];
+          a[e] = fmaf(x0, c, -(y0 * s));
+          b[e] = fmaf(x0, s, y0 * c);
+        }
+      }
+    }
+    if (row < H) {
+      T* dst = static_cast<T*>(p.q_out) + (t * H + row) * D;
+      *reinterpret_cast<uint4*>(dst + d0) = turned ? narrow<T>(a) : ra;
+      *reinterpret_cast<uint4*>(dst + d1) = turned ? narrow<T>(b) : rb;
+      continue;
+    }
+    if constexpr (!kPool) {
+      T* dst = static_cast<T*>(p.key_out) + (t * Hkv + (row - H)) * D;
+      *reinterpret_cast<uint4*>(dst + d0) = turned ? narrow<T>(a) : ra;
+      *reinterpret_cast<uint4*>(dst + d1) = turned ? narrow<T>(b) : rb;
+    } else {
+      constexpr int EC = sizeof(std::conditional_t<kPool, TC, char>), XC = 16 / EC;
+      const int bs = p.block_size, off = s_off[j];
+      if (row < H + Hkv) {  // 16-byte group g of the row -> k_cache[blk, h, g, off, :]
+        const long long base = (blk * Hkv + (row - H)) * (D / XC);
+        unsigned char* kc = static_cast<unsigned char*>(p.k_cache);
+        if constexpr (EC == 1) {
+          auto put = [&](int d, const float(&v)[X]) {
+            unsigned char* at = kc + ((base + d / XC) * bs + off) * 16 + d % XC;
+            const uint2 w = e4m3_codes8(v, p.k_scale);
+            if constexpr (X == 8) *reinterpret_cast<uint2*>(at) = w;
+            else *reinterpret_cast<uint32_t*>(at) = w.x;
+          };
+          put(d0, a);
+          put(d1, b);
+        } else {
+          *reinterpret_cast<uint4*>(kc + ((base + d0 / XC) * bs + off) * 16) = turned ? narrow<T>(a) : ra;
+          *reinterpret_cast<uint4*>(kc + ((base + d1 / XC) * bs + off) * 16) = turned ? narrow<T>(b) : rb;
+        }
+      } else {  // element d -> v_cache[blk, h, d, off]
+        const long long base = (blk * Hkv + (row - H - Hkv)) * D;
+        if constexpr (EC == 1) {
+          unsigned char* vc = static_cast<unsigned char*>(p.v_cache);
+          auto put = [&](int d, const float(&v)[X]) {
+            const uint2 w = e4m3_codes8(v, p.v_scale);
+#pragma unroll
+            for (int e = 0; e < X; ++e)
+              vc[(base + d + e) * bs + off] = static_cast<unsigned char>((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+          };
+          put(d0, a);
+          put(d1, b);
+        } else {
+          using W = std::conditional_t<E == 4, uint32_t, uint16_t>;
+          W* vc = static_cast<W*>(p.v_cache);
+          const W *ea = reinterpret_cast<const W*>(&ra), *eb = reinterpret_cast<const W*>(&rb);
+#pragma unroll
+          for (int e = 0; e < X; ++e) {
+            vc[(base + d0 + e) * bs + off] = ea[e];
+            vc[(base + d1 + e) * bs + off] = eb[e];
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T, typename TC, int D>
+cudaError_t launch_rope_d(const RopeParams& p, bool pairs, dim3 grid, cudaStream_t stream) {
+  return pairs ? launch_pdl(rope_kernel<T, TC, D, true>, grid, dim3(kRopeThreads), 0, stream, p)
+               : launch_pdl(rope_kernel<T, TC, D, false>, grid, dim3(kRopeThreads), 0, stream, p);
+}
+template <typename T, typename TC>
+cudaError_t launch_rope_t(const RopeParams& p, int head_size, bool pairs, dim3 grid, cudaStream_t stream) {
+  return head_size == 64 ? launch_rope_d<T, TC, 64>(p, pairs, grid, stream)
+                         : launch_rope_d<T, TC, 128>(p, pairs, grid, stream);
+}
+template <typename T>
+cudaError_t launch_rope_rows(const RopeParams& p, int head_size, bool pairs, int cache_dtype, dim3 grid,
+                             cudaStream_t stream) {
+  if (cache_dtype < 0) return launch_rope_t<T, void>(p, head_size, pairs, grid, stream);
+  if (cache_dtype == 3) return launch_rope_t<T, __nv_fp8_e4m3>(p, head_size, pairs, grid, stream);
+  return launch_rope_t<T, T>(p, head_size, pairs, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int dtype, int cache_dtype, int head_size, bool pairs, RopeParams p, int sms,
+                        cudaStream_t stream, int* launches) {
+  *launches = 0;
+  if (p.num_tokens == 0) return cudaSuccess;
+  const int rows = p.num_heads + (cache_dtype >= 0 ? 2 : 1) * p.num_kv_heads;
+  const int units = head_size * (dtype == 0 ? 4 : 2) / 32;  // per row
+  p.tile = kRopeTile;
+  while (p.tile > 1 && p.num_tokens * rows * units < (long long)p.tile * kRopeThreads * sms) p.tile /= 2;
+  const long long tiles = (p.num_tokens + p.tile - 1) / p.tile;
+  // rows per CTA: at least one unit a thread, more while the grid still fills the SMs
+  int per = (kRopeThreads + p.tile * units - 1) / (p.tile * units);
+  while (per < rows && tiles * ((rows + 2 * per - 1) / (2 * per)) >= 8ll * sms) per *= 2;
+  while ((rows + per - 1) / per > 65535) per *= 2;  // the grid's second extent
+  p.rows_per = per < rows ? per : rows;
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((rows + p.rows_per - 1) / p.rows_per));
+  const cudaError_t e = dtype == 0   ? launch_rope_rows<float>(p, head_size, pairs, cache_dtype, grid, stream)
+                        : dtype == 1 ? launch_rope_rows<__half>(p, head_size, pairs, cache_dtype, grid, stream)
+                                     : launch_rope_rows<__nv_bfloat16>(p, head_size, pairs, cache_dtype, grid, stream);
+  if (e == cudaSuccess) *launches = 1;
+  return e;
+}
+
+}  // namespace pa
