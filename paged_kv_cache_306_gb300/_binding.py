@@ -491,6 +491,14 @@ def pa_decode_masked(out, q, k_cache, v_cache, block_tables, seq_lens, scale, ma
     none is given, or too small a one, one is taken from torch's allocator.  Returns the
     workspace tensor used (or None).
     """
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.decode_masked(out, q, k_cache, v_cache, block_tables, seq_lens, scale, max_seq_len, softcap,
+                                 alibi_slopes, window, k_scale, v_scale, workspace, stream)
+        if st == PA_OK:
+            return workspace
+        if st > 0 and st != PA_ERR_WORKSPACE:
+            check(st)
     nb, hkv, bs = _masked_pools(q, out, k_cache, v_cache)
     _masked_tables(q, block_tables, seq_lens, alibi_slopes)
     S, H, D = q.shape
@@ -515,6 +523,12 @@ def pa_prefill_masked(out, q, k_cache, v_cache, block_tables, seq_lens, query_st
     """Chunked prefill (pa_prefill) with scores changed as in pa_decode_masked; prefix_lens
     (int32 [S], or None): the leading positions of each sequence that all of its rows see,
     those before them too."""
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.prefill_masked(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+                                  max_seq_len, softcap, alibi_slopes, window, prefix_lens, stream)
+        if st >= 0:
+            return check(st)
     import torch
     nb, hkv, bs = _masked_pools(q, out, k_cache, v_cache)
     _masked_tables(q, block_tables, seq_lens, alibi_slopes)
@@ -588,6 +602,12 @@ def pa_rope(q_out, key_out, q, key, positions, inv_freq, layout=ROPE_HALVES, amp
     """Rotary positions: q [T, H, D] and key [T, Hkv, D] (rows may lie apart, as views of one projection's)
     turned by positions (int64 [T]) times inv_freq (float64 [rotary dims / 2]) into q_out and key_out
     (contiguous; may be q and key themselves)."""
+    calls = _fp4_calls()
+    if calls is not None and key_out is not None:
+        st = calls.rope(q_out, key_out, q, key, None, None, None, positions, None, inv_freq, layout, amplitude, 1.0, 1.0,
+                        stream)
+        if st >= 0:
+            return check(st)
     sq, sk = _rope_args(q_out, q, key, positions, inv_freq)
     _need_here("key_out", key_out, q.dtype, 3)
     if key_out.shape != key.shape:
@@ -602,6 +622,12 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_ma
                       amplitude=1.0, k_scale=1.0, v_scale=1.0, stream=None):
     """pa_rope, but the turned keys go into the paged pools with the values, through slot_mapping
     (int64 [T]), as pa_reshape_and_cache_scaled writes them."""
+    calls = _fp4_calls()
+    if calls is not None:
+        st = calls.rope(q_out, None, q, key, value, k_cache, v_cache, positions, slot_mapping, inv_freq, layout,
+                        amplitude, k_scale, v_scale, stream)
+        if st >= 0:
+            return check(st)
     import torch
     sq, sk = _rope_args(q_out, q, key, positions, inv_freq)
     sv = _rope_rows("value", value, q.dtype, key.shape[1:])
@@ -643,7 +669,7 @@ def _fp4_torch():
 
 @functools.lru_cache(maxsize=None)
 def _fp4_calls():
-    """The extension that checks and marshals the FP4 calls without Python's and ctypes' share of
+    """The extension that checks and marshals the FP4, rotary and masked calls without Python's and ctypes' share of
     their time (csrc/fp4_calls.cpp), or None where it was not built.  It returns -1 for a call it
     does not take; the Python code below then takes it, or says what is wrong with it."""
     import importlib.machinery
@@ -660,7 +686,8 @@ def _fp4_calls():
     except ImportError:
         return None
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.pa_reshape_and_cache_fp4, lib.pa_gather_cache_fp4, lib.pa_expand_blocks_fp4, lib.pa_decode_fp4)))
+        lib.pa_reshape_and_cache_fp4, lib.pa_gather_cache_fp4, lib.pa_expand_blocks_fp4, lib.pa_decode_fp4,
+        lib.pa_rope, lib.pa_rope_and_cache, lib.pa_decode_masked, lib.pa_prefill_masked)))
     return m
 
 

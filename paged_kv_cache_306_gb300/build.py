@@ -5,7 +5,7 @@
 Each translation unit is compiled in parallel, then linked into
 paged_kv_cache_306_gb300/_build/libpa.so.  Rebuilds only when a source or header
 is newer than the library.  Beside it goes the CPython extension that marshals the
-FP4 calls (csrc/fp4_calls.cpp), built for the Python and torch at hand, by itself where
+FP4, rotary and masked calls (csrc/fp4_calls.cpp), built for the Python and torch at hand, by itself where
 only it is missing; without a compiler or their headers it is left out, and the binding
 takes its ctypes path.  A build that failed leaves its message beside it and is tried
 again when the library is rebuilt, or by the command above.

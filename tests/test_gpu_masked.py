@@ -326,7 +326,31 @@ def test_a_layer_as_it_is_used(pa):
             check_attention(out, ref, q, held, 0.125, 20.0, float(window), dtype, f"after {done} tokens")
 
 
-def test_binding_refusals(pa):
+@pytest.fixture(params=["extension", "ctypes"])
+def path(request, monkeypatch):
+    """Both of the binding's paths: the extension, and the Python code that takes its place."""
+    from paged_kv_cache_306_gb300 import _binding as B
+    if request.param == "extension":
+        assert B._fp4_calls() is not None, "the extension was not built"
+    else:
+        monkeypatch.setattr(B, "_fp4_calls", lambda: None)
+    return request.param
+
+
+def test_both_paths(pa, path):
+    for types in (("f16", "f16"), ("bf16", "fp8"), ("f32", "f32")):
+        decode_case(pa, [40, 77], 4, 2, 64, 16, *types, seed=25, cap=9.0, alibi=True, window=50)
+    prefill_case(pa, [40, 0], [60, 33], 4, 2, 64, 16, "bf16", seed=26, cap=9.0, alibi=True, window=50, prefixes=[70, 20])
+    pools = Pools([40, 500], 2, 64, 16, "f16", 27)
+    kc, vc, bt = pools.on("cuda")
+    q, lens = queries(2, 8, 64, "f16", 28).cuda(), torch.tensor([40, 500], dtype=torch.int32, device="cuda")
+    out = [torch.empty_like(q) for _ in range(2)]
+    ws = pa.pa_decode_masked(out[0], q, kc, vc, bt, lens, 0.125, 500, 5.0)
+    assert ws is not None and pa.pa_decode_masked(out[1], q, kc, vc, bt, lens, 0.125, 500, 5.0, workspace=ws) is ws
+    assert torch.equal(*out)
+
+
+def test_binding_refusals(pa, path):
     pools = Pools([40, 40], 2, 64, 16, "f16", 23)
     kc, vc, bt = pools.on("cuda")
     q = queries(2, 8, 64, "f16", 24).cuda()

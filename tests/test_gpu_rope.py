@@ -251,7 +251,36 @@ def test_rope_captured_and_on_another_stream(pa):
         assert torch.equal(a, b)
 
 
-def test_binding_refusals(pa):
+@pytest.fixture(params=["extension", "ctypes"])
+def path(request, monkeypatch):
+    """Both of the binding's paths: the extension, and the Python code that takes its place."""
+    from paged_kv_cache_306_gb300 import _binding as B
+    if request.param == "extension":
+        assert B._fp4_calls() is not None, "the extension was not built"
+    else:
+        monkeypatch.setattr(B, "_fp4_calls", lambda: None)
+    return request.param
+
+
+@pytest.mark.parametrize("t,h,hkv", [(1, 1, 1), (1, 4, 2), (9, 1, 1), (9, 4, 2)])
+def test_both_paths_take_rows_that_lie_apart(pa, path, t, h, hkv):
+    wide = torch.from_numpy(np.random.default_rng(3).standard_normal((t, h + 2 * hkv + 3, 64)).astype(np.float32)).cuda()
+    q, k, v = wide[:, 1:h + 1], wide[:, h + 1:h + 1 + hkv], wide[:, h + 2 + hkv:h + 2 + 2 * hkv]
+    pos, slots = torch.arange(t, device="cuda") + 7, torch.arange(t, device="cuda")
+    f = pa.pa_rope_frequencies(64)[0].cuda()
+    out = []
+    for rows3 in ((q, k, v), (q.clone(), k.contiguous(), v.contiguous())):
+        kc, vc = torch.zeros(1, hkv, 16, 16, 4, device="cuda"), torch.zeros(1, hkv, 64, 16, device="cuda")
+        qo, ko = torch.empty(t, h, 64, device="cuda"), torch.empty(t, hkv, 64, device="cuda")
+        pa.pa_rope_and_cache(qo, *rows3, kc, vc, pos, slots, f, amplitude=1.5)
+        pa.pa_rope(qo, ko, *rows3[:2], pos, f, amplitude=1.5)
+        out.append((qo, ko, kc, vc))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    check_rows(out[0][0], q, masked.rope(f64(q), np.arange(t) + 7, f.cpu().numpy(), False, 1.5), "f32", 1.5, 64, path)
+
+
+def test_binding_refusals(pa, path):
     q, k, v = rows(4, 4, 2, 64, "f16", 51, False)
     f = pa.pa_rope_frequencies(64)[0].cuda()
     pos, slots = torch.arange(4, device="cuda"), torch.arange(4, device="cuda")
