@@ -29,7 +29,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
 SOURCES = ["api.cu", "cache_ops.cu", "decode_f32.cu", "decode_f16.cu", "decode_bf16.cu", "decode_fp8.cu", "decode_noalloc.cu",
            "prefill.cu", "fp4_cache.cu", "fp4_decode.cu", "block_manager.cpp", "rope.cu", "decode_masked_f32.cu",
-           "decode_masked_f16.cu", "decode_masked_bf16.cu", "decode_masked_fp8.cu", "prefill_masked.cu"]
+           "decode_masked_f16.cu", "decode_masked_bf16.cu", "decode_masked_fp8.cu", "prefill_masked.cu", "prefill_capped.cu",
+           "prefill_biased.cu", "prefill_capped_biased.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -257,10 +257,10 @@ int windowed_len(int max_seq_len, int window, int block_size) {
 bool softcap_ok(float cap) { return cap == 0.f || (cap >= 0x1p-64f && cap <= 0x1p64f); }
 
 // The factor that brings q.k to the argument of the kernels' softmax, or, capped, of their tanh:
-// s / cap for the CUDA-core kernels, 2 log2(e) s / cap for the tensor-core ones.
-double score_factor(double scale, float softcap, bool tensor_cores) {
+// s / cap, or, for the tensor-core decode kernels, 2 log2(e) s / cap (by_exp).
+double score_factor(double scale, float softcap, bool by_exp) {
   constexpr double kLog2e = 1.4426950408889634;
-  return softcap == 0.f ? scale * kLog2e : scale / softcap * (tensor_cores ? 2 * kLog2e : 1.0);
+  return softcap == 0.f ? scale * kLog2e : scale / softcap * (by_exp ? 2 * kLog2e : 1.0);
 }
 
 // A fresh tag for every launch, so a launch never mistakes a partial slot left by
@@ -790,7 +790,7 @@ static pa_status prefill_impl(void* out, const void* q, const void* k_cache, con
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
   if (mod) {
-    p.scale_log2 = static_cast<float>(score_factor(scale, mod->softcap, true));
+    p.scale_log2 = static_cast<float>(score_factor(scale, mod->softcap, false));
     if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale / softcap is not finite");
     p.cap_log2 = static_cast<float>(mod->softcap * 1.4426950408889634);
     p.slopes = mod->slopes;

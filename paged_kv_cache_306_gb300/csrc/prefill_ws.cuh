@@ -62,8 +62,6 @@
 
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "pa_device.cuh"
 #include "pa_launch.h"
 #include "tc_ops.cuh"
@@ -80,10 +78,6 @@ using tc::ld32;
 using tc::mma;
 using tc::sdesc;
 using tc::st32;
-
-// a kernel's parameters: those of pa_prefill_masked with kMod
-template <bool kMod>
-using Params = std::conditional_t<kMod, PrefillMaskedParams, PrefillParams>;
 
 constexpr int kRows = 128;  // query rows per tile (= TMEM lanes)
 constexpr int kKeys = 128;  // keys per chunk
@@ -233,14 +227,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 1 / x by the hardware's approximate reciprocal (1 / inf = 0)
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
 // Shared-memory matrix descriptor (tcgen05), K-major with the 32-byte (mode 6) or
 // 64-byte (mode 4) swizzle: rows of 32 or 64 bytes, sbo = the distance between groups
 // of 8 rows; the leading offset is unused when one MMA's K extent fits a row.
@@ -380,34 +366,14 @@ struct Shape {
   static constexpr int kTmemCols = 512;  // tile X at 256 X: S/P 0..127, O 128..128+D
 };
 
-// pa_prefill_masked: the keys that unit `ui` of a sequence takes, from the first one its
-// first row's window reaches (lo) to the last one any of its rows sees (hi): its own
-// position's, or the prefix's.
-__device__ __forceinline__ void masked_keys(const PrefillMaskedParams& p, int s, int L, int ctx, int rows, int ui, int& lo,
-                                            int& hi) {
-  const int G = p.group;
-  const int row_hi = min(rows, (kUnitTiles * ui + kUnitTiles) * kRows);
-  const int prefix = p.prefix_lens ? min(L, __ldg(p.prefix_lens + s)) : 0;
-  hi = max(ctx + (row_hi - 1) / G, prefix - 1);
-  lo = p.window > 0 ? max(0, ctx + (kUnitTiles * ui * kRows) / G - (p.window - 1)) : 0;
-}
-
 // The figures of one unit that every role needs: the same in every role, and in both
-// CTAs of the cluster except for the pair, which is this CTA's.  Keys are counted from
-// the sequence's start; chunk c of the unit holds the kKeys keys from (c0 + c) kKeys on, and
-// no block below key lo's is looked up or read (c0 = lo = 0 without a window).
-template <bool kMod>
+// CTAs of the cluster except for the pair, which is this CTA's.
 struct UnitView {
   int s, kvh, L, tok0, pair_lo, pair_hi, ntiles, ctx, nblk, nchunks;
-  static constexpr int c0 = 0, lo = 0;
 };
-template <>
-struct UnitView<true> {
-  int s, kvh, L, tok0, pair_lo, pair_hi, ntiles, ctx, nblk, nchunks, c0, lo;
-};
-template <int BS, bool kMod>
-__device__ __forceinline__ UnitView<kMod> unit_view(const Params<kMod>& p, int4 u, uint32_t crank) {
-  UnitView<kMod> v;
+template <int BS>
+__device__ __forceinline__ UnitView unit_view(const PrefillParams& p, int4 u, uint32_t crank) {
+  UnitView v;
   v.s = u.x;
   v.kvh = u.y;
   const int G = p.group;
@@ -421,25 +387,15 @@ __device__ __forceinline__ UnitView<kMod> unit_view(const Params<kMod>& p, int4 
   // keys: what the unit's last row sees (the same in both CTAs: they share every chunk)
   const int unit_hi = min(rows, (kUnitTiles * u.z + kUnitTiles) * kRows);
   v.ctx = v.L - n;
-  if constexpr (kMod) {
-    int hi;
-    masked_keys(p, v.s, v.L, v.ctx, rows, u.z, v.lo, hi);
-    v.c0 = v.lo / kKeys;
-    v.nblk = hi / BS + 1;
-    v.nchunks = hi / kKeys + 1 - v.c0;
-  } else {
-    const int p_max = v.ctx + (unit_hi - 1) / G;  // last position any row of the unit has
-    v.nblk = p_max / BS + 1;                      // blocks holding keys 0..p_max
-    v.nchunks = (p_max + kKeys) / kKeys;
-  }
+  const int p_max = v.ctx + (unit_hi - 1) / G;  // last position any row of the unit has
+  v.nblk = p_max / BS + 1;                      // blocks holding keys 0..p_max
+  v.nchunks = (p_max + kKeys) / kKeys;
   return v;
 }
 
-// kMod (pa_prefill_masked): scores capped by a tanh and biased by distance before the
-// softmax, keys below a row's window hidden, and those of a prefix shown to every row.
-template <typename T, int D, int BS, bool kMod>
+template <typename T, int D, int BS>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_ws_kernel(const Params<kMod> p, const __grid_constant__ CUtensorMap tmap_k,
+    prefill_ws_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v) {
   using Sh = Shape<T, D, BS>;
   static_assert(Sh::kSmem > 114 * 1024, "two CTAs on one SM would contend for TMEM");
@@ -530,30 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 256 * X + lane_base;
     const uint32_t t_o = t_s + kKeys;
-    bool capped = false, biased = false;
-    if constexpr (kMod) {
-      capped = p.cap_log2 != 0.f;
-      biased = p.slopes != nullptr;
-    }
-    const float sl2 = capped || biased ? 1.f : p.scale_log2;  // modify() leaves scores in log2 units
-    // kMod: the row's scores of the keys at positions dist .. dist + kKeys - 1 relative to its own
-    auto modify = [&](float(&sv)[kKeys], int dist, float slope) {
-      if constexpr (!kMod) return;
-      else if (capped) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)); scale_log2 gives the exponent
-        const float in = p.scale_log2, cap = p.cap_log2;
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) sv[j] = fmaf(-2.f * cap, rcp(1.f + ex2(sv[j] * in)), cap);
-      }
-      if (biased) {
-        const float in = capped ? 1.f : p.scale_log2, d0 = static_cast<float>(dist);
-#pragma unroll
-        for (int j = 0; j < kKeys; ++j) sv[j] = fmaf(-slope, fabsf(d0 + j), sv[j] * in);
-      }
-    };
+    const float sl2 = p.scale_log2;
     const uint32_t sq = smem_addr(smem + X * Sh::kQTile + (r / 8) * (D / 8) * 128 + (r % 8) * 16);
     // this thread's row of Q_X for unit v into shared memory: every 16-byte piece in
     // flight at once, zeros for a padding row (completed and handed over by q_landed)
-    auto load_q = [&](const UnitView<kMod>& v) {
+    auto load_q = [&](const UnitView& v) {
       const int row = v.pair_lo + X * kRows + r;
       const bool valid = row < v.pair_hi;
       const T* q = static_cast<const T*>(p.q) +
@@ -565,7 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + c * 128), "l"(q + 8 * c), "r"(nbytes)
                      : "memory");
     };
-    auto key0 = [](const UnitView<kMod>& v, int c) { return (v.c0 + c) * kKeys; };  // a chunk's first key
     auto q_landed = [&]() {  // the Q copies done, visible to the MMAs, handed over
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -575,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int g = 0;           // chunks of all units before this one: the K/V ring positions
     int4 u;
     bool ok = take_unit(0, u);
-    UnitView<kMod> U{};
+    UnitView U{};
     if (ok && u.x >= 0) {
-      U = unit_view<BS, kMod>(p, u, crank);
+      U = unit_view<BS>(p, u, crank);
       if (U.ntiles > X) {
         load_q(U);
         q_landed();
@@ -585,11 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = 0; ok && u.x >= 0; ++k) {
       int4 un = make_int4(-1, 0, 0, 0);  // the next unit, taken during this one's last chunk
-      UnitView<kMod> N{};
+      UnitView N{};
       auto next = [&]() {
         if (!(ok = take_unit(k + 1, un))) return;
         if (un.x >= 0) {
-          N = unit_view<BS, kMod>(p, un, crank);
+          N = unit_view<BS>(p, un, crank);
           if (N.ntiles > X) load_q(N);  // Q_X is free: the last S_X of this unit is done
         }
       };
@@ -598,14 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = row < U.pair_hi;
         const int pos = valid ? U.ctx + row / G : U.ctx + (U.pair_hi - 1) / G;  // a padding row behaves as a real one
         const int kz = min(U.L, U.nblk * BS);  // first key whose V must read as zero
-        // keys from `from` to `last` are visible to the row (kMod; else up to pos)
-        int last = pos, from = 0;
-        float slope = 0.f;
-        if constexpr (kMod) {
-          if (p.prefix_lens) last = max(pos, min(U.L, __ldg(p.prefix_lens + U.s)) - 1);
-          if (p.window > 0) from = pos - (p.window - 1);
-          if (p.slopes) slope = __ldg(p.slopes + U.kvh * G + (valid ? row % G : 0)) * kLog2e;
-        }
         float m = -INFINITY, l = 0.f;
         for (int c = 0; c < U.nchunks; ++c, ++cx) {
           // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them
@@ -618,17 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float sv[kKeys];
           ld128(t_s, sv);
-          const int lim = (kMod ? last : pos) - key0(U, c);  // keys 0..lim of the chunk are visible to the row
-          if constexpr (kMod) {
-            modify(sv, key0(U, c) - pos, slope);
-            const int lo = from - key0(U, c);  // and none before this one
-            if (lo > 0) {
-#pragma unroll
-              for (int j = 0; j < kKeys; ++j)
-                if (j < lo) sv[j] = -INFINITY;
-            }
-          }
-          if (lim < kKeys - 1) {  // the diagonal chunk (or past it): hide the later keys
+          const int lim = pos - c * kKeys;  // keys 0..lim of the chunk are visible to the row
+          if (lim < kKeys - 1) {           // the diagonal chunk (or past it): hide the later keys
 #pragma unroll
             for (int j = 0; j < kKeys; ++j)
               if (j > lim) sv[j] = -INFINITY;
@@ -650,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float corr = 1.f;
           const bool move = mx > m + 8.f;
           if (move) {
-            corr = m == -INFINITY ? (kMod ? 1.f : 0.f) : exp2f(m - mx);  // (kMod: l and O are still zero)
+            corr = m == -INFINITY ? 0.f : exp2f(m - mx);
             m = mx;
             l *= corr;
           }
@@ -659,9 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           {
             // P = 2^(scale * s - m) (s = -inf gives 0): the scaling of a pair of scores and
             // the row sums in paired fp32 operations
-            // (kMod: a row whose window starts in a later chunk has seen no score yet: P is 0)
-            const float mref = kMod && m == -INFINITY ? 0.f : m;
-            const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-mref, -mref);
+            const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-m, -m);
             uint64_t ps2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
             for (int k2 = 0; k2 < kKeys / 16; ++k2) {
@@ -699,35 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               st32(t_o + c0, o);
             }
           }
-          // kMod, the first chunk: V of keys below the unit's first one reads as zero too (blocks
-          // before it are not copied)
-          if constexpr (kMod) {
-            if (X == 0 && c == 0 && U.lo > key0(U, c)) {
-              const int gc = g + c;
-              if (!(ok = __all_sync(0xffffffffu, wait(&fullv[gc % kVStages], (gc / kVStages) & 1)))) break;
-              unsigned char* vbase = smem + Sh::kOffV + (gc % kVStages) * Sh::kVBytes;
-              constexpr int kRow = 2 * BS, kUnits = kRow / 16;
-              const int k1 = U.lo - key0(U, c);  // keys 0 .. k1 - 1 of the chunk (k1 < kKeys)
-              for (int i = tid; i < (k1 + 7) / 8 * D; i += kSoftmaxThreads) {
-                const int g8 = i / D, d = i % D;  // as below
-                const int a = d * kRow + ((8 * g8) % BS) * 2;
-                unsigned char* ptr = vbase + ((8 * g8) / BS) * Sh::kTile + (a ^ (((a >> 7) & (kUnits - 1)) << 4));
-                for (int kk = 0; kk < 8 && 8 * g8 + kk < k1; ++kk)
-                  *reinterpret_cast<T*>(ptr + 2 * kk) = DType<T>::from_f32(0.f);
-              }
-              fence_proxy_async_smem();
-            }
-          }
           // the last chunk: V of keys past the sequence (or past the blocks loaded) reads as
           // zero; tile A's threads clear it before either tile's P V of the chunk is issued
-          if (X == 0 && c == U.nchunks - 1 && kz < key0(U, c) + kKeys) {
+          if (X == 0 && c == U.nchunks - 1 && kz < (c + 1) * kKeys) {
             const int gc = g + c;
             if (!(ok = __all_sync(0xffffffffu, wait(&fullv[gc % kVStages], (gc / kVStages) & 1)))) break;
             // block b's tile [D][bs]: dim d's keys 8 g .. 8 g + 7 are the 16 bytes at d * 2 bs + 16 g
             // within the row, moved by the swizzle (16-byte unit bits xor'ed with bits 7 and up)
             unsigned char* vbase = smem + Sh::kOffV + (gc % kVStages) * Sh::kVBytes;
             constexpr int kRow = 2 * BS, kUnits = kRow / 16;
-            const int k0 = kz - key0(U, c);  // first key to clear (0 <= k0 < kKeys)
+            const int k0 = kz - c * kKeys;  // first key to clear (0 <= k0 < kKeys)
             const int g0 = k0 / 8;          // the 8-key group holding it
             for (int i = tid; i < (kKeys / 8 - g0) * D; i += kSoftmaxThreads) {
               const int g8 = g0 + i / D, d = i % D;  // keys 8 g8 .. 8 g8 + 7 of dim d
@@ -800,22 +698,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k) {
       int4 u;
       if (!(ok = take_unit(k, u)) || u.x < 0) break;
-      const UnitView<kMod> U = unit_view<BS, kMod>(p, u, crank);
+      const UnitView U = unit_view<BS>(p, u, crank);
       const int32_t* bt = p.block_tables + (long long)U.s * p.max_blocks_per_seq;
       auto phys_of = [&](int c) {  // lane b: the physical block of the chunk's block b (-1 past the keys)
-        const int gb = (U.c0 + c) * Sh::kBlocks + lane;
-        return lane < Sh::kBlocks && gb < U.nblk && (!kMod || gb >= U.lo / BS) ? __ldg(bt + gb) : -1;
+        const int gb = c * Sh::kBlocks + lane;
+        return lane < Sh::kBlocks && gb < U.nblk ? __ldg(bt + gb) : -1;
       };
       int ph = phys_of(0);  // the next chunk's table entries land while a chunk is in flight
       for (int c = 0; c < U.nchunks; ++c) {
         const int gc = g + c, kb = gc % kKStages, vb = gc % kVStages;
-        const int gb0 = (U.c0 + c) * Sh::kBlocks;
-        const bool live = lane < Sh::kBlocks && gb0 + lane < U.nblk && (!kMod || gb0 + lane >= U.lo / BS);
+        const bool live = lane < Sh::kBlocks && c * Sh::kBlocks + lane < U.nblk;
         const bool bad = ph < 0 || ph >= p.num_blocks;
         if (live && bad) set_error(p.err, kErrBlockId);
-        // the first block of a chunk that holds keys: block 0, or the one a window starts in
-        const int ph0 = __shfl_sync(0xffffffffu, bad ? 0 : ph, kMod ? max(0, U.lo / BS - gb0) : 0);
-        // a block past (or before) the keys: any rows do (S there is masked; its V is not copied)
+        const int ph0 = __shfl_sync(0xffffffffu, bad ? 0 : ph, 0);  // block 0 of a chunk always holds keys
+        // a block past the keys: any rows do (S there is masked; its V is not copied)
         const long long tl = (long long)(live ? (bad ? 0 : ph) : ph0) * p.num_kv_heads + U.kvh;
         const int nlive = __popc(__ballot_sync(0xffffffffu, live));
         int rw[4];
@@ -910,16 +806,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               if (bi == cid) push(s0 + src, kvh, ff + jj);
-              int work = x;
-              if constexpr (kMod) {  // (x, what the unit would read causally, only orders the units)
-                int lo, hi;
-                masked_keys(p, s0 + src, __ldg(p.seq_lens + s0 + src), tab[s0 + src],
-                            tab[kMaxSeqsPerLaunch + s0 + src], ff + jj, lo, hi);
-                work = hi / kKeys - lo / kKeys + 1;
-              }
 #pragma unroll
               for (int i = 0; i < kLoadsPerLane; ++i)
-                if (bi == lane + 32 * i) load[i] += work + kUnitCost;
+                if (bi == lane + 32 * i) load[i] += x + kUnitCost;
             }
         }
       }
@@ -982,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k) {
       int4 u;
       if (!(ok = take_unit(k, u)) || u.x < 0) break;
-      const UnitView<kMod> U = unit_view<BS, kMod>(p, u, crank);
+      const UnitView U = unit_view<BS>(p, u, crank);
       const int nt = U.ntiles, nc = U.nchunks;
       // S of the unit's first chunk, for each tile as soon as its Q has landed (the
       // previous unit's P V run ahead of it on the tensor cores)
