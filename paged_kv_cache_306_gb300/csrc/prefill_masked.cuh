@@ -479,20 +479,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    const uint32_t sq = smem_addr(smem + X * Sh::kQTile + (r / 8) * (D / 8) * 128 + (r % 8) * 16);
-    // this thread's row of Q_X for unit v into shared memory: every 16-byte piece in
-    // flight at once, zeros for a padding row (completed and handed over by q_landed)
+    // the warp's rows of Q_X for unit v into shared memory: every 16-byte piece in flight at
+    // once, zeros for a padding row (completed and handed over by q_landed).  Four threads read 64 bytes of
+    // one row side by side, as store_rows writes them (and for the same reason: a thread on each row, the
+    // copies took ~4500 clocks to issue); eight rows of a piece are 128 bytes of shared memory.
     auto load_q = [&](const UnitView& v) {
       const int row = v.pair_lo + X * kRows + r;
-      const bool valid = row < v.pair_hi;
-      const T* q = static_cast<const T*>(p.q) +
-                   ((long long)(v.tok0 + (valid ? row / G : 0)) * p.num_heads + (long long)v.kvh * G +
-                    (valid ? row % G : 0)) * D;
-      const uint32_t nbytes = valid ? 16u : 0u;
+      const long long at = row < v.pair_hi ? (long long)(v.tok0 + row / G) * p.num_heads + (long long)v.kvh * G + row % G : -1;
+      const uint32_t sq = smem_addr(smem + X * Sh::kQTile) + (warp & 3) * (4 * (D / 8) * 128) + (lane >> 2) * 16 + (lane & 3) * 128;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + c * 128), "l"(q + 8 * c), "r"(nbytes)
-                     : "memory");
+      for (int i = 0; i < 4; ++i) {  // rows 8 i .. 8 i + 7 of the warp's
+        const long long from = __shfl_sync(0xffffffffu, at, 8 * i + (lane >> 2));
+        const T* q = static_cast<const T*>(p.q) + (from < 0 ? 0 : from) * D + (lane & 3) * 8;
+        const uint32_t nbytes = from < 0 ? 0u : 16u;
+#pragma unroll
+        for (int c = 0; c < D / 8; c += 4)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + i * (D / 8) * 128 + c * 128),
+                       "l"(q + 8 * c), "r"(nbytes)
+                       : "memory");
+      }
     };
     auto key0 = [](const UnitView& v, int c) { return (v.c0 + c) * kKeys; };  // a chunk's first key
     auto q_landed = [&]() {  // the Q copies done, visible to the MMAs, handed over
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     for (int k = 0; ok && U.s >= 0; ++k) {
-      UnitView N{};  // the next unit, taken during this one's last chunk
+      UnitView N{};  // the next unit, taken once this one's last chunk is handed over
       N.s = -1;
       auto next = [&]() {
         if (!(ok = take_unit(k + 1, N))) return;
@@ -534,10 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is taken by the whole warp, so each wait's outcome is agreed across the warp
           if (!(ok = __all_sync(0xffffffffu, wait(sfull(X), cx & 1)))) break;
           fence_after();
-          if (c == U.nchunks - 1) {
-            next();
-            if (!ok) break;
-          }
           const int lim = last - key0(U, c);  // keys 0..lim of the chunk are visible to the row
           const int lo = from - key0(U, c);  // and none before this one
           float corr = 1.f;
@@ -693,7 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(pfull(X));
         }
         if (!ok) break;
-        if (N.s >= 0 && N.ntiles > X) q_landed();  // the next unit's first S_X may go
+        next();
+        if (!ok) break;
         // the unit's output: O / l, read out of TMEM (then the columns are free for the
         // next unit's P V), rounded to T, stored as the row's D contiguous elements
         if (!(ok = __all_sync(0xffffffffu, wait(pvdone(X), ux & 1)))) break;
@@ -714,6 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_before();
         mbar_arrive(ofree(X));
+        if (N.s >= 0 && N.ntiles > X) q_landed();  // the next unit's first S_X may go
         store_rows<T, D>(o16, static_cast<T*>(p.out),
                          valid ? (long long)(U.tok0 + row / G) * p.num_heads + (long long)U.kvh * G + row % G : -1);
         ++ux;
