@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto modify = [&](float(&sv)[kKeys], int dist, float slope) {
       if constexpr (kCap) {
         const float size = fmaxf(largest(sv), -smallest(sv));
-        if (!kBias && !__any_sync(0xffffffffu, size > p.tanh_near_to)) {
+        if (!__any_sync(0xffffffffu, size > p.tanh_near_to)) {
           const uint64_t zero = f2pack(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < kKeys; j += 2) {
