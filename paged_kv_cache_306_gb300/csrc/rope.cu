@@ -16,12 +16,13 @@
 // would be bound by this GPU's fp64 rate; f_i / 2 pi is computed in fp64 once per CTA.)
 //
 // Work.  A unit is two 16-byte pieces of a row: the two halves' pieces of the same pairs,
-// or two neighbouring ones.  A CTA takes `tile` tokens and `rows_per` of a token's rows (its q heads, then
-// its k heads, then its v heads), puts the cosines and sines of its tokens into shared memory, and a
-// thread turns a unit in registers: it reads both pieces before it writes either, so q may be rotated in
-// place.  Key and value units run over 16 tokens with the pieces of a pair of units innermost: the rows are
-// read in whole 32-byte sectors, and consecutive slots of a block are written in whole sectors
-// too, for K (16 bytes a token) and V (one element a token) alike.
+// or two neighbouring ones.  A CTA takes a tile of up to 16 tokens and some of their rows (q heads, then k heads, then v
+// heads), puts the cosines and sines of its tokens into shared memory, and a thread keeps one unit and one token for
+// all rows of a kind, with that unit's cosines and sines in registers.  It reads both pieces of a unit before it writes
+// either, so q may be rotated in place.  For q a warp reads and writes whole rows; for k and v it runs over
+// 16 tokens with the pieces of a pair of units innermost: rows are read in whole 32-byte sectors, and
+// consecutive slots of a block are written in whole sectors too, for K (16 bytes a token) and V (one element a
+// token) alike.
 #include <stdint.h>
 
 #include <type_traits>
@@ -35,6 +36,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTile = 16;  // tokens per CTA at most
+constexpr int kRopeBatch = 2;  // units per thread in flight
+constexpr int kRopeCtasPerSm = 4;  // CTAs of a large launch, at least
 
 // f / 2 pi as a 64-bit fraction of a turn (whole turns drop out).  The quotient is kept as an
 // unevaluated sum hi + lo: 1 / 2 pi to twice the precision of a double.
@@ -109,13 +112,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   constexpr bool kPool = !std::is_void<TC>::value;
   constexpr int E = sizeof(T), X = 16 / E, U = D / (2 * X);  // units per row
   __shared__ uint64_t s_turn[D / 2];
-  __shared__ __align__(16) float s_cos[kRopeTile][D / 2], s_sin[kRopeTile][D / 2];
+  // (a row's length is 4 past a multiple of 32 floats, so that the threads of four tokens read other banks)
+  __shared__ __align__(16) float s_cos[kRopeTile][D / 2 + 4], s_sin[kRopeTile][D / 2 + 4];
   __shared__ long long s_pos[kRopeTile], s_blk[kRopeTile];
   __shared__ int s_off[kRopeTile];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, tile = p.tile, H = p.num_heads, Hkv = p.num_kv_heads;
-  const long long t0 = (long long)blockIdx.x * tile;
+  const int tid = threadIdx.x, tile = 1 << p.log2_tile, H = p.num_heads, Hkv = p.num_kv_heads;
+  const long long t0 = (long long)blockIdx.x << p.log2_tile;
   const int ntok = static_cast<int>(min((long long)tile, p.num_tokens - t0));
   const int r2 = p.rotary_dim / 2;
   const int rows = H + (kPool ? 2 : 1) * Hkv;  // a token's rows: q heads, k heads, v heads
@@ -151,107 +155,148 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     }
   __syncthreads();
 
-  const int rot_units = p.rotary_dim / (2 * X), half = p.rotary_dim / 2;
-  const int items = (row1 - row0) * tile * U;
-  for (int i = tid; i < items; i += kRopeThreads) {
-    int row = i / (tile * U), k = i - row * (tile * U), j, u;
-    row += row0;
-    if (row < H) {  // q: a row's units side by side
-      u = k % U;
-      j = k / U;
-    } else {        // k and v: two units, the tokens, the other units
-      const int pr = k / (2 * tile);
-      k -= pr * 2 * tile;
-      u = 2 * pr + (k & 1);
-      j = k >> 1;
-    }
-    if (j >= ntok) continue;
-    const long long t = t0 + j;
-    const bool turned = u < rot_units && row < H + Hkv;
-    // the unit's pieces: the first dims of each
-    const int d0 = !kPairs && turned ? u * X : 2 * u * X, d1 = !kPairs && turned ? d0 + half : d0 + X;
-    const T* src;
-    if (row < H) src = static_cast<const T*>(p.q) + t * p.q_stride + row * D;
-    else if (row < H + Hkv) src = static_cast<const T*>(p.key) + t * p.key_stride + (row - H) * D;
-    else src = static_cast<const T*>(p.value) + t * p.value_stride + (row - H - Hkv) * D;
-    long long blk = -1;
-    if constexpr (kPool) {
-      blk = s_blk[j];
-      if (row >= H && blk < 0) continue;  // a padding token's key and value go nowhere
-    }
-    uint4 ra = *reinterpret_cast<const uint4*>(src + d0), rb = *reinterpret_cast<const uint4*>(src + d1);
-    float a[X], b[X];
-    widen<T>(ra, a);
-    widen<T>(rb, b);
-    if (turned) {
-      // pair indices u X .. u X + X - 1 in both layouts
+  // A thread keeps its unit u and its token j for all rows of a kind, so that the cosines and sines of
+  // both stay in registers; `per` rows are under way in the CTA at once.
+  constexpr int kLog2U = U == 4 ? 2 : U == 8 ? 3 : 4;
+  static_assert(1 << kLog2U == U, "units per row");
+  const int spot = tid & ((tile << kLog2U) - 1), per = kRopeThreads >> (p.log2_tile + kLog2U);
+  const int mine = tid >> (p.log2_tile + kLog2U);
+  struct Spot {
+    int u, j, d0, d1;  // the unit, the token, and the first dims of the unit's pieces
+    bool turned;
+    float c[X], s[X];
+  };
+  auto settle = [&](int u, int j, bool turn) {
+    Spot w;
+    w.u = u;
+    w.j = j;
+    w.turned = turn && u < p.rotary_dim / (2 * X);
+    w.d0 = !kPairs && w.turned ? u * X : 2 * u * X;
+    w.d1 = !kPairs && w.turned ? w.d0 + r2 : w.d0 + X;
+    if (w.turned) {  // pair indices u X .. u X + X - 1 in both layouts
 #pragma unroll
-      for (int e = 0; e < X; ++e) {
-        const float c = s_cos[j][u * X + e], s = s_sin[j][u * X + e];
-        if constexpr (kPairs) {
-          float& x = e < X / 2 ? a[2 * e % X] : b[2 * e % X];
-          float& y = e < X / 2 ? a[(2 * e + 1) % X] : b[(2 * e + 1) % X];
-          const float x0 = x, y0 = y;
-          x = fmaf(x0, c, -(y0 * s));
-          y = fmaf(x0, s, y0 * c);
-        } else {
-          const float x0 = a[e], y0 = b[e];
-          a[e] = fmaf(x0, c, -(y0 * s));
-          b[e] = fmaf(x0, s, y0 * c);
-        }
+      for (int e = 0; e < X; e += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(&s_cos[j][u * X + e]);
+        const float4 v = *reinterpret_cast<const float4*>(&s_sin[j][u * X + e]);
+        w.c[e] = c.x, w.c[e + 1] = c.y, w.c[e + 2] = c.z, w.c[e + 3] = c.w;
+        w.s[e] = v.x, w.s[e + 1] = v.y, w.s[e + 2] = v.z, w.s[e + 3] = v.w;
       }
     }
-    if (row < H) {
-      T* dst = static_cast<T*>(p.q_out) + (t * H + row) * D;
-      *reinterpret_cast<uint4*>(dst + d0) = turned ? narrow<T>(a) : ra;
-      *reinterpret_cast<uint4*>(dst + d1) = turned ? narrow<T>(b) : rb;
-      continue;
+    return w;
+  };
+  auto turn = [&](const Spot& w, uint4& ra, uint4& rb, float(&a)[X], float(&b)[X]) {
+    widen<T>(ra, a);
+    widen<T>(rb, b);
+    if (!w.turned) return;
+#pragma unroll
+    for (int e = 0; e < X; ++e) {
+      float& x = kPairs ? (e < X / 2 ? a[2 * e % X] : b[2 * e % X]) : a[e];
+      float& y = kPairs ? (e < X / 2 ? a[(2 * e + 1) % X] : b[(2 * e + 1) % X]) : b[e];
+      const float x0 = x, y0 = y;
+      x = fmaf(x0, w.c[e], -(y0 * w.s[e]));
+      y = fmaf(x0, w.s[e], y0 * w.c[e]);
     }
-    if constexpr (!kPool) {
-      T* dst = static_cast<T*>(p.key_out) + (t * Hkv + (row - H)) * D;
-      *reinterpret_cast<uint4*>(dst + d0) = turned ? narrow<T>(a) : ra;
-      *reinterpret_cast<uint4*>(dst + d1) = turned ? narrow<T>(b) : rb;
-    } else {
-      constexpr int EC = sizeof(std::conditional_t<kPool, TC, char>), XC = 16 / EC;
-      const int bs = p.block_size, off = s_off[j];
-      if (row < H + Hkv) {  // 16-byte group g of the row -> k_cache[blk, h, g, off, :]
-        const long long base = (blk * Hkv + (row - H)) * (D / XC);
+    ra = narrow<T>(a);
+    rb = narrow<T>(b);
+  };
+  // rows first .. last - 1 of a kind, from src (the token's row 0 of the kind) to put(row, pieces): kRopeBatch
+  // rows' loads are on their way together
+  auto walk = [&](const Spot& w, const T* src, int first, int last, auto put) {
+    for (int row = first + mine; row < last; row += kRopeBatch * per) {
+      uint4 ra[kRopeBatch], rb[kRopeBatch];
+#pragma unroll
+      for (int b = 0; b < kRopeBatch; ++b)
+        if (row + b * per < last) {
+          ra[b] = *reinterpret_cast<const uint4*>(src + (row + b * per) * D + w.d0);
+          rb[b] = *reinterpret_cast<const uint4*>(src + (row + b * per) * D + w.d1);
+        }
+#pragma unroll
+      for (int b = 0; b < kRopeBatch; ++b)
+        if (row + b * per < last) {
+          float x[X], y[X];
+          turn(w, ra[b], rb[b], x, y);
+          put(row + b * per, ra[b], rb[b], x, y);
+        }
+    }
+  };
+
+  // q (and k as rows): a row's units side by side
+  auto to_rows = [&](const void* src, long long stride, void* dst, int heads, int first, int last) {
+    const Spot w = settle(spot & (U - 1), spot >> kLog2U, true);
+    if (w.j >= ntok) return;
+    const long long t = t0 + w.j;
+    T* out = static_cast<T*>(dst) + t * heads * D;
+    walk(w, static_cast<const T*>(src) + t * stride, first, last,
+         [&](int row, const uint4& ra, const uint4& rb, const float(&)[X], const float(&)[X]) {
+           *reinterpret_cast<uint4*>(out + row * D + w.d0) = ra;
+           *reinterpret_cast<uint4*>(out + row * D + w.d1) = rb;
+         });
+  };
+  if (row0 < H) to_rows(p.q, p.q_stride, p.q_out, H, row0, min(row1, H));
+  if constexpr (!kPool) {
+    if (row1 > H) to_rows(p.key, p.key_stride, p.key_out, Hkv, max(row0, H) - H, row1 - H);
+  } else {
+    constexpr int EC = sizeof(TC), XC = 16 / EC;
+    const int bs = p.block_size;
+    // k and v: two units, the tokens, the other units
+    const int pr = spot >> (p.log2_tile + 1), k = spot & ((2 << p.log2_tile) - 1);
+    if (row1 > H && row0 < H + Hkv) {
+      const Spot w = settle(2 * pr + (k & 1), k >> 1, true);
+      const long long t = t0 + w.j, blk = w.j < ntok ? s_blk[w.j] : -1;
+      if (blk >= 0) {  // (a padding token's key goes nowhere)
+        const int off = s_off[w.j];
         unsigned char* kc = static_cast<unsigned char*>(p.k_cache);
-        if constexpr (EC == 1) {
-          auto put = [&](int d, const float(&v)[X]) {
-            unsigned char* at = kc + ((base + d / XC) * bs + off) * 16 + d % XC;
-            const uint2 w = e4m3_codes8(v, p.k_scale);
-            if constexpr (X == 8) *reinterpret_cast<uint2*>(at) = w;
-            else *reinterpret_cast<uint32_t*>(at) = w.x;
-          };
-          put(d0, a);
-          put(d1, b);
-        } else {
-          *reinterpret_cast<uint4*>(kc + ((base + d0 / XC) * bs + off) * 16) = turned ? narrow<T>(a) : ra;
-          *reinterpret_cast<uint4*>(kc + ((base + d1 / XC) * bs + off) * 16) = turned ? narrow<T>(b) : rb;
-        }
-      } else {  // element d -> v_cache[blk, h, d, off]
-        const long long base = (blk * Hkv + (row - H - Hkv)) * D;
-        if constexpr (EC == 1) {
-          unsigned char* vc = static_cast<unsigned char*>(p.v_cache);
-          auto put = [&](int d, const float(&v)[X]) {
-            const uint2 w = e4m3_codes8(v, p.v_scale);
+        walk(w, static_cast<const T*>(p.key) + t * p.key_stride, max(row0, H) - H, min(row1, H + Hkv) - H,
+             [&](int h, const uint4& ra, const uint4& rb, const float(&x)[X], const float(&y)[X]) {
+               // 16-byte group g of the row -> k_cache[blk, h, g, off, :]
+               const long long base = (blk * Hkv + h) * (D / XC);
+               if constexpr (EC == 1) {
+                 auto put = [&](int d, const float(&v)[X]) {
+                   unsigned char* at = kc + ((base + d / XC) * bs + off) * 16 + d % XC;
+                   const uint2 codes = e4m3_codes8(v, p.k_scale);
+                   if constexpr (X == 8) *reinterpret_cast<uint2*>(at) = codes;
+                   else *reinterpret_cast<uint32_t*>(at) = codes.x;
+                 };
+                 put(w.d0, x);
+                 put(w.d1, y);
+               } else {
+                 *reinterpret_cast<uint4*>(kc + ((base + w.d0 / XC) * bs + off) * 16) = ra;
+                 *reinterpret_cast<uint4*>(kc + ((base + w.d1 / XC) * bs + off) * 16) = rb;
+               }
+             });
+      }
+    }
+    if (row1 > H + Hkv) {
+      const Spot w = settle(2 * pr + (k & 1), k >> 1, false);
+      const long long t = t0 + w.j, blk = w.j < ntok ? s_blk[w.j] : -1;
+      if (blk >= 0) {
+        const int off = s_off[w.j];
+        walk(w, static_cast<const T*>(p.value) + t * p.value_stride, max(row0, H + Hkv) - H - Hkv, row1 - H - Hkv,
+             [&](int h, const uint4& ra, const uint4& rb, const float(&x)[X], const float(&y)[X]) {
+               // element d -> v_cache[blk, h, d, off]
+               const long long base = (blk * Hkv + h) * D;
+               if constexpr (EC == 1) {
+                 unsigned char* vc = static_cast<unsigned char*>(p.v_cache);
+                 auto put = [&](int d, const float(&v)[X]) {
+                   const uint2 codes = e4m3_codes8(v, p.v_scale);
 #pragma unroll
-            for (int e = 0; e < X; ++e)
-              vc[(base + d + e) * bs + off] = static_cast<unsigned char>((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
-          };
-          put(d0, a);
-          put(d1, b);
-        } else {
-          using W = std::conditional_t<E == 4, uint32_t, uint16_t>;
-          W* vc = static_cast<W*>(p.v_cache);
-          const W *ea = reinterpret_cast<const W*>(&ra), *eb = reinterpret_cast<const W*>(&rb);
+                   for (int e = 0; e < X; ++e)
+                     vc[(base + d + e) * bs + off] =
+                         static_cast<unsigned char>((e < 4 ? codes.x : codes.y) >> (8 * (e & 3)));
+                 };
+                 put(w.d0, x);
+                 put(w.d1, y);
+               } else {
+                 using W = std::conditional_t<E == 4, uint32_t, uint16_t>;
+                 W* vc = static_cast<W*>(p.v_cache);
+                 const W *ea = reinterpret_cast<const W*>(&ra), *eb = reinterpret_cast<const W*>(&rb);
 #pragma unroll
-          for (int e = 0; e < X; ++e) {
-            vc[(base + d0 + e) * bs + off] = ea[e];
-            vc[(base + d1 + e) * bs + off] = eb[e];
-          }
-        }
+                 for (int e = 0; e < X; ++e) {
+                   vc[(base + w.d0 + e) * bs + off] = ea[e];
+                   vc[(base + w.d1 + e) * bs + off] = eb[e];
+                 }
+               }
+             });
       }
     }
   }
@@ -283,15 +328,18 @@ cudaError_t launch_rope(int dtype, int cache_dtype, int head_size, bool pairs, R
   if (p.num_tokens == 0) return cudaSuccess;
   const int rows = p.num_heads + (cache_dtype >= 0 ? 2 : 1) * p.num_kv_heads;
   const int units = head_size * (dtype == 0 ? 4 : 2) / 32;  // per row
-  p.tile = kRopeTile;
-  while (p.tile > 1 && p.num_tokens * rows * units < (long long)p.tile * kRopeThreads * sms) p.tile /= 2;
-  const long long tiles = (p.num_tokens + p.tile - 1) / p.tile;
+  int tile = kRopeTile;
+  while (tile > 1 && p.num_tokens * rows * units < (long long)tile * kRopeThreads * sms) tile /= 2;
+  p.log2_tile = 0;
+  while (1 << p.log2_tile < tile) ++p.log2_tile;
+  const long long tiles = (p.num_tokens + tile - 1) / tile;
   // rows per CTA: at least one unit a thread, more while the grid still fills the SMs
-  int per = (kRopeThreads + p.tile * units - 1) / (p.tile * units);
-  while (per < rows && tiles * ((rows + 2 * per - 1) / (2 * per)) >= 8ll * sms) per *= 2;
+  int per = (kRopeThreads + tile * units - 1) / (tile * units);
+  while (per < rows && tiles * ((rows + 2 * per - 1) / (2 * per)) >= kRopeCtasPerSm * (long long)sms) per *= 2;
   while ((rows + per - 1) / per > 65535) per *= 2;  // the grid's second extent
-  p.rows_per = per < rows ? per : rows;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>((rows + p.rows_per - 1) / p.rows_per));
+  const int parts = (rows + per - 1) / per;
+  p.rows_per = (rows + parts - 1) / parts;  // (equal shares)
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
   const cudaError_t e = dtype == 0   ? launch_rope_rows<float>(p, head_size, pairs, cache_dtype, grid, stream)
                         : dtype == 1 ? launch_rope_rows<__half>(p, head_size, pairs, cache_dtype, grid, stream)
                                      : launch_rope_rows<__nv_bfloat16>(p, head_size, pairs, cache_dtype, grid, stream);
