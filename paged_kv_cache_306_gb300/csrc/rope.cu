@@ -88,20 +88,29 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[X]) {
     return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
 
-// Two E4M3 codes of a / scale and b / scale: the quotients rounded in fp32, the codes to
-// nearest even and at most 448 in size, as the write path stores them.
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b, float scale) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)), __NV_SATFINITE, __NV_E4M3) &
-         0xffffu;
+// x / scale, correctly rounded where an E4M3 code can tell: the product with the rounded
+// reciprocal, corrected once by its remainder (P. Markstein's division by a rounded reciprocal; exact for the
+// quotients in [2^-12, 1024) and scales in [2^-64, 2^64]).  Other quotients keep the product: smaller ones
+// become zero (of their sign) in any case, larger ones, infinities and NaN saturate as they do.  inv == 0: a scale outside that range, divided.
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+  if (inv == 0.f) return __fdiv_rn(x, scale);
+  const float q = x * inv;
+  const float c = fmaf(fmaf(-q, scale, x), inv, q);
+  constexpr uint32_t kLo = 0x39800000u, kHi = 0x44800000u;  // the bits of 2^-12 and 1024
+  return (__float_as_uint(q) & 0x7fffffffu) - kLo < kHi - kLo ? c : q;
 }
 
-// X (8) elements as E4M3 codes, 8 bytes
+// X elements as E4M3 codes of x / scale, to nearest even and at most 448 in size, as the write
+// path stores them (the first X bytes).
 template <int X>
-__device__ __forceinline__ uint2 e4m3_codes8(const float (&v)[X], float scale) {
+__device__ __forceinline__ uint2 e4m3_codes8(const float (&v)[X], float scale, float inv) {
   static_assert(X == 8 || X == 4, "a 16-byte piece");
   uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < X; i += 2) w[i / 4] |= e4m3_pair(v[i], v[i + 1], scale) << (16 * ((i / 2) & 1));
+  for (int i = 0; i < X; i += 2) {
+    const float2 q = make_float2(quotient(v[i], scale, inv), quotient(v[i + 1], scale, inv));
+    w[i / 4] |= (__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) & 0xffffu) << (16 * ((i / 2) & 1));
+  }
   return make_uint2(w[0], w[1]);
 }
 
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                if constexpr (EC == 1) {
                  auto put = [&](int d, const float(&v)[X]) {
                    unsigned char* at = kc + ((base + d / XC) * bs + off) * 16 + d % XC;
-                   const uint2 codes = e4m3_codes8(v, p.k_scale);
+                   const uint2 codes = e4m3_codes8(v, p.k_scale, p.k_inv);
                    if constexpr (X == 8) *reinterpret_cast<uint2*>(at) = codes;
                    else *reinterpret_cast<uint32_t*>(at) = codes.x;
                  };
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                if constexpr (EC == 1) {
                  unsigned char* vc = static_cast<unsigned char*>(p.v_cache);
                  auto put = [&](int d, const float(&v)[X]) {
-                   const uint2 codes = e4m3_codes8(v, p.v_scale);
+                   const uint2 codes = e4m3_codes8(v, p.v_scale, p.v_inv);
 #pragma unroll
                    for (int e = 0; e < X; ++e)
                      vc[(base + d + e) * bs + off] =
@@ -328,6 +337,9 @@ cudaError_t launch_rope(int dtype, int cache_dtype, int head_size, bool pairs, R
   if (p.num_tokens == 0) return cudaSuccess;
   const int rows = p.num_heads + (cache_dtype >= 0 ? 2 : 1) * p.num_kv_heads;
   const int units = head_size * (dtype == 0 ? 4 : 2) / 32;  // per row
+  auto inverse = [](float scale) { return scale >= 0x1p-64f && scale <= 0x1p64f ? 1.f / scale : 0.f; };
+  p.k_inv = inverse(p.k_scale);
+  p.v_inv = inverse(p.v_scale);
   int tile = kRopeTile;
   while (tile > 1 && p.num_tokens * rows * units < (long long)tile * kRopeThreads * sms) tile /= 2;
   p.log2_tile = 0;

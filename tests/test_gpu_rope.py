@@ -301,3 +301,32 @@ def test_binding_refusals(pa, path):
             pa.pa_rope_and_cache(**{**good, **b})
     with pytest.raises(pa.PAError):
         pa.pa_rope(qo, torch.empty_like(k)[:3], q, k, pos, f)
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.0173, 3.7e-5, 1234.567, 2.0 ** -70, 3.1e25, 1e-30])
+def test_codes_of_any_value_and_scale(pa, scale):
+    """Values over all magnitudes, borders between codes, infinities and NaN: the codes that the write path stores."""
+    t, d = 64, 64
+    rng = np.random.default_rng(7)
+    x = (rng.standard_normal(t * d) * 2.0 ** rng.integers(-14, 12, t * d)).astype(np.float32)
+    grid = np.array([m / 512 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7) for e in range(16) for m in range(8)][:127])
+    border = (grid[1:] + grid[:-1]) / 2
+    near = np.concatenate([border, border * (1 + 2.0 ** -23), border * (1 - 2.0 ** -23), [448, 480, 464, 1e5, 0.0]])
+    x[:len(near)] = near
+    with np.errstate(over="ignore", under="ignore"):
+        x = (x.astype(np.float64) * np.float64(np.float32(scale))).astype(np.float32)
+    x[-8:] = [np.inf, -np.inf, np.nan, 3.4e38, -3.4e38, 1e-45, -1e-45, -0.0]
+    v = torch.from_numpy(x.reshape(t, 1, d)).cuda()
+    q = torch.zeros(t, 1, d, device="cuda")
+    pools = [torch.zeros(4, 1, d // 16, 16, 16, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+    vpools = [torch.zeros(4, 1, d, 16, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+    slots, pos = torch.arange(t, device="cuda"), torch.zeros(t, dtype=torch.int64, device="cuda")
+    f = pa.pa_rope_frequencies(16)[0].cuda()
+    # position 0 turns nothing: x cos - y sin = x (an infinite or NaN partner apart, so k's turned dims are zero)
+    k = v.clone()
+    k[..., :16] = 0
+    pa.pa_rope_and_cache(q, q, k, v, pools[0], vpools[0], pos, slots, f, k_scale=scale, v_scale=scale)
+    pa.pa_reshape_and_cache_scaled(k, v, pools[1], vpools[1], slots, scale, scale)
+    assert pa.pa_get_device_error() == 0
+    for a, b in ((pools[0], pools[1]), (vpools[0], vpools[1])):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
