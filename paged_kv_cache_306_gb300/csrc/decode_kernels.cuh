@@ -1023,6 +1023,55 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
   __syncthreads();  // s_pre and s_red are rewritten by the prefix sums that follow
 }
 
+// The merge of a launch of one CTA (kMod), by that CTA's warps once all their pieces are there: a
+// warp per output row, with the formula of the merge kernel below, over the at most `warps` pieces of
+// the row's segment.  (A launch that small is all latency: one short sequence takes 6.4 us with the merge as a kernel of
+// its own and MERGE_US with it here.)
+template <typename T, int D, bool kMma>
+__device__ __forceinline__ void merge_here(const DecodeParams& p, int warp, int warps, int lane) {
+  constexpr int CPL = D / 32;  // head dims per lane
+  asm volatile("bar.sync 0;" ::: "memory");  // warps come here from two places
+  for (int row = warp; row < p.num_seqs * p.num_heads; row += warps) {
+    const int s = row / p.num_heads, h = row - s * p.num_heads;
+    int u = h, r = 0;  // the head unit of h and h's row within it
+    if (kMma) {
+      const int kvh = h / p.group, hh = h - kvh * p.group;
+      u = kvh * ((p.group + 15) >> 4) + (hh >> 4);
+      r = hh & 15;
+    }
+    const int seg = s * p.units + u, first = p.seg_first[seg];
+    if (first < 0) continue;  // straight to the output
+    const int n = p.seg_last[seg] - first + 1;
+    if (n < 1 || n > 32) continue;  // (an aborted launch)
+    float m = -INFINITY, l = 0.f;
+    if (lane < n) {
+      const int2 tag = p.part_tag[first + lane];
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + ((long long)(first + lane) * p.rows + r) * 2);
+      if (tag.x == seg && tag.y == static_cast<int>(p.epoch)) {
+        m = ml.x;
+        l = ml.y;
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float w = m == -INFINITY ? 0.f : l * exp2f(m - top);
+    float sum = w, acc[CPL] = {};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (!(wi != 0.f)) continue;  // a slot that no piece wrote holds anything (a NaN weight is a row's own)
+      const float* o = p.part_o + ((long long)(first + i) * p.rows + r) * D + CPL * lane;
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) acc[c] = fmaf(wi, o[c], acc[c]);
+    }
+    T* out = static_cast<T*>(p.out) + (long long)row * D + CPL * lane;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) out[c] = DType<T>::from_f32(acc[c] / sum);
+  }
+}
+
 // The kernel's parameters: those of pa_decode_masked with kMod.
 template <bool kMod>
 using DecodeArgs = std::conditional_t<kMod, DecodeMaskedParams, DecodeParams>;
@@ -1292,6 +1341,8 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       p.part_tag[(long long)w + seg_id(s, u, shared && j < shared_len(s) ? 0 : 1)] = make_int2(-1, 0);
     }
     if (fused) write_tokens();
+    if constexpr (kMod)
+      if (gridDim.x == 1) merge_here<T, D, kMma>(p, warp, kDecodeWarps, lane);
     return;
   }
 
@@ -1499,6 +1550,8 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       }
     }
   }
+  if constexpr (kMod)
+    if (gridDim.x == 1) merge_here<T, D, kMma>(p, warp, kDecodeWarps, lane);
 }
 
 // --- merge of pieces --------------------------------------------------------------------------------
@@ -1721,6 +1774,7 @@ cudaError_t launch_decode_t(const DecodeArgs<kMod>& p, int grid, cudaStream_t st
                  decode_smem_bytes<TC, D, BS, kMode>(), stream, p);
   if (e != cudaSuccess) return e;
   *launches = 1;
+  if (kMod && grid == 1) return cudaSuccess;  // (see merge_here)
   // rows whose segments average 16 pieces or more (a few very long sequences) take a CTA each
   const long long rows = (long long)p.num_seqs * p.num_heads;
   const long long segs = (long long)p.num_seqs * p.units;

@@ -105,6 +105,39 @@ def test_decode_unchanged_scores_equal_pa_decode(pa):
         check_attention(out, ref, q, pools, 0.09, dtype=dtype)
 
 
+@pytest.mark.parametrize("types", TYPES, ids=lambda t: "/".join(t))
+def test_decode_of_few_blocks(pa, types):
+    """Launches of one CTA, which merges its pieces itself: one sequence of every length around a block's, and
+    batches of short ones with a few warps' work or less."""
+    for d, bs in ((64, 16), (128, 32)):
+        for n in (1, 2, bs - 1, bs, bs + 1, 3 * bs + 5, 100):
+            decode_case(pa, [n], 4, 1, d, bs, *types, seed=n + d, cap=12.0, window=40)
+        decode_case(pa, [1, 5, 17, 2, 33], 1, 1, d, bs, *types, seed=31, alibi=True)
+        decode_case(pa, [60, 3], 20, 1, d, bs, *types, seed=32, cap=4.0)
+        decode_case(pa, [100], 8, 2, d, bs, *types, seed=33)
+
+
+def test_decode_of_few_blocks_replayed(pa):
+    """A captured launch of one CTA over other lengths: warps without work leave no piece behind."""
+    pools = Pools([120], 1, 64, 16, "f16", 34)
+    kc, vc, bt = pools.on("cuda")
+    q = queries(1, 4, 64, "f16", 35).cuda()
+    lens, out = torch.tensor([120], dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    ws = pa.pa_decode_masked(out, q, kc, vc, bt, lens, 0.125, 120, softcap=6.0)
+    n0 = pa.pa_launch_count()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_decode_masked(out, q, kc, vc, bt, lens, 0.125, 120, softcap=6.0, workspace=ws)
+    assert pa.pa_launch_count() == n0 + 1
+    for n in (120, 16, 1, 97, 33, 120):
+        lens.fill_(n)
+        out.fill_(99.0)
+        graph.replay()
+        ref = masked.decode(f64(q), *pools.exact(), pools.table, [n], 0.125, 16, softcap=6.0)
+        check_attention(out, ref, q, pools, 0.125, 6.0)
+    assert pa.pa_get_device_error() == 0
+
+
 def test_decode_many_sequences(pa):
     """More sequences than one launch takes."""
     lens = [(37 * i) % 70 + 1 for i in range(1100)]
