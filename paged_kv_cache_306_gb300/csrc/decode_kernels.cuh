@@ -51,6 +51,7 @@
 //     while the decode kernel finishes.
 #pragma once
 
+#include <limits.h>
 #include <math.h>
 
 #include <type_traits>
@@ -899,7 +900,9 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, int& kv
 // Segment and block of global work position g (g < T): the sequence s with
 // units * pre[s] <= g < units * pre[s + 1] (empty sequences are skipped because
 // their prefix equals the next one's), then the unit and the block within it.
-__device__ __forceinline__ void locate(long long g, const int* pre, int S, int U, int& s, int& u, int& j) {
+// small: all positions fit 31 bits (a 64-bit division takes ~300 clocks).
+__device__ __forceinline__ void locate(long long g, const int* pre, int S, int U, int& s, int& u, int& j,
+                                       bool small = false) {
   int lo = 0, hi = S - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -909,6 +912,11 @@ __device__ __forceinline__ void locate(long long g, const int* pre, int S, int U
   s = lo;
   const int nb = pre[s + 1] - pre[s];
   const long long r = g - (long long)pre[s] * U;
+  if (small) {
+    u = static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(nb));
+    j = static_cast<int>(r) - u * nb;
+    return;
+  }
   u = static_cast<int>(r / nb);
   j = static_cast<int>(r - (long long)u * nb);
 }
@@ -1024,11 +1032,15 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
 }
 
 // The merge of a launch of one CTA (kMod), by that CTA's warps once all their pieces are there: a
-// warp per output row, with the formula of the merge kernel below, over the at most `warps` pieces of
-// the row's segment.  (A launch that small is all latency: one short sequence takes 6.4 us with the merge as a kernel of
-// its own and MERGE_US with it here.)
-template <typename T, int D, bool kMma>
-__device__ __forceinline__ void merge_here(const DecodeParams& p, int warp, int warps, int lane) {
+// warp per output row, with the formula of the merge kernel below.  The pieces never leave shared memory: a warp has at
+// most two that do not hold their whole segment, its first and its last; the last one (or the only one) lies in the
+// warp's ring, whose copies have all been used by then, the other where caller partitions would keep
+// their running state (there are none).  s_piece[2 w], s_piece[2 w + 1]: the segments of warp w's pieces in the state
+// and in the ring, -1: none.  (A launch that small is all latency: one short sequence took 6.4 us with the merge as a
+// kernel of its own, MERGE_US with it here.)
+template <typename T, int D, bool kMma, int kRows>
+__device__ __forceinline__ void merge_here(const DecodeParams& p, const int* s_piece, const float* states, const unsigned char* rings,
+                                           int ring_bytes, int warp, int warps, int lane) {
   constexpr int CPL = D / 32;  // head dims per lane
   asm volatile("bar.sync 0;" ::: "memory");  // warps come here from two places
   for (int row = warp; row < p.num_seqs * p.num_heads; row += warps) {
@@ -1039,32 +1051,38 @@ __device__ __forceinline__ void merge_here(const DecodeParams& p, int warp, int 
       u = kvh * ((p.group + 15) >> 4) + (hh >> 4);
       r = hh & 15;
     }
-    const int seg = s * p.units + u, first = p.seg_first[seg];
-    if (first < 0) continue;  // straight to the output
-    const int n = p.seg_last[seg] - first + 1;
-    if (n < 1 || n > 32) continue;  // (an aborted launch)
+    const int seg = s * p.units + u;
+    const float* o = nullptr;  // lane i: warp i's piece of the segment
     float m = -INFINITY, l = 0.f;
-    if (lane < n) {
-      const int2 tag = p.part_tag[first + lane];
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + ((long long)(first + lane) * p.rows + r) * 2);
-      if (tag.x == seg && tag.y == static_cast<int>(p.epoch)) {
-        m = ml.x;
-        l = ml.y;
+    if (lane < warps) {
+      if (s_piece[2 * lane] == seg) o = states + lane * kRows * (D + 2);
+      if (s_piece[2 * lane + 1] == seg) o = reinterpret_cast<const float*>(rings + lane * ring_bytes);
+      if (o) {
+        m = o[kRows * D + 2 * r];
+        l = o[kRows * D + 2 * r + 1];
       }
     }
+    const unsigned have = __ballot_sync(0xffffffffu, o != nullptr);
+    if (have == 0) continue;  // straight to the output
     float top = m;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int k = 1; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
     const float w = m == -INFINITY ? 0.f : l * exp2f(m - top);
     float sum = w, acc[CPL] = {};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    for (int i = 0; i < n; ++i) {
+    for (int k = 1; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    const uint32_t at = o ? smem_addr(o) : 0;
+    for (unsigned left = have; left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (!(wi != 0.f)) continue;  // a slot that no piece wrote holds anything (a NaN weight is a row's own)
-      const float* o = p.part_o + ((long long)(first + i) * p.rows + r) * D + CPL * lane;
+      const uint32_t from = __shfl_sync(0xffffffffu, at, i) + (r * D + CPL * lane) * 4;
 #pragma unroll
-      for (int c = 0; c < CPL; ++c) acc[c] = fmaf(wi, o[c], acc[c]);
+      for (int c = 0; c < CPL; c += 2) {
+        float x, y;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(from + 4 * c));
+        acc[c] = fmaf(wi, x, acc[c]);
+        acc[c + 1] = fmaf(wi, y, acc[c + 1]);
+      }
     }
     T* out = static_cast<T*>(p.out) + (long long)row * D + CPL * lane;
 #pragma unroll
@@ -1112,6 +1130,14 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   float* st_o = reinterpret_cast<float*>(smem + Sh::kRingBytes + Sh::kBarBytes + Sh::kTableBytes) +
                 kDecodeWarps * BS + warp * kRows * (D + 2);
   float* st_ml = st_o + kRows * D;
+  // kMod, a launch of one CTA: its pieces are merged here (see merge_here)
+  const bool alone = kMod && gridDim.x == 1;
+  int* s_piece = s_info;  // (no shared prefixes with kMod)
+  static_assert(!kMod || kRows * (D + 2) * 4 <= STAGES * 2 * TILE, "a piece in its warp's ring");
+  if (alone && lane < 2) s_piece[2 * warp + lane] = -1;
+  auto merge = [&]() {
+    merge_here<T, D, kMma, kRows>(p, s_piece, st_o - warp * kRows * (D + 2), smem, STAGES * 2 * TILE, warp, kDecodeWarps, lane);
+  };
 
   if (lane == 0) {
     for (int st = 0; st < STAGES; ++st) mbar_init(&bars[st], 1);
@@ -1306,6 +1332,10 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   long long start, end;
   {
     const long long Tw = (long long)s_wpre[S] * U;
+    const bool small = kMod && Tw <= INT_MAX;  // 32-bit divisions (see locate)
+    auto div = [&](long long a, int b) -> long long {
+      return small ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+    };
     // the first block whose cost starts at or after t
     auto block_at = [&](long long t) -> long long {
       if (t >= Tw) return T_all;
@@ -1317,7 +1347,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       }
       const int s = lo, wl = s_wpre[s + 1] - s_wpre[s], nbl = s_pre[s + 1] - s_pre[s];
       const long long r = t - (long long)s_wpre[s] * U;
-      const int u = static_cast<int>(r / wl), rr = static_cast<int>(r - (long long)u * wl);
+      const int u = static_cast<int>(div(r, wl)), rr = static_cast<int>(r - (long long)u * wl);
       // a unit's cost: [segment, shared blocks] (a leader with a shared part), segment, own blocks
       const int B = shared ? shared_len(s) : 0;
       const int wS = B > 0 ? kSegCost + kSharedCost * B : 0;
@@ -1325,9 +1355,9 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
                             : B + max(0, rr - wS - kSegCost + kOwnCost - 1) / kOwnCost;
       return (long long)s_pre[s] * U + (long long)u * nbl + j;
     };
-    const long long qt = Tw / W, rt = Tw % W;
-    start = block_at(w * qt + (w * rt) / W);
-    end = block_at((w + 1) * qt + ((w + 1) * rt) / W);
+    const long long qt = div(Tw, W), rt = Tw - qt * W;
+    start = block_at(w * qt + div(w * rt, W));
+    end = block_at((w + 1) * qt + div((w + 1) * rt, W));
     __syncthreads();  // every warp has its range: the side buffers may now receive copies
   }
   const int len = static_cast<int>(end - start);
@@ -1337,12 +1367,12 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     // lengths may have left a piece there.  (Slots grow with the warp and the segment: no piece uses this one.)
     if (lane == 0 && start < T_all) {
       int s, u, j;
-      locate(start, s_pre, S, U, s, u, j);
+      locate(start, s_pre, S, U, s, u, j, kMod && T_all <= INT_MAX);
       p.part_tag[(long long)w + seg_id(s, u, shared && j < shared_len(s) ? 0 : 1)] = make_int2(-1, 0);
     }
     if (fused) write_tokens();
     if constexpr (kMod)
-      if (gridDim.x == 1) merge_here<T, D, kMma>(p, warp, kDecodeWarps, lane);
+      if (alone) merge();
     return;
   }
 
@@ -1355,7 +1385,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     kvh = 0;
     if (gpos < end) {
       int s, u, j, h0, nh;
-      locate(gpos, s_pre, S, U, s, u, j);
+      locate(gpos, s_pre, S, U, s, u, j, kMod && T_all <= INT_MAX);
       unit_heads<kMma>(p, u, kvh, h0, nh);
       bool in_shared = false;
       int row = s;  // the table the block is read through
@@ -1422,7 +1452,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   math.init(lane, pw);
   math.set_columns(p.group);
   int cs, cu, cj;
-  locate(start, s_pre, S, U, cs, cu, cj);
+  locate(start, s_pre, S, U, cs, cu, cj, kMod && T_all <= INT_MAX);
   int part = 1;
   if (shared) {  // position cj of the unit's work: in the shared part, or past it in the own part
     const int B = shared_len(cs);
@@ -1506,6 +1536,11 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       if (j0 == jstart && seg_end && direct_ok) {  // the whole segment: straight to the output
         math.store_out(static_cast<T*>(p.out) + ((long long)cs * p.num_heads + h0) * D, nh, p.out_scale);
         if (lane == 0) p.seg_first[seg] = -1;
+      } else if (alone) {
+        float* o = last ? reinterpret_cast<float*>(ring) : st_o;
+        __syncwarp();  // (every lane has read the last stage)
+        math.store_partial(o, o + kRows * D, nh, p.out_scale);
+        if (lane == 0) s_piece[2 * warp + last] = seg;
       } else {
         // pieces start only at warp and segment boundaries, so this slot is unique
         const long long slot = (long long)w + seg;
@@ -1551,7 +1586,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     }
   }
   if constexpr (kMod)
-    if (gridDim.x == 1) merge_here<T, D, kMma>(p, warp, kDecodeWarps, lane);
+    if (alone) merge();
 }
 
 // --- merge of pieces --------------------------------------------------------------------------------
