@@ -9,23 +9,29 @@
 // ping-pong between the tensor cores and the softmax warps.  What differs:
 //
 //   * Keys.  A unit takes the chunks of 128 keys from the one its first row's window starts in to the last one
-//     that any of its rows sees.  Within them each row hides what it does not see; a chunk that no row of a
+//     that any of its rows sees.  Within them each row hides what it does not see; half a chunk that no row of a
 //     warp sees leaves P = 0 without a score looked at.  V of keys below the unit's first one reads as
 //     zero, as V past the sequence does (P is 0 there, but 0 * NaN would poison O).  A row's first chunks may
 //     be hidden whole: its maximum is -inf until one is not, and every term 0.
-//   * The cap.  A chunk's period is the softmax's time for a tile plus ~1900 clocks of MMAs and hand-overs, so
-//     what the tanh adds to it counts.  cap - 2 cap / (1 + e^(2x)) costs two operations of the special-function
-//     unit (16 a clock and SM) beside the softmax's own one: the chunk 2.4 times as long.  So: the tanh keeps
-//     the scores' order, the row's maximum is the raw scores' one, and the cap becomes an odd polynomial in the
-//     raw score within the exponentials' loop, its multiply-adds (128 a clock and SM) beside the exponentials:
-//     4 terms where all scores of the warp's chunk lie within cap / 2, 6 within cap, the exponential form past it.
-//     (Polynomials over all scores first, then the softmax: the chunk 1.5 times as long; so now only where a
-//     chunk is cut by a mask, or with a bias, after which the maximum is another one.)
-//   * Registers.  The 128 scores of a thread, the polynomials' coefficients and the packed P do not fit 168
-//     registers; a twelfth warp without work makes three whole warpgroups, of which the softmax's two take
-//     the third one's registers (setmaxnreg).
+//   * The cap.  cap - 2 cap / (1 + e^(2x)) costs two operations of the special-function unit (16 a clock and SM)
+//     beside the softmax's own one: 566 us for 16 chunks of 512 tokens behind 3584 (28 heads of 128 dims, fp16), which
+//     take 277 us uncapped.  So: the tanh keeps the scores' order, the row's maximum is the raw scores' one, and the cap
+//     becomes an odd polynomial in the raw score within the exponentials' loop, its multiply-adds (128 a clock and SM)
+//     beside the exponentials: 4 terms where all scores of the warp's half chunk lie within cap / 2 (355 us), 6 within
+//     cap (435 us), the exponential form past it.  (Polynomials over all scores first, then the softmax: 403 us;
+//     so now only where a mask cuts the half, or with a bias, after which the maximum is another one.)
+//   * Two threads to a row, one for each half of a chunk's keys, which exchange their maxima; each reads
+//     its scores twice, for the maximum and for P, and keeps 32 in registers at a time.  A row's softmax is a
+//     step of the chain S, softmax, P V, S; halved, 16 chunks of 512 tokens with capped scores in a window of 1024 take
+//     179 us for 192, whole prompts in bf16 675 for 779.  (The first half of P handed over before the second is
+//     done, so that its P V may start, cost more than it gave: 207 us.)
+//   * Registers.  640 threads have 96 each; the softmax's four warpgroups take 8 of each thread of the fifth
+//     (setmaxnreg), which copies, issues the MMAs and assigns.
 //   * Units are assigned in rounds (assign_units) and their figures handed over in the ring (unit_view).
-//   * The output is stored four threads to a row (store_rows).
+//   * Q is loaded and the output stored four threads to a row (load_q, store_rows).
+//   * The MMA warp waits for the next chunk's K before it issues a chunk's P V, so that nothing stands between
+//     a tile's P V and its next S (a wait takes 100 to 200 clocks even when what it waits for is there): 177.1 us for
+//     179.6 in fp16.  In bf16, whose P V is twice as long, the K is waited for behind it: 677 us for 686.
 #pragma once
 
 #include "prefill_ws.cuh"
@@ -38,15 +44,15 @@ using namespace ws;
 // the kinds of kernels: any sum of these
 constexpr int kCapped = 1, kBiased = 2;
 
-constexpr int kThreads = 12 * 32, kIdleWarp = 11;
-// registers per thread of the softmax warps and the others, out of the launch's 384 x 168
-template <int kKind>
-constexpr int kSoftmaxRegs = (kKind & kCapped) ? 216 : 208;
-template <int kKind>
-constexpr int kOtherRegs = (kKind & kCapped) ? 72 : 88;
-constexpr int kLaunchRegs = 168;
-template <int kKind>
-constexpr bool kRegsFit = 256 * kSoftmaxRegs<kKind> + 128 * kOtherRegs<kKind> <= kThreads * kLaunchRegs;
+// Warps 0..7 are tile A's softmax, 8..15 tile B's, four for each half of a chunk's keys; then the copies,
+// the MMAs, the unit ring and one without work.
+constexpr int kHalf = kKeys / 2, kStep = 32, kTileThreads = 256;  // (scores are taken kStep at a time)
+constexpr int kSoftmaxWarps = 16, kCopyWarp = 16, kSchedWarp = 18, kIdleWarp = 19;
+constexpr int kThreads = 20 * 32;  // (the warps' numbers of prefill_ws.cuh's header are 16 to 18 here)
+constexpr int kUnitReaders = kSoftmaxWarps + 2;
+// registers per thread of the softmax warps and the others, out of the launch's 640 x 96
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
+static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "what the launch has");
 
 // the smallest of three (a NaN operand is ignored, as by fminf)
 __device__ __forceinline__ float min3(float a, float b, float c) {
@@ -54,24 +60,26 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// The largest (smallest) of a chunk's scores, as a tree of three-input maxima in 8 chains
-__device__ __forceinline__ float largest(const float (&sv)[kKeys]) {
-  static_assert(kKeys % 16 == 0, "8 chains, two keys a step");
+// The largest (smallest) of N scores, as a tree of three-input maxima in 8 chains
+template <int N>
+__device__ __forceinline__ float largest(const float (&sv)[N]) {
+  static_assert(N % 16 == 0, "8 chains, two keys a step");
   float t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = fmaxf(sv[i], sv[8 + i]);
 #pragma unroll
-  for (int j = 16; j < kKeys; j += 16)
+  for (int j = 16; j < N; j += 16)
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = max3(t[i], sv[j + i], sv[j + 8 + i]);
   return fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], t[4], t[5]), t[6], t[7]));
 }
-__device__ __forceinline__ float smallest(const float (&sv)[kKeys]) {
+template <int N>
+__device__ __forceinline__ float smallest(const float (&sv)[N]) {
   float t[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) t[i] = fminf(sv[i], sv[8 + i]);
 #pragma unroll
-  for (int j = 16; j < kKeys; j += 16)
+  for (int j = 16; j < N; j += 16)
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = min3(t[i], sv[j + i], sv[j + 8 + i]);
   return fminf(min3(t[0], t[1], t[2]), min3(min3(t[3], t[4], t[5]), t[6], t[7]));
@@ -87,15 +95,15 @@ __device__ __forceinline__ uint64_t odd_poly(uint64_t x, const uint64_t (&c)[N],
   return fma2(x, t, d);
 }
 
-// The rows that a warp's threads hold (D elements each, as D / 2 words) to rows `at` of out (below 0:
-// nowhere).  Four threads exchange their pieces of 16 bytes first, so that they store 64 bytes of one row
+// Half a row of out, which a warp's threads hold (N elements each, as N / 2 words), to rows `at` of D elements
+// (below 0: nowhere).  Four threads exchange their pieces of 16 bytes first, so that they store 64 bytes of one row
 // side by side, then of the next.  (Each thread on its own row made 32 requests of every store: 4096 a unit, behind
 // which the MMA warp's look-ups of its next unit waited ~5000 clocks.)
-template <typename T, int D>
-__device__ __forceinline__ void store_rows(uint32_t (&w)[D / 2], T* out, long long at) {
+template <typename T, int N, int D>
+__device__ __forceinline__ void store_rows(uint32_t (&w)[N / 2], T* out, long long at) {
   const int q = threadIdx.x & 3;
 #pragma unroll
-  for (int g = 0; g < D / 32; ++g) {  // four pieces: piece i of lane j of the four becomes piece j of lane i
+  for (int g = 0; g < N / 32; ++g) {  // four pieces: piece i of lane j of the four becomes piece j of lane i
 #pragma unroll
     for (int m = 1; m <= 2; m <<= 1)
 #pragma unroll
@@ -115,7 +123,7 @@ __device__ __forceinline__ void store_rows(uint32_t (&w)[D / 2], T* out, long lo
     const long long row = __shfl_sync(0xffffffffu, at, (threadIdx.x & 28) + a);
     if (row < 0) continue;
 #pragma unroll
-    for (int g = 0; g < D / 32; ++g)
+    for (int g = 0; g < N / 32; ++g)
       reinterpret_cast<uint4*>(out + row * D)[4 * g + q] =
           make_uint4(w[16 * g + 4 * a], w[16 * g + 4 * a + 1], w[16 * g + 4 * a + 2], w[16 * g + 4 * a + 3]);
   }
@@ -291,13 +299,14 @@ struct Shape {  // the plain kernel's, but for the ring and the table
   static constexpr int kOffV = kOffK + kKStages * kKBytes; // V ring
   static constexpr int kOffBar = kOffV + kVStages * kVBytes;
   // fullk[K], fullv[V], kfree[K], vfree[V], per tile 5 (sfull, pfull, pvdone, qfull,
-  // ofree), ufull[U], uempty[U], never
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * 5 + 2 * kUnitSlots + 1;
+  // ofree), ufull[U], uempty[U], pair[8], never
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * 5 + 2 * kUnitSlots + 8 + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;  // TMEM address, abort flag
   static constexpr int kOffUnits = kOffMisc + 16;                           // [kUnitSlots][kUnitInts]: the unit ring
   static constexpr int kUnitInts = 9;                                       // a slot: see unit_view
   static constexpr int kOffTab = kOffUnits + kUnitSlots * kUnitInts * 4;    // unit selection's table
-  static constexpr int kEnd = kOffTab + 5 * kMaxSeqsPerLaunch * 4;
+  static constexpr int kOffMax = kOffTab + 5 * kMaxSeqsPerLaunch * 4;       // [2 turns][2 tiles][2 halves][128 rows]
+  static constexpr int kEnd = kOffMax + 2 * 2 * 2 * kRows * 4;
   // more than half an SM's shared memory, so one CTA per SM: it takes all of TMEM
   static constexpr int kSmem = kEnd > 116 * 1024 ? kEnd : 116 * 1024;
   static constexpr int kTmemCols = 512;  // tile X at 256 X: S/P 0..127, O 128..128+D
@@ -346,11 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(Sh::kSmem > 114 * 1024, "two CTAs on one SM would contend for TMEM");
   static_assert(Sh::kSmem <= 227 * 1024, "shared memory per CTA");
   static_assert(kKeys % BS == 0, "a chunk is whole blocks");
-  static_assert(kRegsFit<kKind>, "registers shared out that the launch does not have");
   // P in one 16-bit part for fp16 (11 significant bits, the operands' own precision); for
   // bf16 a high and a low part (~16 bits), since one bf16 part (8 bits) would add
   // errors as large as the output's own rounding
   constexpr int kParts = std::is_same<T, __half>::value ? 1 : 2;
+  constexpr bool kEarlyK = kParts == 1;  // when the MMA warp waits for the next chunk's K
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::kOffBar);
   uint64_t* fullk = bars;                   // [kKStages] K buffer landed (TMA bytes)
@@ -360,15 +369,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* tbars = vfree + kVStages;       // per tile X at 5 X: sfull, pfull, pvdone, qfull, ofree
   uint64_t* ufull = tbars + 10;             // [kUnitSlots] the scheduler wrote the slot
   uint64_t* uempty = ufull + kUnitSlots;    // [kUnitSlots] every reader took the slot
-  uint64_t* never = uempty + kUnitSlots;    // nothing completes it: the timeout-path test waits on it
+  uint64_t* pair = uempty + kUnitSlots;     // [8] the two warps that hold a row's halves: tile X, quarter i at 4 X + i
+  uint64_t* never = pair + 8;               // nothing completes it: the timeout-path test waits on it
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Sh::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);  // a thread gave up
   volatile int* s_unit = reinterpret_cast<volatile int*>(smem + Sh::kOffUnits);  // [kUnitSlots][4]
   int* tab = reinterpret_cast<int*>(smem + Sh::kOffTab);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // S(c) in TMEM (commit); P(c) in TMEM, O rescaled, V tail zeroed (128 arrivals); the
-  // unit's last P V done (commit); the next unit's Q in shared memory (128 arrivals);
-  // the unit's O read out of TMEM (128 arrivals)
+  // S(c) in TMEM (commit); P(c) in TMEM, O rescaled, V tail zeroed (256 arrivals); the
+  // unit's last P V done (commit); the next unit's Q in shared memory (256 arrivals);
+  // the unit's O read out of TMEM (256 arrivals)
   auto sfull = [&](int X) { return tbars + 5 * X; };
   auto pfull = [&](int X) { return tbars + 5 * X + 1; };
   auto pvdone = [&](int X) { return tbars + 5 * X + 2; };
@@ -390,15 +400,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int X = 0; X < 2; ++X) {
       mbar_init(sfull(X), 1);
-      mbar_init(pfull(X), kSoftmaxThreads);
+      mbar_init(pfull(X), kTileThreads);
       mbar_init(pvdone(X), 1);
-      mbar_init(qfull(X), kSoftmaxThreads);
-      mbar_init(ofree(X), kSoftmaxThreads);
+      mbar_init(qfull(X), kTileThreads);
+      mbar_init(ofree(X), kTileThreads);
     }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&ufull[i], 1);
       mbar_init(&uempty[i], kUnitReaders);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&pair[i], 2);
     mbar_init(never, 1);
     fence_barrier_init();
   }
@@ -413,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();  // both CTAs' mbarriers are initialised before either copies into the other
   const uint32_t tmem = *s_tmem;
   const int G = p.group;
-  int issued_k = 0, issued_v = 0;  // chunks (of all units) whose K (V) copies warp 8 issued
+  int issued_k = 0, issued_v = 0;  // chunks (of all units) whose K (V) copies the copy warp issued
   auto wait = [&](uint64_t* bar, int parity) { return wait_or_abort(bar, parity, s_abort, p.err); };
   // the k-th unit of the ring (the slot's ufull phase k / kUnitSlots); every reader
   // takes it once and frees it with one arrival per warp
@@ -426,24 +437,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<kKind>));
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<kKind>));
-  if (warp < 8) {
-    // ================= softmax: tile X, row r, all keys of each chunk of each unit =================
-    const int X = warp >> 2, r = tid & (kRows - 1);
+  if (warp < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp < kSoftmaxWarps) {
+    // ================= softmax: tile X, row r, half hf of the keys of each chunk of each unit =================
+    const int X = warp >> 3, hf = (warp >> 2) & 1, r = tid & (kRows - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + 256 * X + lane_base;
-    const uint32_t t_o = t_s + kKeys;
+    const uint32_t t_h = t_s + hf * kHalf, t_o = t_s + kKeys;  // this half's scores; the tile's O
     const float sl2 = kCap || kBias ? 1.f : p.scale_log2;  // modify() leaves scores in log2 units
-    // kCap, kBias: the row's scores of the keys at positions dist .. dist + kKeys - 1 relative to its
+    // kCap, kBias: the row's scores of the keys at positions dist .. dist + kStep - 1 relative to its
     // own, capped and biased, in log2 units
-    auto modify = [&](float(&sv)[kKeys], int dist, float slope) {
+    auto modify = [&](float(&sv)[kStep], int dist, float slope) {
       if constexpr (kCap) {
         const float size = fmaxf(largest(sv), -smallest(sv));
         if (!__any_sync(0xffffffffu, size > p.tanh_near_to)) {
           const uint64_t zero = f2pack(0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < kKeys; j += 2) {
+          for (int j = 0; j < kStep; j += 2) {
             const float2 v = f2unpack(odd_poly(f2pack(sv[j], sv[j + 1]), p.tanh_near, zero));
             sv[j] = v.x;
             sv[j + 1] = v.y;
@@ -451,11 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (__any_sync(0xffffffffu, size > p.tanh_wide_to)) {
           const float e = 2.f * kLog2e * p.scale_log2, cap = p.cap_log2;
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j) sv[j] = fmaf(-2.f * cap, rcp(1.f + ex2(sv[j] * e)), cap);
+          for (int j = 0; j < kStep; ++j) sv[j] = fmaf(-2.f * cap, rcp(1.f + ex2(sv[j] * e)), cap);
         } else {
           const uint64_t zero = f2pack(0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < kKeys; j += 2) {
+          for (int j = 0; j < kStep; j += 2) {
             const float2 v = f2unpack(odd_poly(f2pack(sv[j], sv[j + 1]), p.tanh_wide, zero));
             sv[j] = v.x;
             sv[j + 1] = v.y;
@@ -466,11 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float d0 = static_cast<float>(dist), in = kCap ? 1.f : p.scale_log2;
         if (p.prefix_lens) {  // keys on both sides of the row's position
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j) sv[j] = fmaf(-slope, fabsf(d0 + j), sv[j] * in);
+          for (int j = 0; j < kStep; ++j) sv[j] = fmaf(-slope, fabsf(d0 + j), sv[j] * in);
         } else {              // keys up to it: the distance is -(d0 + j)
           const uint64_t in2 = f2pack(in, in), slope2 = f2pack(slope, slope), base2 = f2pack(slope * d0, slope * d0);
 #pragma unroll
-          for (int j = 0; j < kKeys; j += 2) {
+          for (int j = 0; j < kStep; j += 2) {
             const uint64_t bias = fma2(slope2, f2pack(static_cast<float>(j), static_cast<float>(j + 1)), base2);
             const float2 v = f2unpack(fma2(f2pack(sv[j], sv[j + 1]), in2, bias));
             sv[j] = v.x;
@@ -493,13 +504,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const T* q = static_cast<const T*>(p.q) + (from < 0 ? 0 : from) * D + (lane & 3) * 8;
         const uint32_t nbytes = from < 0 ? 0u : 16u;
 #pragma unroll
-        for (int c = 0; c < D / 8; c += 4)
+        for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); c += 4)  // (its half's warps take half of a row)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sq + i * (D / 8) * 128 + c * 128),
                        "l"(q + 8 * c), "r"(nbytes)
                        : "memory");
       }
     };
     auto key0 = [](const UnitView& v, int c) { return (v.c0 + c) * kKeys; };  // a chunk's first key
+    // this thread's number for the thread with the row's other half, and that one's for it; ok as for every wait
+    int turn = 0;
+    float* s_max = reinterpret_cast<float*>(smem + Sh::kOffMax);
+    auto exchange = [&](float mine, float& other) -> bool {
+      float* at = s_max + ((turn & 1) * 2 + X) * 2 * kRows + r;
+      at[hf * kRows] = mine;
+      __syncwarp();
+      uint64_t* bar = pair + 4 * X + (warp & 3);
+      if (lane == 0) mbar_arrive(bar);
+      if (!__all_sync(0xffffffffu, wait(bar, turn & 1))) return false;
+      other = at[(hf ^ 1) * kRows];
+      ++turn;  // (two turns' numbers: a warp writes over one only after both have met again)
+      return true;
+    };
     auto q_landed = [&]() {  // the Q copies done, visible to the MMAs, handed over
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -539,68 +564,79 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is taken by the whole warp, so each wait's outcome is agreed across the warp
           if (!(ok = __all_sync(0xffffffffu, wait(sfull(X), cx & 1)))) break;
           fence_after();
-          const int lim = last - key0(U, c);  // keys 0..lim of the chunk are visible to the row
-          const int lo = from - key0(U, c);  // and none before this one
-          float corr = 1.f;
-          bool move = false;
-          if (!__any_sync(0xffffffffu, lo < kKeys && lim >= 0)) {  // a chunk that no row of the warp sees
-            const uint32_t zero[16] = {};
-#pragma unroll
-            for (int k2 = 0; k2 < kKeys / 16; ++k2) st16(t_s + 16 * k2, zero);
-            wait_st();
-          } else {
-            float sv[kKeys];
-            ld128(t_s, sv);
-            // Capped without a bias, in a chunk that the warp's rows see whole: the tanh keeps the order of the
+          const int k0c = key0(U, c) + hf * kHalf;       // the half's first key
+          const int lim = last - k0c, lo = from - k0c;  // of the half, keys lo .. lim are visible to the row
+          const bool seen = __any_sync(0xffffffffu, lo < kHalf && lim >= 0);  // by any of the warp's rows
+          int form = 0;
+          float mx = -INFINITY;
+          if (seen) {
+            // Capped without a bias, where the warp's rows see the half whole: the tanh keeps the order of the
             // scores, so the row's maximum is that of the raw ones, and the cap is taken within the exponentials'
             // loop below, by the form that the scores' size allows (so that its multiply-adds run beside the
-            // exponentials)
-            int form = 0;
-            float mx;
-            if (kCap && !kBias && !__any_sync(0xffffffffu, lo > 0 || lim < kKeys - 1)) {
+            // exponentials).  Elsewhere the scores are changed and hidden first, in TMEM.
+            const bool whole = !__any_sync(0xffffffffu, lo > 0 || lim < kHalf - 1);
+            if (whole && !kBias) {
+              float sv[kHalf];
+              ld64(t_h, sv);
+              mx = largest(sv) * sl2;  // (scale > 0 keeps the order)
               if constexpr (kCap) {
-                mx = largest(sv);
                 const float size = fmaxf(mx, -smallest(sv));
                 form = __any_sync(0xffffffffu, size > p.tanh_wide_to) ? 3 : __any_sync(0xffffffffu, size > p.tanh_near_to) ? 2 : 1;
                 mx = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(mx * (2.f * kLog2e * p.scale_log2))), p.cap_log2);
               }
             } else {
-              if constexpr (kCap || kBias) modify(sv, key0(U, c) - pos, slope);
-              if (lo > 0) {
+#pragma unroll 1
+              for (int k0 = 0; k0 < kHalf; k0 += kStep) {
+                float sv[kStep];
+                ld32(t_h + k0, sv);
+                if constexpr (kCap || kBias) modify(sv, k0c + k0 - pos, slope);
+                if (lo > k0) {
 #pragma unroll
-                for (int j = 0; j < kKeys; ++j)
-                  if (j < lo) sv[j] = -INFINITY;
+                  for (int j = 0; j < kStep; ++j)
+                    if (j < lo - k0) sv[j] = -INFINITY;
+                }
+                if (lim - k0 < kStep - 1) {  // the diagonal chunk (or past it): hide the later keys
+#pragma unroll
+                  for (int j = 0; j < kStep; ++j)
+                    if (j > lim - k0) sv[j] = -INFINITY;
+                }
+                mx = fmaxf(mx, largest(sv) * sl2);
+                st32(t_h + k0, sv);
               }
-              if (lim < kKeys - 1) {  // the diagonal chunk (or past it): hide the later keys
-#pragma unroll
-                for (int j = 0; j < kKeys; ++j)
-                  if (j > lim) sv[j] = -INFINITY;
-              }
-              mx = largest(sv) * sl2;  // the row maximum of the raw scores (scale > 0 keeps the order)
             }
-            move = mx > m + 8.f;
-            if (move) {
-              corr = m == -INFINITY ? 1.f : exp2f(m - mx);  // (l and O are still zero)
-              m = mx;
-              l *= corr;
-            }
-            // P over the row's S columns, 16 keys at a time: the 16 columns of keys 16 k ..
-            // 16 k + 15 become 8 columns of high parts (then, for bf16, 8 of low parts)
-            {
-              // P = 2^(scale * s - m) (s = -inf gives 0): the scaling of a pair of scores and
-              // the row sums in paired fp32 operations
-              // (a row whose window starts in a later chunk has seen no score yet: P is 0)
-              const float mref = m == -INFINITY ? 0.f : m;
-              const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-mref, -mref);
-              uint64_t ps2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
-              auto store_p = [&](auto exponent) {
+          }
+          {
+            float other;
+            if (!(ok = exchange(mx, other))) break;
+            mx = fmaxf(mx, other);
+          }
+          float corr = 1.f;
+          const bool move = mx > m + 8.f;
+          if (move) {
+            corr = m == -INFINITY ? 1.f : exp2f(m - mx);  // (l and O are still zero)
+            m = mx;
+            l *= corr;
+          }
+          // P over the row's S columns, 16 keys at a time: the 16 columns of keys 16 k ..
+          // 16 k + 15 become 8 columns of high parts (then, for bf16, 8 of low parts)
+          if (seen) {
+            // P = 2^(scale * s - m) (s = -inf gives 0): the scaling of a pair of scores and
+            // the row sums in paired fp32 operations
+            // (a row whose window starts in a later chunk has seen no score yet: P is 0)
+            const float mref = m == -INFINITY ? 0.f : m;
+            const uint64_t sl2x2 = f2pack(sl2, sl2), negm2 = f2pack(-mref, -mref);
+            uint64_t ps2[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+            auto store_p = [&](auto exponent) {
 #pragma unroll
-                for (int k2 = 0; k2 < kKeys / 16; ++k2) {
+              for (int k0 = 0; k0 < kHalf; k0 += kStep) {
+                float sv[kStep];
+                ld32(t_h + k0, sv);
+#pragma unroll
+                for (int k2 = 0; k2 < kStep; k2 += 16) {
                   uint32_t blk[8 * kParts];
 #pragma unroll
                   for (int j = 0; j < 8; ++j) {
-                    const int key = 16 * k2 + 2 * j;
-                    const float2 y = f2unpack(exponent(f2pack(sv[key], sv[key + 1])));
+                    const float2 y = f2unpack(exponent(f2pack(sv[k2 + 2 * j], sv[k2 + 2 * j + 1])));
                     const float x0 = ex2(y.x), x1 = ex2(y.y);
                     ps2[j & 1] = add2(ps2[j & 1], f2pack(x0, x1));
                     blk[j] = pack2<T>(x0, x1);
@@ -609,37 +645,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                       blk[8 + j] = pack2<T>(x0 - back.x, x1 - back.y);
                     }
                   }
-                  if constexpr (kParts == 2) st16(t_s + 16 * k2, blk);
-                  else st8(t_s + 16 * k2, blk);
-                }
-              };
-              if constexpr (kCap && !kBias) {
-                if (form == 1) {
-                  store_p([&](uint64_t x) { return odd_poly(x, p.tanh_near, negm2); });
-                } else if (form == 2) {
-                  store_p([&](uint64_t x) { return odd_poly(x, p.tanh_wide, negm2); });
-                } else if (form == 3) {  // cap - 2 cap / (1 + e^(2 s / cap))
-                  const float e = 2.f * kLog2e * p.scale_log2, top = p.cap_log2 - mref, cap2 = -2.f * p.cap_log2;
-                  store_p([&](uint64_t x) {
-                    const float2 v = f2unpack(x);
-                    return f2pack(fmaf(cap2, rcp(1.f + ex2(v.x * e)), top), fmaf(cap2, rcp(1.f + ex2(v.y * e)), top));
-                  });
+                  if constexpr (kParts == 2) st16(t_h + k0 + k2, blk);
+                  else st8(t_h + k0 + k2, blk);
                 }
               }
-              if (form == 0) store_p([&](uint64_t x) { return fma2(x, sl2x2, negm2); });
-              wait_st();
-              const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
-              l += (s0.x + s0.y) + (s1.x + s1.y);
+            };
+            if constexpr (kCap && !kBias) {
+              if (form == 1) {
+                store_p([&](uint64_t x) { return odd_poly(x, p.tanh_near, negm2); });
+              } else if (form == 2) {
+                store_p([&](uint64_t x) { return odd_poly(x, p.tanh_wide, negm2); });
+              } else if (form == 3) {  // cap - 2 cap / (1 + e^(2 s / cap))
+                const float e = 2.f * kLog2e * p.scale_log2, top = p.cap_log2 - mref, cap2 = -2.f * p.cap_log2;
+                store_p([&](uint64_t x) {
+                  const float2 v = f2unpack(x);
+                  return f2pack(fmaf(cap2, rcp(1.f + ex2(v.x * e)), top), fmaf(cap2, rcp(1.f + ex2(v.y * e)), top));
+                });
+              }
             }
+            if (form == 0) store_p([&](uint64_t x) { return fma2(x, sl2x2, negm2); });
+            const float2 s0 = f2unpack(ps2[0]), s1 = f2unpack(ps2[1]);
+            l += (s0.x + s0.y) + (s1.x + s1.y);
+          } else {
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int k2 = 0; k2 < kHalf / 16; ++k2) st16(t_h + 16 * k2, zero);
           }
-          // O holds P V up to chunk c - 1, finished (S(c) was issued after it): rescale the
-          // row if the maximum moved (the whole warp takes the branch when one of its rows
+          wait_st();
+          // O holds P V up to chunk c - 1, finished (S(c) was issued after it): rescale half of the
+          // row's columns if the maximum moved (the whole warp takes the branch when one of its rows
           // needs it; the others scale by 1)
           const bool rescale = c > 0 && move && corr != 1.f;
           if (__any_sync(0xffffffffu, rescale)) {
             const float f = rescale ? corr : 1.f;
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
+            for (int c0 = hf * (D / 2); c0 < (hf + 1) * (D / 2); c0 += 32) {
               float o[32];
               ld32(t_o + c0, o);
 #pragma unroll
@@ -655,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char* vbase = smem + Sh::kOffV + (gc % kVStages) * Sh::kVBytes;
             constexpr int kRow = 2 * BS, kUnits = kRow / 16;
             const int k1 = U.lo - key0(U, c);  // keys 0 .. k1 - 1 of the chunk (k1 < kKeys)
-            for (int i = tid; i < (k1 + 7) / 8 * D; i += kSoftmaxThreads) {
+            for (int i = tid; i < (k1 + 7) / 8 * D; i += kTileThreads) {
               const int g8 = i / D, d = i % D;  // as below
               const int a = d * kRow + ((8 * g8) % BS) * 2;
               unsigned char* ptr = vbase + ((8 * g8) / BS) * Sh::kTile + (a ^ (((a >> 7) & (kUnits - 1)) << 4));
@@ -678,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kRow = 2 * BS, kUnits = kRow / 16;
             const int k0 = kz - key0(U, c);  // first key to clear (0 <= k0 < kKeys)
             const int g0 = k0 / 8;          // the 8-key group holding it
-            for (int i = tid; i < (kKeys / 8 - g0) * D; i += kSoftmaxThreads) {
+            for (int i = tid; i < (kKeys / 8 - g0) * D; i += kTileThreads) {
               const int g8 = g0 + i / D, d = i % D;  // keys 8 g8 .. 8 g8 + 7 of dim d
               const int a = d * kRow + ((8 * g8) % BS) * 2;
               unsigned char* ptr = vbase + ((8 * g8) / BS) * Sh::kTile + (a ^ (((a >> 7) & (kUnits - 1)) << 4));
@@ -700,16 +740,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // next unit's P V), rounded to T, stored as the row's D contiguous elements
         if (!(ok = __all_sync(0xffffffffu, wait(pvdone(X), ux & 1)))) break;
         fence_after();
+        {
+          float other;
+          if (!(ok = exchange(l, other))) break;
+          l = hf ? other + l : l + other;  // (the same sum in both)
+        }
         const float inv = 1.f / l;
         const uint64_t inv2 = f2pack(inv, inv);
-        uint32_t o16[D / 2];
+        uint32_t o16[D / 4];
 #pragma unroll
-        static_assert(D % 64 == 0, "O read 64 columns at a time");
-        for (int c0 = 0; c0 < D; c0 += 64) {  // 64 columns per wait
-          float o[64];
-          ld64(t_o + c0, o);
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {  // half of the row's columns
+          float o[32];
+          ld32(t_o + hf * (D / 2) + c0, o);
 #pragma unroll
-          for (int j = 0; j < 64; j += 2) {
+          for (int j = 0; j < 32; j += 2) {
             const float2 v = f2unpack(mul2(f2pack(o[j], o[j + 1]), inv2));
             o16[(c0 + j) / 2] = pack2<T>(v.x, v.y);
           }
@@ -717,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before();
         mbar_arrive(ofree(X));
         if (N.s >= 0 && N.ntiles > X) q_landed();  // the next unit's first S_X may go
-        store_rows<T, D>(o16, static_cast<T*>(p.out),
+        store_rows<T, D / 2, D>(o16, static_cast<T*>(p.out) + hf * (D / 2),
                          valid ? (long long)(U.tok0 + row / G) * p.num_heads + (long long)U.kvh * G + row % G : -1);
         ++ux;
       } else {  // no rows of this tile in the unit: only the next unit's Q
@@ -730,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // no Q copy lands after the CTA exits
   } else if (warp == kCopyWarp) {
-    // ================= copies (warp 8): K gathers, then V boxes, chunk after chunk of each unit =================
+    // ================= copies (warp 16): K gathers, then V boxes, chunk after chunk of each unit =================
     // This CTA issues its half of each chunk's copies, each into both CTAs of the
     // cluster: lane i the gather4 load crank * kGathers / 2 + i of K (8-dim slice dc,
     // keys 64 h .. 64 h + 63), lane b the V box of the chunk's block b when b % 2 is
@@ -792,9 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += U.nchunks;
     }
   } else if (warp == kIdleWarp) {
-    // =============== nothing (warp 11) ===============
+    // =============== nothing (warp 19) ===============
   } else if (warp == kSchedWarp) {
-    // ================= the unit ring (warp 10): this cluster's units =================
+    // ================= the unit ring (warp 18): this cluster's units =================
     // Every cluster replays the same assignment of all units of the launch (assign_units);
     // this cluster's enter the ring in that order.  Both CTAs of a cluster write
     // the same sequence; a unit with x < 0 ends it.
@@ -835,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     });
     if (ok) push(-1, 0, 0);
   } else {
-    // ================= MMAs (warp 9): per unit S_X(0), then per chunk P V_A(c), S_A(c + 1), P V_B(c), S_B(c + 1) =================
+    // ================= MMAs (warp 17): per unit S_X(0), then per chunk P V_A(c), S_A(c + 1), P V_B(c), S_B(c + 1) =================
     // The whole warp runs the loop and the waits (so the loop state and the descriptors
     // stay warp-uniform); one elected lane issues the MMAs and the commits.  A CTA
     // without rows in a unit (the unit's second pair missing) still frees each buffer
@@ -908,6 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int gc = g + c, vb = gc % kVStages, g1 = gc + 1;
         if (c == nc - 1 && !(ok = take_unit(k + 1, N))) break;
         if (!(ok = wait_all(&fullv[vb], (gc / kVStages) & 1))) break;
+        if (kEarlyK && c + 1 < nc && nt > 0 && !(ok = wait_all(&fullk[g1 % kKStages], (g1 / kKStages) & 1))) break;
         for (int Xm = 0; Xm < nt && ok; ++Xm) {
           if (!(ok = wait_all(pfull(Xm), cx[Xm] & 1))) break;  // the softmax wrote P_X(c)
           // the first P V of a unit overwrites O_X: the previous unit's O_X is read out
@@ -918,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c == nc - 1) commit_to(pvdone(Xm), ux[Xm] & 1);  // O_X is complete
           ++cx[Xm];
           if (c + 1 < nc) {
-            if (Xm == 0 && !(ok = wait_all(&fullk[g1 % kKStages], (g1 / kKStages) & 1))) break;
+            if (!kEarlyK && Xm == 0 && !(ok = wait_all(&fullk[g1 % kKStages], (g1 / kKStages) & 1))) break;
             // S_X(c + 1) overwrites the columns P V_X(c) reads, issued right behind it: MMAs
             // of one thread run in issue order, so no wait is needed between the two
             fence_after();
@@ -952,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   fence_before();
   __syncthreads();
-  // After an abort no consumer waits for the copies still landing: warp 8 waits
+  // After an abort no consumer waits for the copies still landing: the copy warp waits
   // (bounded) for the last chunks it issued, so nothing lands after the CTA exits.
   if (*s_abort && warp == kCopyWarp && lane == 0) {
     for (int c = issued_k - kKStages; c < issued_k; ++c)
