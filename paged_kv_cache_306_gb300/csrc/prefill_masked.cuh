@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* never = pair + 8;               // nothing completes it: the timeout-path test waits on it
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Sh::kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);  // a thread gave up
-  volatile int* s_unit = reinterpret_cast<volatile int*>(smem + Sh::kOffUnits);  // [kUnitSlots][4]
+  volatile int* s_unit = reinterpret_cast<volatile int*>(smem + Sh::kOffUnits);  // [kUnitSlots][kUnitInts]
   int* tab = reinterpret_cast<int*>(smem + Sh::kOffTab);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // S(c) in TMEM (commit); P(c) in TMEM, O rescaled, V tail zeroed (256 arrivals); the
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = max(pos, U.prefix - 1);
         int from = 0;
         float slope = 0.f;
-        if (p.window > 0) from = pos - (p.window - 1);
+        if (p.window > 0) from = max(0, pos - (p.window - 1));  // (from - k0c below would not fit an int otherwise)
         if constexpr (kBias) slope = __ldg(p.slopes + U.kvh * G + (valid ? row % G : 0)) * kLog2e;
         float m = -INFINITY, l = 0.f;
         for (int c = 0; c < U.nchunks; ++c, ++cx) {

@@ -198,3 +198,12 @@ def test_more_sequences_than_the_table_of_a_launch_holds(pa, n):
     call, check = decode_call(pa, lens, n + 1, softcap=9.0, window=15)
     check(call())
     assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200, 300])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=9.0)])
+def test_the_longest_windows_behind_rows_before_their_prefix(pa, window, kw):
+    """Rows near position 0 that see a prefix of several chunks through a window longer than any sequence."""
+    call, check = prefill_call(pa, [0, 3], [400, 200], 9, prefixes=[390, 150], window=window, **kw)
+    check(call())
+    assert pa.pa_get_device_error() == 0
