@@ -454,7 +454,8 @@ PA_API pa_status pa_prefill_masked(void* out, const void* q, const void* k_cache
  *                dims; *_stride elements lie between a token's row and the next, so that all
  *                three may be views of one projection's rows.  A stride is a multiple of 16 bytes.
  * q_out          [num_tokens, num_heads, head_size]; may be q itself (q_stride then being a
- *                row's elements), else it overlaps no input.  Every token's q is turned, padding tokens' too.
+ *                row's elements), else it overlaps no input, from its first to its last row
+ *                (PA_ERR_INVALID_ARG otherwise).  Every token's q is turned, padding tokens' too.
  * positions      int64 [num_tokens], any values
  * inv_freq       double [rotary_dim / 2] in device memory, finite: radians per position
  *                (pa_rope_frequencies computes them)

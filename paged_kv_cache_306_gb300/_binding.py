@@ -614,7 +614,7 @@ def pa_rope(q_out, key_out, q, key, positions, inv_freq, layout=ROPE_HALVES, amp
         raise PAError(PA_ERR_INVALID_ARG, "key_out and key differ in shape")
     T, H, D = q.shape
     check(load().pa_rope(_ptr(q_out), _ptr(key_out), _ptr(q), _ptr(key), sq, sk, _ptr(positions), _ptr(inv_freq), T, H,
-                         key.shape[1], D, 2 * inv_freq.shape[0], layout, float(amplitude), dtype_code(q.dtype),
+                         key.shape[1], D, 2 * inv_freq.shape[0], _int32("layout", layout), float(amplitude), dtype_code(q.dtype),
                          _stream(stream)))
 
 
@@ -647,7 +647,7 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_ma
         raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must have one entry per token")
     check(load().pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(key), _ptr(value), sq, sk, sv, _ptr(k_cache),
                                    _ptr(v_cache), _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), T, H, hkv, D,
-                                   2 * inv_freq.shape[0], bs, nb, layout, float(amplitude), dtype_code(q.dtype),
+                                   2 * inv_freq.shape[0], bs, nb, _int32("layout", layout), float(amplitude), dtype_code(q.dtype),
                                    dtype_code(k_cache.dtype), float(k_scale), float(v_scale), _stream(stream)))
 
 

@@ -906,6 +906,16 @@ static pa_status check_stride(const char* name, int64_t stride, int64_t row, pa_
   return PA_OK;
 }
 
+// An output [num_tokens, row] against an input's rows: they have to lie apart, or be the same rows.
+static pa_status check_apart(const char* names, const void* out, int64_t out_row, const void* in, int64_t row,
+                             int64_t stride, int64_t num_tokens, bool same_ok, pa_dtype dtype) {
+  const auto a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+  const auto e = static_cast<uintptr_t>(elem_bytes(dtype)), last = static_cast<uintptr_t>(num_tokens - 1);
+  if (a >= b + (last * stride + row) * e || b >= a + (last + 1) * out_row * e) return PA_OK;
+  if (same_ok && a == b && (stride == row || num_tokens == 1)) return PA_OK;
+  return fail(PA_ERR_INVALID_ARG, "%s overlap", names);
+}
+
 static pa_status launch_rope(pa::RopeParams& p, pa_dtype dtype, int cache_dtype, int head_size, pa_rope_layout layout,
                              void* stream) {
   pa_status st = device_error_ptr(&p.err);
@@ -931,6 +941,13 @@ pa_status pa_rope(void* q_out, void* key_out, const void* q, const void* key, in
   if (!aligned(q_out, 16) || !aligned(key_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(positions, 8) ||
       !aligned(inv_freq, 8))
     return fail(PA_ERR_ALIGNMENT, "q/key and their outputs need 16-byte, positions and inv_freq 8-byte alignment");
+  const int64_t qr = (int64_t)num_heads * head_size, kr = (int64_t)num_kv_heads * head_size;
+  st = check_apart("q_out and q", q_out, qr, q, qr, q_stride, num_tokens, true, dtype);
+  if (st == PA_OK) st = check_apart("q_out and key", q_out, qr, key, kr, key_stride, num_tokens, false, dtype);
+  if (st == PA_OK) st = check_apart("key_out and key", key_out, kr, key, kr, key_stride, num_tokens, true, dtype);
+  if (st == PA_OK) st = check_apart("key_out and q", key_out, kr, q, qr, q_stride, num_tokens, false, dtype);
+  if (st == PA_OK) st = check_apart("q_out and key_out", q_out, qr, key_out, kr, kr, num_tokens, false, dtype);
+  if (st != PA_OK) return st;
   pa::RopeParams p{};
   p.q_out = q_out;
   p.key_out = key_out;
@@ -972,6 +989,11 @@ pa_status pa_rope_and_cache(void* q_out, const void* q, const void* key, const v
   if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) || !aligned(k_cache, 16) ||
       !aligned(v_cache, 16) || !aligned(positions, 8) || !aligned(slot_mapping, 8) || !aligned(inv_freq, 8))
     return fail(PA_ERR_ALIGNMENT, "q/key/value/caches need 16-byte, positions, slot_mapping and inv_freq 8-byte alignment");
+  const int64_t qr = (int64_t)num_heads * head_size, kr = (int64_t)num_kv_heads * head_size;
+  st = check_apart("q_out and q", q_out, qr, q, qr, q_stride, num_tokens, true, key_dtype);
+  if (st == PA_OK) st = check_apart("q_out and key", q_out, qr, key, kr, key_stride, num_tokens, false, key_dtype);
+  if (st == PA_OK) st = check_apart("q_out and value", q_out, qr, value, kr, value_stride, num_tokens, false, key_dtype);
+  if (st != PA_OK) return st;
   pa::RopeParams p{};
   p.q_out = q_out;
   p.q = q;

@@ -178,7 +178,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-//
 // kMod (pa_decode_masked): scores are capped and biased before the softmax, and tokens
 // before the window are hidden (see Scores).
 struct Scores {  // of a block, for kMod; unused otherwise
@@ -1037,7 +1036,7 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
 // warp's ring, whose copies have all been used by then, the other where caller partitions would keep
 // their running state (there are none).  s_piece[2 w], s_piece[2 w + 1]: the segments of warp w's pieces in the state
 // and in the ring, -1: none.  (A launch that small is all latency: one short sequence took 6.4 us with the merge as a
-// kernel of its own, MERGE_US with it here.)
+// kernel of its own, 5.1 with it here.)
 template <typename T, int D, bool kMma, int kRows>
 __device__ __forceinline__ void merge_here(const DecodeParams& p, const int* s_piece, const float* states, const unsigned char* rings,
                                            int ring_bytes, int warp, int warps, int lane) {

@@ -91,7 +91,8 @@ __device__ __forceinline__ uint4 narrow(const float (&v)[X]) {
 // x / scale, correctly rounded where an E4M3 code can tell: the product with the rounded
 // reciprocal, corrected once by its remainder (P. Markstein's division by a rounded reciprocal; exact for the
 // quotients in [2^-12, 1024) and scales in [2^-64, 2^64]).  Other quotients keep the product: smaller ones
-// become zero (of their sign) in any case, larger ones, infinities and NaN saturate as they do.  inv == 0: a scale outside that range, divided.
+// become zero (of their sign) in any case, larger ones, infinities and NaN saturate as they do.  inv == 0: a scale
+// outside that range, divided.
 __device__ __forceinline__ float quotient(float x, float scale, float inv) {
   if (inv == 0.f) return __fdiv_rn(x, scale);
   const float q = x * inv;

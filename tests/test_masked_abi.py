@@ -202,6 +202,24 @@ def test_rope_and_cache_refuses(lib, kw, status):
     assert rope_and_cache(lib, **kw) == status
 
 
+@pytest.mark.parametrize("kw", [                # rows: q 2 x 1024 bytes, k 2 x 256
+    dict(qo=12288, sq=640),                      # in place, but not the same rows
+    dict(qo=12288 + 1024), dict(qo=12288 - 16), dict(qo=12288 + 2032),
+    dict(qo=12288 + 2048 + 240, sq=640),         # q's second row ends 256 bytes later
+    dict(ko=12288), dict(ko=16384 + 256), dict(ko=16384, sk=136), dict(ko=4096 + 2032), dict(ko=4096 - 496),
+    dict(qo=16384 - 2032), dict(qo=16384 + 496),
+])
+def test_rope_refuses_outputs_over_other_rows(lib, kw):
+    assert rope(lib, **kw) == B.PA_ERR_INVALID_ARG
+    assert b"overlap" in lib.pa_last_error_message()
+
+
+@pytest.mark.parametrize("kw", [dict(qo=12288, sq=640), dict(qo=16384 + 240), dict(qo=24576 - 2032, v=24576)])
+def test_rope_and_cache_refuses_outputs_over_other_rows(lib, kw):
+    assert rope_and_cache(lib, **kw) == B.PA_ERR_INVALID_ARG
+    assert b"overlap" in lib.pa_last_error_message()
+
+
 def test_rope_and_cache_with_no_tokens_is_a_no_op(lib):
     assert rope_and_cache(lib, T=0, q=0, kc=0) == B.PA_OK
 
