@@ -256,6 +256,7 @@ struct RopeParams {
   float k_scale, v_scale;       // FP8 pools: stored code = E4M3(x / scale)
   float k_inv, v_inv;           // their rounded reciprocals, 0 where division is needed: set by launch_rope
   int log2_tile, rows_per;      // tokens (a power of two), and rows of a token, per CTA: set by launch_rope
+  int value_rows;               // rows that one of v counts as there
 };
 // cache_dtype < 0: rows (key_out) instead of a pool.  head_size 64 or 128.
 cudaError_t launch_rope(int dtype, int cache_dtype, int head_size, bool pairs, RopeParams p, int sms,

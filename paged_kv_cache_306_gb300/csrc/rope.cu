@@ -16,15 +16,21 @@
 // would be bound by this GPU's fp64 rate; f_i / 2 pi is computed in fp64 once per CTA.)
 //
 // Work.  A unit is two 16-byte pieces of a row: the two halves' pieces of the same pairs,
-// or two neighbouring ones.  A CTA takes a tile of up to 16 tokens and some of their rows (q heads, then k heads, then v
-// heads), puts the cosines and sines of its tokens into shared memory, and a thread keeps one unit and one token for
-// all rows of a kind, with that unit's cosines and sines in registers.  It reads both pieces of a unit before it writes
+// or two neighbouring ones.  A CTA takes a tile of up to 16 tokens and some of their rows (q heads, then k heads,
+// then v heads), puts the cosines and sines of its tokens into shared memory, and a thread keeps one unit and one
+// token for all rows of a kind, with that unit's cosines and sines in registers.  It reads both pieces of a unit before it writes
 // either, so q may be rotated in place.  For q a warp reads and writes whole rows; for k and v it runs over
 // 16 tokens with the pieces of a pair of units innermost: rows are read in whole 32-byte sectors, and
 // consecutive slots of a block are written in whole sectors too, for K (16 bytes a token) and V (one element a
 // token) alike.
+//
+// What bounds it: memory.  16384 tokens of 32 + 8 heads of 128 dims in bf16, 64 of them turned (336 MB): 53.8 us,
+// 6.2 TB/s, 93% of a copy's rate.  8192 tokens of 28 + 4 + 4 heads in fp16 into the pools (151 MB): 28 us, 5.4 TB/s;
+// what lies between is V, two bytes to each place.  One token: 2.5 us in a graph, latency: the launch, the frequencies,
+// a row.
 #include <stdint.h>
 
+#include <numeric>
 #include <type_traits>
 
 #include "pa_device.cuh"
@@ -37,7 +43,8 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTile = 16;  // tokens per CTA at most
 constexpr int kRopeBatch = 2;  // units per thread in flight
-constexpr int kRopeCtasPerSm = 4;  // CTAs of a large launch, at least
+constexpr int kRopeValueRows = 4;               // rows of q that a row of v counts as (see launch_rope)
+constexpr int kRopeBusy = 7, kRopeMost = 9;     // units a thread
 
 // f / 2 pi as a 64-bit fraction of a turn (whole turns drop out).  The quotient is kept as an
 // unevaluated sum hi + lo: 1 / 2 pi to twice the precision of a double.
@@ -132,8 +139,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const long long t0 = (long long)blockIdx.x << p.log2_tile;
   const int ntok = static_cast<int>(min((long long)tile, p.num_tokens - t0));
   const int r2 = p.rotary_dim / 2;
-  const int rows = H + (kPool ? 2 : 1) * Hkv;  // a token's rows: q heads, k heads, v heads
-  const int row0 = blockIdx.y * p.rows_per, row1 = min(rows, row0 + p.rows_per);
+  // a token's rows: q heads, k heads, v heads; of each kind this CTA's
+  const int row0 = blockIdx.y * p.rows_per, row1 = row0 + p.rows_per;
+  const int v0 = (max(row0 - H - Hkv, 0) + p.value_rows - 1) / p.value_rows;
+  const int v1 = kPool ? min(Hkv, (max(row1 - H - Hkv, 0) + p.value_rows - 1) / p.value_rows) : 0;
 
   if (tid < r2) s_turn[tid] = turns_of(__ldg(p.inv_freq + tid));
   if (tid >= kRopeThreads - kRopeTile) {
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   };
   if (row0 < H) to_rows(p.q, p.q_stride, p.q_out, H, row0, min(row1, H));
   if constexpr (!kPool) {
-    if (row1 > H) to_rows(p.key, p.key_stride, p.key_out, Hkv, max(row0, H) - H, row1 - H);
+    if (row1 > H) to_rows(p.key, p.key_stride, p.key_out, Hkv, max(row0, H) - H, min(row1 - H, Hkv));
   } else {
     constexpr int EC = sizeof(TC), XC = 16 / EC;
     const int bs = p.block_size;
@@ -276,12 +285,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
              });
       }
     }
-    if (row1 > H + Hkv) {
+    if (v1 > v0) {
       const Spot w = settle(2 * pr + (k & 1), k >> 1, false);
       const long long t = t0 + w.j, blk = w.j < ntok ? s_blk[w.j] : -1;
       if (blk >= 0) {
         const int off = s_off[w.j];
-        walk(w, static_cast<const T*>(p.value) + t * p.value_stride, max(row0, H + Hkv) - H - Hkv, row1 - H - Hkv,
+        walk(w, static_cast<const T*>(p.value) + t * p.value_stride, v0, v1,
              [&](int h, const uint4& ra, const uint4& rb, const float(&x)[X], const float(&y)[X]) {
                // element d -> v_cache[blk, h, d, off]
                const long long base = (blk * Hkv + h) * D;
@@ -336,20 +345,40 @@ cudaError_t launch_rope(int dtype, int cache_dtype, int head_size, bool pairs, R
                         cudaStream_t stream, int* launches) {
   *launches = 0;
   if (p.num_tokens == 0) return cudaSuccess;
-  const int rows = p.num_heads + (cache_dtype >= 0 ? 2 : 1) * p.num_kv_heads;
+  p.value_rows = kRopeValueRows;
+  const int rows = p.num_heads + (cache_dtype >= 0 ? 1 + p.value_rows : 1) * p.num_kv_heads;
   const int units = head_size * (dtype == 0 ? 4 : 2) / 32;  // per row
   auto inverse = [](float scale) { return scale >= 0x1p-64f && scale <= 0x1p64f ? 1.f / scale : 0.f; };
   p.k_inv = inverse(p.k_scale);
   p.v_inv = inverse(p.v_scale);
-  int tile = kRopeTile;
-  while (tile > 1 && p.num_tokens * rows * units < (long long)tile * kRopeThreads * sms) tile /= 2;
+  // The split.  A CTA takes tile x per rows; what it costs beside them (the turns of its frequencies, its tokens'
+  // cosines) takes 1.5 us, so the launch is two CTAs an SM, or four (one wave still) where two would have more than
+  // kRopeBusy units a thread each.  In a CTA about as many tokens as rows: fewer tokens compute the same cosines in
+  // more CTAs, more leave the tile's rows to few.  A row of v, whose elements go to places of their own, costs as
+  // much as several of q: counted as one, the CTAs with v ran alone at the end of a decode step (64/8 heads of 128
+  // dims fp16, 128 tokens: 10.3 us for 4.9; 32/8 heads into FP8 pools 7.0 for 4.8); counted as 8, long prompts slow
+  // down (16/16 heads bf16, 20000 tokens: 95 us for 85).  At least a unit a thread and 4 CTAs an SM whatever the work:
+  // 28/4 heads fp16, 1 token 3.3 us for 2.5, 256 tokens 6.2 for 5.0, 1024 7.2 for 5.7, 4096 17.6 for 15.8 (in a
+  // graph, inputs in L2; 16/16 heads bf16 8.6 for 4.5 at 400 tokens, but 7.7 for 10.3 at 1024).
+  const long long all = p.num_tokens * rows * units;
+  const long long target = (all > 2ll * sms * kRopeBusy * kRopeThreads ? 4ll : 2ll) * sms;
+  const long long share = (p.num_tokens * rows + target - 1) / target;  // rows of tokens a CTA
+  int tile = 1;
+  while (tile < kRopeTile && tile < p.num_tokens && 16ll * tile * tile <= 9 * share) tile *= 2;
   p.log2_tile = 0;
   while (1 << p.log2_tile < tile) ++p.log2_tile;
   const long long tiles = (p.num_tokens + tile - 1) / tile;
-  // rows per CTA: at least one unit a thread, more while the grid still fills the SMs
-  int per = (kRopeThreads + tile * units - 1) / (tile * units);
-  while (per < rows && tiles * ((rows + 2 * per - 1) / (2 * per)) >= kRopeCtasPerSm * (long long)sms) per *= 2;
-  while ((rows + per - 1) / per > 65535) per *= 2;  // the grid's second extent
+  const long long most = target / tiles > 1 ? target / tiles : 1;  // CTAs a tile
+  int per = static_cast<int>(most >= rows ? 1 : (rows + most - 1) / most);
+  // (CTAs of many more units with v among them leave SMs idle at the end: 64/8 heads, 8192 tokens 57.6 us for 61.4;
+  // without v the cosines are better computed once: 32 + 8 heads, 16381 tokens 53.8 us for 56.5)
+  if (cache_dtype >= 0 && per * tile * units > kRopeMost * kRopeThreads)
+    per = kRopeMost * kRopeThreads / (tile * units);
+  // Small launches: rows of one kind where the heads allow it, since a CTA walks over its q, k and v rows one after
+  // the other (a token of 16/16 heads 2.4 us for 4.8 with all three); large ones keep even shares.
+  const int common = std::gcd(p.num_heads, p.num_kv_heads);
+  if (target == 2ll * sms && per <= common)
+    while (common % per) ++per;
   const int parts = (rows + per - 1) / per;
   p.rows_per = (rows + parts - 1) / parts;  // (equal shares)
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
