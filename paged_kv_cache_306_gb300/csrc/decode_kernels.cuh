@@ -1098,6 +1098,9 @@ using DecodeArgs = std::conditional_t<kMod, DecodeMaskedParams, DecodeParams>;
 // kMod: capped or biased scores and windows (pa_decode_masked); no fused step, no shared
 // prefixes.  A window of w tokens leaves each sequence the blocks from (L - w) / BS on: they
 // are its work, and nothing before them is looked up or read.
+// What that costs: a capped score a reciprocal and an exponential more, hidden by the copies -- 64 sequences of
+// 512 .. 4096 tokens, 28/4 heads of 128 dims, fp16, cap 50, window 1024 (130 MB to read) take 30 us, a plain call over
+// 1024 tokens each 29; 4 x 32K .. 131K capped (1.46 GB) 226 us, 97% of a copy's rate.
 template <typename T, typename TC, int D, int BS, int kMode, bool kMod>
 __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     decode_kernel(const DecodeArgs<kMod> p) {
