@@ -18,7 +18,7 @@
 //     take 283 us uncapped.  So: the tanh keeps the scores' order, the row's maximum is the raw scores' one, and the cap
 //     becomes an odd polynomial in the raw score within the exponentials' loop, its multiply-adds (128 a clock and SM)
 //     beside the exponentials: 4 terms where all scores of the warp's half chunk lie within cap / 2 (356 us), 6 within
-//     cap (435 us), the exponential form past it.  (Polynomials over all scores first, then the softmax: 403 us for the
+//     cap (394 us), the exponential form past it.  (Polynomials over all scores first, then the softmax: 403 us for the
 //     4 terms; so now only where a mask cuts the half, or with a bias, after which the maximum is another one: 367 us
 //     biased, 496 us capped and biased.)
 //   * Two threads to a row, one for each half of a chunk's keys, which exchange their maxima; each reads
@@ -250,7 +250,7 @@ __device__ __forceinline__ void assign_units(const PrefillMaskedParams& p, const
           for (int i = 0; i < kLoadsPerLane; ++i) k += __popc(__ballot_sync(0xffffffffu, load[i] < t));
           return k;
         };
-        // this round's: those below `t`, then, where the units do not suffice for all below least + w, of those
+        // this turn's: those below `t`, then, where the units do not suffice for all below least + w, of those
         // at `t` the first ones
         int t = least + w, all = below(t), ties = 0;
         if (all > n - done) {
@@ -267,7 +267,7 @@ __device__ __forceinline__ void assign_units(const PrefillMaskedParams& p, const
         for (int i = 0; i < kLoadsPerLane; ++i) {
           const unsigned who = __ballot_sync(0xffffffffu, load[i] < t);
           const unsigned tie = __ballot_sync(0xffffffffu, ties && load[i] == t);
-          auto rank = [&](int l) {  // of cluster l + 32 i among this round's; INT_MAX / 2: not one of them
+          auto rank = [&](int l) {  // of cluster l + 32 i among this turn's; INT_MAX / 2: not one of them
             const unsigned less = (1u << l) - 1;
             return who >> l & 1 ? before + __popc(who & less) : tie >> l & 1 ? tied + __popc(tie & less) : INT_MAX / 2;
           };
