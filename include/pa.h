@@ -406,7 +406,7 @@ PA_API pa_status pa_prefill(void* out, const void* q, const void* k_cache, const
  * first block.  Everything else as in pa_decode_scaled (q_dtype, cache_dtype, scales), without caller
  * partitions; the workspace is pa_decode_masked_workspace_size bytes.  fp32 caches and 16-bit caches
  * with one query head per kv head take the tanh in full fp32 accuracy, the others to
- * 2^-21 of softcap.  With softcap 0, alibi_slopes NULL and window 0 the result is
+ * 2^-20 of its own size, whatever softcap.  With softcap 0, alibi_slopes NULL and window 0 the result is
  * pa_decode_scaled's up to fp32 rounding.
  */
 PA_API size_t pa_decode_masked_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_size,

@@ -256,11 +256,10 @@ int windowed_len(int max_seq_len, int window, int block_size) {
 // A cap is 0 or in a range in which cap * log2(e) and 1 / cap are ordinary fp32 numbers.
 bool softcap_ok(float cap) { return cap == 0.f || (cap >= 0x1p-64f && cap <= 0x1p64f); }
 
-// The factor that brings q.k to the argument of the kernels' softmax, or, capped, of their tanh:
-// s / cap, or, for the tensor-core decode kernels, 2 log2(e) s / cap (by_exp).
-double score_factor(double scale, float softcap, bool by_exp) {
+// The prefill kernels' factor of q.k: to log2 units, or, capped, to the argument of their tanh.
+double score_factor(double scale, float softcap) {
   constexpr double kLog2e = 1.4426950408889634;
-  return softcap == 0.f ? scale * kLog2e : scale / softcap * (by_exp ? 2 * kLog2e : 1.0);
+  return softcap == 0.f ? scale * kLog2e : scale / softcap;
 }
 
 // A fresh tag for every launch, so a launch never mistakes a partial slot left by
@@ -565,10 +564,9 @@ static pa_status decode_impl(void* out, const void* q, const void* k_cache, cons
   p.out_scale = v_scale;
   p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
   if (mod) {
-    p.scale_log2 = static_cast<float>(score_factor(static_cast<double>(scale) * k_scale, mod->softcap,
-                                                   pl.kind != pa::DecodeKind::kSimt));
-    if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale / softcap is not finite");
+    if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale * k_scale is not finite");
     p.cap_log2 = static_cast<float>(mod->softcap * 1.4426950408889634);
+    p.cap_inv = mod->softcap != 0.f ? 1.f / p.cap_log2 : 0.f;
     p.slopes = mod->slopes;
     p.window = mod->window;
   }
@@ -790,7 +788,7 @@ static pa_status prefill_impl(void* out, const void* q, const void* k_cache, con
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
   if (mod) {
-    p.scale_log2 = static_cast<float>(score_factor(scale, mod->softcap, false));
+    p.scale_log2 = static_cast<float>(score_factor(scale, mod->softcap));
     if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale / softcap is not finite");
     p.cap_log2 = static_cast<float>(mod->softcap * 1.4426950408889634);
     p.slopes = mod->slopes;

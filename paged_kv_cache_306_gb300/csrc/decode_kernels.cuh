@@ -178,10 +178,26 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
+// cap tanh(v / cap) of a score v (both in log2 units; inv = 1 / cap), in two forms, so that the error is a share of the
+// score, whatever the cap:
+//   |v / cap| <= 1/2   v tanh(t) / t with t = v / cap (tanh_ratio);
+//   past it            cap - 2 cap / (1 + e^(2 v / cap)), off by 2^-22 of the cap, 2^-21 of the result.  (Of a score far
+//                      below the cap that is nothing to go by: at a cap of 10^6 it was off by 0.25, and at 10^8 every
+//                      score came out as 0.)
+__device__ __forceinline__ float cap_near(float v, float inv) {
+  const float t = v * inv;
+  return v * tanh_ratio(t * t);
+}
+__device__ __forceinline__ float cap_any(float v, float cap, float inv) {
+  const float far = fmaf(-2.f * cap, rcp_approx(1.f + ex2_approx(v * inv * (2.f * kLog2e))), cap);
+  return fabsf(v * inv) <= 0.5f ? cap_near(v, inv) : far;
+}
+
 // kMod (pa_decode_masked): scores are capped and biased before the softmax, and tokens
 // before the window are hidden (see Scores).
 struct Scores {  // of a block, for kMod; unused otherwise
   float cap_log2;   // cap * log2(e); 0: no cap
+  float cap_inv;    // 1 / cap_log2
   int from;         // the block's tokens below this one are hidden
   float base;       // position of the block's first token less that of the query (<= 0)
 };
@@ -409,7 +425,19 @@ struct MmaMath {
 #pragma unroll
         for (int c = 0; c < 4; ++c) sc[mt][n][c] += so[mt][n][c];
     }
-    if constexpr (kMod) {  // hs_ brings scores to log2 units, or, capped, to 2 log2(e) s / cap
+    if constexpr (kMod) {  // hs_ brings scores to log2 units; then the cap, then the bias
+      float size = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            sc[mt][n][c] *= hs_[n][c & 1];
+            size = fmaxf(size, fabsf(sc[mt][n][c]));
+          }
+      // (the second form only where a score of the block is past half the cap: the same values either way)
+      const bool far = ms.cap_log2 != 0.f && __any_sync(0xffffffffu, size * ms.cap_inv > 0.5f);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -417,10 +445,10 @@ struct MmaMath {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int tok = 16 * mt + ((c >> 1) ? tok1 : tok0);
-            float v = sc[mt][n][c] * hs_[n][c & 1];
-            // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)); off by 2^-22 of the cap at most
-            if (ms.cap_log2 != 0.f) v = fmaf(-2.f * ms.cap_log2, rcp_approx(1.f + ex2_approx(v)), ms.cap_log2);
-            sc[mt][n][c] = fmaf(slope_[n][c & 1], ms.base + tok, v);
+            float& v = sc[mt][n][c];
+            if (far) v = cap_any(v, ms.cap_log2, ms.cap_inv);
+            else if (ms.cap_log2 != 0.f) v = cap_near(v, ms.cap_inv);
+            v = fmaf(slope_[n][c & 1], ms.base + tok, v);
           }
     }
     // Online softmax update per head (column), log2 domain; tokens past the sequence
@@ -717,9 +745,9 @@ struct SimtMath {
         for (int k = 0; k < X; ++k) dot = fmaf(qv[gi * X + k], DType<TC>::to_f32(kv[k]), dot);
       }
       dot += __shfl_xor_sync(0xffffffffu, dot, 16);
-      if constexpr (kMod) {  // scale_log2 brings scores to log2 units, or, capped, to s / cap (fp32 pools: tanhf's accuracy)
+      if constexpr (kMod) {  // (fp32 pools: tanhf's accuracy)
         float v = dot * scale_log2;
-        if (ms.cap_log2 != 0.f) v = ms.cap_log2 * tanhf(v);
+        if (ms.cap_log2 != 0.f) v = ms.cap_log2 * tanhf(v * ms.cap_inv);
         v = fmaf(slope_, ms.base + tok, v);
         sc[tp] = tok < rem && tok >= ms.from ? v : -INFINITY;
       } else {
@@ -1511,6 +1539,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     Scores ms{};
     if constexpr (kMod) {
       ms.cap_log2 = p.cap_log2;
+      ms.cap_inv = p.cap_inv;
       ms.from = p.window > 0 ? L - p.window - cj * BS : 0;  // (below 0 past the window's first block)
       ms.base = static_cast<float>(cj * BS - (L - 1));
     }

@@ -94,11 +94,9 @@ struct DecodeParams {
   int members;
 };
 
-// Capped and biased scores, windows (pa_decode_masked).  With a cap, scale_log2 is the
-// factor to the tanh's argument instead: 2 log2(e) scale * k_scale / cap for the
-// tensor-core kernels, scale / cap for the others.
+// Capped and biased scores, windows (pa_decode_masked).
 struct DecodeMaskedParams : DecodeParams {
-  float cap_log2;               // cap * log2(e); 0: no cap
+  float cap_log2, cap_inv;      // cap * log2(e) and its inverse; 0: no cap
   const float* slopes;          // [H]: the score of a token at distance n falls by slopes[h] n; null: no bias
   int window;                   // the last `window` tokens are attended to; 0: all
 };
