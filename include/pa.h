@@ -428,7 +428,8 @@ PA_API pa_status pa_decode_masked(void* out, const void* q, const void* k_cache,
  *              seen by rows before them too (their K/V must be in the cache: the chunk, or an
  *              earlier one, holds them); below 1 none; NULL: none anywhere
  * scale        positive (PA_ERR_INVALID_ARG otherwise)
- * softcap, alibi_slopes, window as in pa_decode_masked, the tanh to 2^-21 of softcap.
+ * softcap, alibi_slopes, window as in pa_decode_masked, the tanh to 2^-20 of its own size or, with
+ *              caps up to 88, to 2^-21 of the cap if that is more.
  *
  * Block-table entries of blocks that end before the window of the sequence's first row may hold
  * anything.  As in pa_prefill, an infinity or NaN in the V of a position that some row of a

@@ -256,12 +256,6 @@ int windowed_len(int max_seq_len, int window, int block_size) {
 // A cap is 0 or in a range in which cap * log2(e) and 1 / cap are ordinary fp32 numbers.
 bool softcap_ok(float cap) { return cap == 0.f || (cap >= 0x1p-64f && cap <= 0x1p64f); }
 
-// The prefill kernels' factor of q.k: to log2 units, or, capped, to the argument of their tanh.
-double score_factor(double scale, float softcap) {
-  constexpr double kLog2e = 1.4426950408889634;
-  return softcap == 0.f ? scale * kLog2e : scale / softcap;
-}
-
 // A fresh tag for every launch, so a launch never mistakes a partial slot left by
 // an earlier launch for its own.  (A call replayed from a graph keeps its tag: there
 // the kernel leaves no slot of a segment unwritten, see its warps without work.)  The sequence starts at a random point, so tags
@@ -788,9 +782,9 @@ static pa_status prefill_impl(void* out, const void* q, const void* k_cache, con
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.test_wait_ns = g_test_wait_ns.load(std::memory_order_relaxed);
   if (mod) {
-    p.scale_log2 = static_cast<float>(score_factor(scale, mod->softcap));
-    if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale / softcap is not finite");
+    if (!std::isfinite(p.scale_log2)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
     p.cap_log2 = static_cast<float>(mod->softcap * 1.4426950408889634);
+    p.cap_inv = mod->softcap != 0.f ? 1.f / p.cap_log2 : 0.f;
     p.slopes = mod->slopes;
     p.window = mod->window;
   }

@@ -211,11 +211,12 @@ cudaError_t launch_prefill(int dtype, int head_size, int block_size, const Prefi
 
 // pa_prefill_masked (prefill_masked.cu).
 struct PrefillMaskedParams : PrefillParams {
-  float cap_log2;                  // cap * log2(e); 0: no cap (with one, scale_log2 is scale / cap)
+  float cap_log2, cap_inv;         // cap * log2(e) and its inverse; 0: no cap
   // With a cap: cap_log2 tanh(scale / cap * s) as odd polynomials of the raw score s, the coefficients of
-  // s, s^3, .. each twice in a pair, and the largest |s| that each is good for.
+  // s, s^3, .. each twice in a pair, and the largest |s| that each is good for (below 0: none).
   uint64_t tanh_near[4], tanh_wide[6];
   float tanh_near_to, tanh_wide_to;
+  float tanh_exp;                  // 2 log2(e) scale / cap (at most 2^126, so that a score of 0 stays 0)
   const float* slopes;             // [H]: the score of a key at distance n falls by slopes[h] n; null: no bias
   int window;                      // a row sees the last `window` positions up to its own; 0: all
   const int32_t* prefix_lens;      // [S]: positions below it are seen by every row; null: none

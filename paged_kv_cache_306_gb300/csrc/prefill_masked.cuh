@@ -18,7 +18,7 @@
 //     take 283 us uncapped.  So: the tanh keeps the scores' order, the row's maximum is the raw scores' one, and the cap
 //     becomes an odd polynomial in the raw score within the exponentials' loop, its multiply-adds (128 a clock and SM)
 //     beside the exponentials: 4 terms where all scores of the warp's half chunk lie within cap / 2 (356 us), 6 within
-//     cap (394 us), the exponential form past it.  (Polynomials over all scores first, then the softmax: 403 us for the
+//     cap (394 us), past it the exponential form (for the scores that need it: cap_any, cap_small).  (Polynomials over all scores first, then the softmax: 403 us for the
 //     4 terms; so now only where a mask cuts the half, or with a bias, after which the maximum is another one: 367 us
 //     biased, 496 us capped and biased.)
 //   * Two threads to a row, one for each half of a chunk's keys, which exchange their maxima; each reads
@@ -86,6 +86,30 @@ __device__ __forceinline__ float smallest(const float (&sv)[N]) {
   return fminf(min3(t[0], t[1], t[2]), min3(min3(t[3], t[4], t[5]), t[6], t[7]));
 }
 
+// 1 / x by the hardware's approximate reciprocal (1 / inf = 0)
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// cap tanh(v / cap) of a score v, both in log2 units, inv = 1 / cap.  Past cap / 2 cap - 2 cap / (1 + e^(2 v / cap)), off
+// by 2^-22 of the cap; a score below it may be small against that, so it goes through tanh_ratio.
+__device__ __forceinline__ float cap_any(float v, float cap, float inv) {
+  const float t = v * inv, far = fmaf(-2.f * cap, rcp(1.f + ex2(t * (2.f * kLog2e))), cap);
+  return fabsf(t) <= 0.5f ? v * tanh_ratio(t * t) : far;
+}
+
+// Up to this cap (in log2 units; 88 in the scores' own) its second form alone is within 2^-15 of every score, less
+// than a weight's rounding, and serves the small scores beside the large ones too: 621 us where cap_any takes 919 (16
+// chunks of 512 tokens behind 3584, 28 heads, scores of twice the cap).
+constexpr float kSmallCap = 128.f;
+// It, of a raw score s; e brings that to 2 log2(e) v / cap.
+__device__ __forceinline__ float cap_small(float s, float e, float cap, float top) {
+  return fmaf(-2.f * cap, rcp(1.f + ex2(s * e)), top);
+}
+
 // The odd polynomial c[0] s + c[1] s^3 + .. of a pair (each coefficient twice in a pair), plus d.
 template <int N>
 __device__ __forceinline__ uint64_t odd_poly(uint64_t x, const uint64_t (&c)[N], uint64_t d) {
@@ -129,14 +153,6 @@ __device__ __forceinline__ void store_rows(uint32_t (&w)[N / 2], T* out, long lo
           make_uint4(w[16 * g + 4 * a], w[16 * g + 4 * a + 1], w[16 * g + 4 * a + 2], w[16 * g + 4 * a + 3]);
   }
 }
-
-// 1 / x by the hardware's approximate reciprocal (1 / inf = 0)
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Unit selection's figures of each sequence, in shared memory (5 kMaxSeqsPerLaunch ints): tokens
 // before the chunk, the chunk's n G query rows, its tiles (the plain kernel's three, see
@@ -461,9 +477,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             sv[j + 1] = v.y;
           }
         } else if (__any_sync(0xffffffffu, size > p.tanh_wide_to)) {
-          const float e = 2.f * kLog2e * p.scale_log2, cap = p.cap_log2;
+          if (p.cap_log2 <= kSmallCap) {
 #pragma unroll
-          for (int j = 0; j < kStep; ++j) sv[j] = fmaf(-2.f * cap, rcp(1.f + ex2(sv[j] * e)), cap);
+            for (int j = 0; j < kStep; ++j) sv[j] = cap_small(sv[j], p.tanh_exp, p.cap_log2, p.cap_log2);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) sv[j] = cap_any(sv[j] * p.scale_log2, p.cap_log2, p.cap_inv);
+          }
         } else {
           const uint64_t zero = f2pack(0.f, 0.f);
 #pragma unroll
@@ -574,18 +594,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Capped without a bias, where the warp's rows see the half whole: the tanh keeps the order of the
             // scores, so the row's maximum is that of the raw ones, and the cap is taken within the exponentials'
             // loop below, by the form that the scores' size allows (so that its multiply-adds run beside the
-            // exponentials).  Elsewhere the scores are changed and hidden first, in TMEM.
-            const bool whole = !__any_sync(0xffffffffu, lo > 0 || lim < kHalf - 1);
-            if (whole && !kBias) {
+            // exponentials).  Elsewhere, and where no form serves all of the scores, they are changed and hidden first,
+            // in TMEM.
+            bool change = kBias || __any_sync(0xffffffffu, lo > 0 || lim < kHalf - 1);
+            if (!change) {
               float sv[kHalf];
               ld64(t_h, sv);
               mx = largest(sv) * sl2;  // (scale > 0 keeps the order)
               if constexpr (kCap) {
                 const float size = fmaxf(mx, -smallest(sv));
-                form = __any_sync(0xffffffffu, size > p.tanh_wide_to) ? 3 : __any_sync(0xffffffffu, size > p.tanh_near_to) ? 2 : 1;
-                mx = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(mx * (2.f * kLog2e * p.scale_log2))), p.cap_log2);
+                const bool past = __any_sync(0xffffffffu, size > p.tanh_wide_to);
+                change = past && p.cap_log2 > kSmallCap;
+                form = past ? 3 : __any_sync(0xffffffffu, size > p.tanh_near_to) ? 2 : 1;
+                mx = cap_any(mx * p.scale_log2, p.cap_log2, p.cap_inv);
               }
-            } else {
+            }
+            if (change) {
+              form = 0;
+              mx = -INFINITY;
 #pragma unroll 1
               for (int k0 = 0; k0 < kHalf; k0 += kStep) {
                 float sv[kStep];
@@ -656,11 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_p([&](uint64_t x) { return odd_poly(x, p.tanh_near, negm2); });
               } else if (form == 2) {
                 store_p([&](uint64_t x) { return odd_poly(x, p.tanh_wide, negm2); });
-              } else if (form == 3) {  // cap - 2 cap / (1 + e^(2 s / cap))
-                const float e = 2.f * kLog2e * p.scale_log2, top = p.cap_log2 - mref, cap2 = -2.f * p.cap_log2;
+              } else if (form == 3) {
+                const float e = p.tanh_exp, cap = p.cap_log2, top = p.cap_log2 - mref;
                 store_p([&](uint64_t x) {
                   const float2 v = f2unpack(x);
-                  return f2pack(fmaf(cap2, rcp(1.f + ex2(v.x * e)), top), fmaf(cap2, rcp(1.f + ex2(v.y * e)), top));
+                  return f2pack(cap_small(v.x, e, cap, top), cap_small(v.y, e, cap, top));
                 });
               }
             }

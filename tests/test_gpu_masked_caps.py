@@ -79,3 +79,41 @@ def test_decode_scales_that_a_small_cap_divides(pa):
         assert pa.pa_get_device_error() == 0
         ref = masked.decode(f64(q), *pools.exact(), pools.table, pools.lens, scale, 16, softcap=cap)
         check_rows(out, ref, q, pools, scale, cap)
+
+
+@pytest.mark.parametrize("caps", CAPS, ids=lambda c: "-".join(f"{x:g}" for x in c))
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_prefill_caps(pa, dtype, caps):
+    """Chunks that the rows see whole, chunks that the diagonal or a window cuts, and biased ones."""
+    cap, size, other = caps
+    for group, hkv, d, bs, kw in ((4, 2, 64, 16, dict()), (1, 1, 128, 32, dict(window=200)), (7, 1, 128, 16, dict(alibi=True))):
+        ctx, news = [600, 3], [70, 150]
+        lens = [a + b for a, b in zip(ctx, news)]
+        pools = Pools(lens, hkv, d, bs, dtype, group)
+        h = group * hkv
+        q = mixed_queries(sum(news), h, d, dtype, group + 1, size, other)
+        sl = slopes_of(h) if kw.get("alibi") else None
+        starts = np.concatenate(([0], np.cumsum(news))).astype(np.int32)
+        out = torch.empty_like(q).cuda()
+        kc, vc, bt = pools.on("cuda")
+        pa.pa_prefill_masked(out, q.cuda(), kc, vc, bt, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                             torch.from_numpy(starts).cuda(), d ** -0.5, max(lens), cap,
+                             None if sl is None else torch.from_numpy(sl).cuda(), kw.get("window", 0))
+        assert pa.pa_get_device_error() == 0
+        ref = masked.prefill(f64(q), *pools.exact(), pools.table, lens, starts, d ** -0.5, bs, softcap=cap, slopes=sl,
+                             window=kw.get("window", 0))
+        check_rows(out, ref, q, pools, d ** -0.5, cap, float(max(lens)) if sl is not None else 0.0, dtype, f"group {group}")
+
+
+def test_prefill_scales_that_a_small_cap_divides(pa):
+    pools = Pools([140, 9], 1, 64, 16, "f16", 5)
+    kc, vc, bt = pools.on("cuda")
+    lens = torch.tensor(pools.lens, dtype=torch.int32, device="cuda")
+    starts = np.array([0, 100, 109], np.int32)
+    q = queries(109, 4, 64, "f16", 6)
+    for scale, cap in ((2.0 ** 70, 2.0 ** -64), (2.0 ** -70, 2.0 ** 64), (2.0 ** 30, 2.0 ** 40), (2.0 ** -30, 2.0 ** -20)):
+        out = torch.empty_like(q).cuda()
+        pa.pa_prefill_masked(out, q.cuda(), kc, vc, bt, lens, torch.from_numpy(starts).cuda(), scale, 140, cap)
+        assert pa.pa_get_device_error() == 0
+        ref = masked.prefill(f64(q), *pools.exact(), pools.table, pools.lens, starts, scale, 16, softcap=cap)
+        check_rows(out, ref, q, pools, scale, cap)
