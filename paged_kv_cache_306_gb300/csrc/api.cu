@@ -193,7 +193,7 @@ pa_status make_plan(int num_seqs, int num_heads, int num_kv_heads, int head_size
                     int partition_size, pa_dtype dtype, DecodePlan* pl, bool shared = false, bool masked = false) {
   const int group = num_heads / num_kv_heads;
   pl->members = shared ? shared_members(dtype, num_heads, num_kv_heads) : 0;
-  if (pl->members && (max_seq_len + block_size - 1) / block_size >= (1 << pa::kInfoOffBits))
+  if (pl->members && ceil_div(max_seq_len, block_size) >= (1 << pa::kInfoOffBits))
     return fail(PA_ERR_UNSUPPORTED, "shared prefixes: at most %d blocks per sequence", (1 << pa::kInfoOffBits) - 1);
   pl->kind = pl->members ? (dtype == PA_FP8_E4M3 ? pa::DecodeKind::kMma8 : pa::DecodeKind::kMma16)
                          : pa::decode_kind(static_cast<int>(dtype), group);

@@ -924,6 +924,12 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, int& kv
   }
 }
 
+// Blocks of L >= 0 tokens (the sum unsigned: L may be 2^31 - 1).
+template <int BS>
+__device__ __forceinline__ int blocks_of(int L) {
+  return static_cast<int>((static_cast<unsigned>(L) + (BS - 1)) / BS);
+}
+
 // Segment and block of global work position g (g < T): the sequence s with
 // units * pre[s] <= g < units * pre[s + 1] (empty sequences are skipped because
 // their prefix equals the next one's), then the unit and the block within it.
@@ -1198,7 +1204,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       int L = i < S ? __ldg(p.seq_lens + i) : 0;
       if (L < 1 || L > p.max_seq_len) L = 0;
       if (i < S) s_len[i] = L;
-      nb[k] = (L + BS - 1) / BS - first_block(L);
+      nb[k] = blocks_of<BS>(L) - first_block(L);
     }
     if (shared) {
       shared_layout<PER>(p, s_pre, s_info, s_lead, s_wsum, nb, wt, tid, warp, lane);
@@ -1434,7 +1440,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
           if (j < info_off(s_info[s + m]) && __ldg(bt + (long long)(s + m) * p.max_blocks_per_seq + j) != phys)
             set_error(p.err, kErrShared);
       }
-      const bool last_blk = !in_shared && j == (s_len[s] + BS - 1) / BS - 1;
+      const bool last_blk = !in_shared && j == blocks_of<BS>(s_len[s]) - 1;
       kvh |= (s << 16) | (static_cast<int>(last_blk) << 30);
     }
   };
@@ -1497,7 +1503,7 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   bool folded = false;     // earlier partitions of this piece are in the running state
   auto enter = [&]() {
     L = s_len[cs];
-    nblk = (L + BS - 1) / BS;
+    nblk = blocks_of<BS>(L);
     unit_heads<kMma>(p, cu, kvh, h0, nh);
     jstart = first_block(L);
     jend = nblk;
