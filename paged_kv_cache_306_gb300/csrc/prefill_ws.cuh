@@ -389,7 +389,7 @@ __device__ __forceinline__ UnitView unit_view(const PrefillParams& p, int4 u, ui
   v.ctx = v.L - n;
   const int p_max = v.ctx + (unit_hi - 1) / G;  // last position any row of the unit has
   v.nblk = p_max / BS + 1;                      // blocks holding keys 0..p_max
-  v.nchunks = (p_max + kKeys) / kKeys;
+  v.nchunks = p_max / kKeys + 1;
   return v;
 }
 
@@ -533,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = U.pair_lo + X * kRows + r;
         const bool valid = row < U.pair_hi;
         const int pos = valid ? U.ctx + row / G : U.ctx + (U.pair_hi - 1) / G;  // a padding row behaves as a real one
-        const int kz = min(U.L, U.nblk * BS);  // first key whose V must read as zero
+        // first key whose V must read as zero (the blocks' end as an unsigned number: it may be 2^31)
+        const int kz = static_cast<int>(min(static_cast<unsigned>(U.L), static_cast<unsigned>(U.nblk) * BS));
         float m = -INFINITY, l = 0.f;
         for (int c = 0; c < U.nchunks; ++c, ++cx) {
           // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // the last chunk: V of keys past the sequence (or past the blocks loaded) reads as
           // zero; tile A's threads clear it before either tile's P V of the chunk is issued
-          if (X == 0 && c == U.nchunks - 1 && kz < (c + 1) * kKeys) {
+          if (X == 0 && c == U.nchunks - 1 && kz - c * kKeys < kKeys) {
             const int gc = g + c;
             if (!(ok = __all_sync(0xffffffffu, wait(&fullv[gc % kVStages], (gc / kVStages) & 1)))) break;
             // block b's tile [D][bs]: dim d's keys 8 g .. 8 g + 7 are the 16 bytes at d * 2 bs + 16 g

@@ -55,3 +55,28 @@ def test_decode_at_the_longest_lengths(pa, dtype, bs, ends, window):
             ref = masked.decode(f64(q), *pools.exact(), pools.table, lens, 0.125, bs, softcap=9.0, window=window,
                                 slopes=slopes)
             check_rows(out, ref, q, pools, 0.125, 9.0, 64.0 if slopes is not None else 0.0, dtype)
+
+
+@pytest.mark.parametrize("window", [1, 50, 64])
+@pytest.mark.parametrize("dtype,bs,ends", CASES[:2], ids=lambda x: str(x))
+def test_prefill_at_the_longest_lengths(pa, dtype, bs, ends, window):
+    long_lens = [BIG - e for e in ends] + [100, 1]
+    lens = [big if big < 1000 else 96 + big % bs for big in long_lens]
+    news = [30, 1, 7, 100, 1]
+    starts = np.concatenate(([0], np.cumsum(news))).astype(np.int32)
+    # (V past a sequence's end is NaN in the pools: it may not reach a row)
+    for group, cap in ((4, 9.0), (1, 0.0)):
+        pools = Pools(lens, 2, 64, bs, dtype, group)
+        kc, vc, _ = pools.on("cuda")
+        q = queries(sum(news), 2 * group, 64, dtype, group + 1)
+        sl = slopes_of(2 * group)
+        for slopes in (None, sl):
+            out = torch.full_like(q, 99.0).cuda()
+            pa.pa_prefill_masked(out, q.cuda(), kc, vc, long_table(pools, long_lens),
+                                 torch.tensor(long_lens, dtype=torch.int32, device="cuda"),
+                                 torch.from_numpy(starts).cuda(), 0.125, BIG, cap,
+                                 None if slopes is None else torch.from_numpy(slopes).cuda(), window)
+            assert pa.pa_get_device_error() == 0
+            ref = masked.prefill(f64(q), *pools.exact(), pools.table, lens, starts, 0.125, bs, softcap=cap,
+                                 window=window, slopes=slopes)
+            check_rows(out, ref, q, pools, 0.125, cap, 64.0 if slopes is not None else 0.0, dtype)
