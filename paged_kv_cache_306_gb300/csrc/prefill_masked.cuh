@@ -200,8 +200,8 @@ __device__ __forceinline__ void masked_keys(int window, int prefix, int ctx, int
 // least work so far, as the plain kernel's; every warp that calls it replays the same sequence, and mine(sequence,
 // kv head, unit) is called for the units of cluster `cid` until it returns false.
 //   * A prefix makes all units of its sequence read at least its chunks; a window bounds what any
-//     unit reads, so that all units that would read that much or more come first, together
-//     (there is no walk over a long context's chunks).
+//     unit reads (with prefixes, what any sequence's rows see), so that all units that would read that much or more
+//     come first, together (there is no walk over a long context's chunks).
 //   * The units that read as many chunks, of 32 sequences and all kv heads, are given out in rounds: every
 //     cluster whose work is below the least one's plus a unit's gets one (the least loaded ones, where the units do
 //     not suffice), which is what giving them one by one to the least loaded comes to.  One by one, a unit took
@@ -217,14 +217,20 @@ __device__ __forceinline__ void assign_units(const PrefillMaskedParams& p, const
   for (int i = 0; i < kLoadsPerLane; ++i) load[i] = lane + 32 * i < ncl ? 0 : INT_MAX;
   int top = longest;
   if (p.prefix_lens) {
-    for (int s = lane; s < S; s += 32) top = max(top, (tab[3 * kMaxSeqsPerLaunch + s] + kKeys - 1) / kKeys);
-    top = __reduce_max_sync(0xffffffffu, top);
+    int seen = 1;
+    for (int s = lane; s < S; s += 32) {
+      const int prefix = tab[3 * kMaxSeqsPerLaunch + s], rows = tab[kMaxSeqsPerLaunch + s], ctx = tab[s];
+      top = max(top, prefix / kKeys + (prefix % kKeys != 0));
+      const int lo = p.window > 0 ? max(0, ctx - (p.window - 1)) : 0;
+      if (rows) seen = max(seen, max(ctx + (rows - 1) / G, prefix - 1) / kKeys - lo / kKeys + 1);
+    }
+    top = min(__reduce_max_sync(0xffffffffu, top), __reduce_max_sync(0xffffffffu, seen));
   } else if (p.window > 0) {  // what a unit's rows and the window before them span
     top = static_cast<int>(min((long long)top, ((long long)p.window + (kUnitTiles * kRows - 1) / G) / kKeys + 2));
   }
   auto reading = [&](int s, int x) {  // units of sequence s, per kv head, that would read >= x chunks without a window
     const int prefix = tab[3 * kMaxSeqsPerLaunch + s];
-    if (x <= (prefix + kKeys - 1) / kKeys) return (tab[2 * kMaxSeqsPerLaunch + s] + kUnitTiles - 1) / kUnitTiles;
+    if (x <= prefix / kKeys + (prefix % kKeys != 0)) return (tab[2 * kMaxSeqsPerLaunch + s] + kUnitTiles - 1) / kUnitTiles;
     return units_reading(tab, G, s, x);
   };
   for (int x = top; x >= 1; --x) {

@@ -80,3 +80,26 @@ def test_prefill_at_the_longest_lengths(pa, dtype, bs, ends, window):
             ref = masked.prefill(f64(q), *pools.exact(), pools.table, lens, starts, 0.125, bs, softcap=cap,
                                  window=window, slopes=slopes)
             check_rows(out, ref, q, pools, 0.125, cap, 64.0 if slopes is not None else 0.0, dtype)
+
+
+@pytest.mark.parametrize("dtype,bs,ends", CASES[:2], ids=lambda x: str(x))
+def test_prefill_at_the_longest_lengths_with_windows_and_prefixes(pa, dtype, bs, ends):
+    """Prefixes that end before the window, within the chunk and past the sequence."""
+    window = 60
+    long_lens = [BIG - e for e in ends] + [100, 1]
+    lens = [big if big < 1000 else 96 + big % bs for big in long_lens]
+    news = [30, 25, 7, 100, 1]
+    starts = np.concatenate(([0], np.cumsum(news))).astype(np.int32)
+    cut = [big - n for big, n in zip(long_lens, lens)]
+    for prefixes in ([10, long_lens[1] - 10, BIG, 60, 0], [long_lens[0] - 20, 0, 3, 100, -7]):
+        short = [min(max(x - c, 0), n) for x, c, n in zip(prefixes, cut, lens)]
+        pools = Pools(lens, 2, 64, bs, dtype, 8)
+        kc, vc, _ = pools.on("cuda")
+        q = queries(sum(news), 8, 64, dtype, 9)
+        out = torch.full_like(q, 99.0).cuda()
+        pa.pa_prefill_masked(out, q.cuda(), kc, vc, long_table(pools, long_lens),
+                             torch.tensor(long_lens, dtype=torch.int32, device="cuda"), torch.from_numpy(starts).cuda(),
+                             0.125, BIG, 9.0, None, window, torch.tensor(prefixes, dtype=torch.int32, device="cuda"))
+        assert pa.pa_get_device_error() == 0
+        ref = masked.prefill(f64(q), *pools.exact(), pools.table, lens, starts, 0.125, bs, short, softcap=9.0, window=window)
+        check_rows(out, ref, q, pools, 0.125, 9.0, 0.0, dtype)
