@@ -351,7 +351,8 @@ PA_API uint64_t pa_launch_count(void);
  * stays usable.  While `nanoseconds` > 0, decode, the fused step and prefill
  * launched afterwards make their first pipeline wait (per decode warp, per
  * prefill CTA) on a barrier that nothing completes, for that long, so that this
- * path runs for real (pa_decode_fp4: its waits for other CTAs).  0 (the default) restores normal operation.  The setting
+ * path runs for real (pa_decode_fp4: its waits for other CTAs; pa_decode_masked with an odd
+ * number of them: only the warp that takes a launch's first block).  0 (the default) restores normal operation.  The setting
  * is process-wide and is read when a call enqueues its kernels.
  */
 PA_API void pa_set_test_wait_limit(uint64_t nanoseconds);

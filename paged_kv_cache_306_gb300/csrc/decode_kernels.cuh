@@ -1069,13 +1069,14 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
 // most two that do not hold their whole segment, its first and its last; the last one (or the only one) lies in the
 // warp's ring, whose copies have all been used by then, the other where caller partitions would keep
 // their running state (there are none).  s_piece[2 w], s_piece[2 w + 1]: the segments of warp w's pieces in the state
-// and in the ring, -1: none.  (A launch that small is all latency: one short sequence took 6.4 us with the merge as a
+// and in the ring, -1: none; s_piece[2 warps]: a warp's wait ran out, so that pieces are missing, and nothing is merged.  (A launch that small is all latency: one short sequence took 6.4 us with the merge as a
 // kernel of its own, 5.1 with it here.)
 template <typename T, int D, bool kMma, int kRows>
 __device__ __forceinline__ void merge_here(const DecodeParams& p, const int* s_piece, const float* states, const unsigned char* rings,
                                            int ring_bytes, int warp, int warps, int lane) {
   constexpr int CPL = D / 32;  // head dims per lane
   asm volatile("bar.sync 0;" ::: "memory");  // warps come here from two places
+  if (s_piece[2 * warps]) return;
   for (int row = warp; row < p.num_seqs * p.num_heads; row += warps) {
     const int s = row / p.num_heads, h = row - s * p.num_heads;
     int u = h, r = 0;  // the head unit of h and h's row within it
@@ -1170,7 +1171,9 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   const bool alone = kMod && gridDim.x == 1;
   int* s_piece = s_info;  // (no shared prefixes with kMod)
   static_assert(!kMod || kRows * (D + 2) * 4 <= STAGES * 2 * TILE, "a piece in its warp's ring");
+  static_assert(2 * kDecodeWarps + 1 <= kMaxSeqsPerLaunch, "s_piece in s_info's place");
   if (alone && lane < 2) s_piece[2 * warp + lane] = -1;
+  if (alone && tid == 0) s_piece[2 * kDecodeWarps] = 0;  // (a barrier of the prologue lies before any other write)
   auto merge = [&]() {
     merge_here<T, D, kMma, kRows>(p, s_piece, st_o - warp * kRows * (D + 2), smem, STAGES * 2 * TILE, warp, kDecodeWarps, lane);
   };
@@ -1528,9 +1531,14 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     if constexpr (kMod) math.load_slopes(p.slopes ? p.slopes + h0 : nullptr, nh);
   };
   enter();
+  // (an odd limit: only the warp with the first block waits in vain, see pa_set_test_wait_limit)
+  const unsigned long long test_ns = kMod && (p.test_wait_ns & 1) && start > 0 ? 0 : p.test_wait_ns;
 
   for (int k = 0; k < len; ++k) {
-    if (!wait_stage<STAGES>(bars, never, p.test_wait_ns, k, len, p.err, lane)) break;
+    if (!wait_stage<STAGES>(bars, never, test_ns, k, len, p.err, lane)) {
+      if (alone && lane == 0) s_piece[2 * kDecodeWarps] = 1;
+      break;
+    }
     unsigned char* stage = ring + (k % STAGES) * 2 * TILE;
     // valid tokens in this block (>= 1); a shared block is full for every member that takes it
     const int rem = part == 0 ? BS : L - cj * BS;
