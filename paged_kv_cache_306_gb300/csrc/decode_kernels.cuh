@@ -955,6 +955,19 @@ __device__ __forceinline__ void locate(long long g, const int* pre, int S, int U
 }
 
 
+// What the schedule is made of, of sequences tid + k * (the CTA's threads): the lengths and, with shared prefixes,
+// prefix_group and prefix_blocks.
+template <int PER>
+struct DecodeInputs {
+  int len[PER], group[PER], blocks[PER];
+  __device__ __forceinline__ bool differs(const DecodeInputs& o) const {
+    bool d = false;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) d |= len[k] != o.len[k] || group[k] != o.group[k] || blocks[k] != o.blocks[k];
+    return d;
+  }
+};
+
 // Shared prefixes: the clusters and the work of each sequence (see DecodeParams).
 // On entry nb[k] holds the blocks of sequence tid * PER + k; on exit its blocks of
 // work per unit -- a leader's: its cluster's shared segment plus its own blocks;
@@ -968,7 +981,7 @@ __device__ __forceinline__ void locate(long long g, const int* pre, int S, int U
 //   the cluster's shared segment is its first B blocks, read through the table of
 //   the member with the largest prefix_blocks (the donor).
 // wt[k] receives the cost of the sequence's work per unit (see kSegCost).
-// s_pre and s_red are scratch here.
+// s_pre and s_red are scratch here; s_lead and s_info hold prefix_group and prefix_blocks on entry.
 template <int PER>
 __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre, int* s_info, int* s_lead,
                                               int* s_red, int (&nb)[PER], int (&wt)[PER], int tid, int warp,
@@ -990,9 +1003,8 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
     bool link = false;
     int sh = 0;
     if (i < S && nb[k] > 0) {
-      const int gi = __ldg(p.prefix_group + i), pb = __ldg(p.prefix_blocks + i);
-      link = i > 0 && s_pre[i - 1] > 0 && __ldg(p.prefix_group + i - 1) == gi;
-      sh = max(0, min(pb, nb[k] - 1));
+      link = i > 0 && s_pre[i - 1] > 0 && s_lead[i - 1] == s_lead[i];
+      sh = max(0, min(s_info[i], nb[k] - 1));
     }
     if (i < S) s_info[i] = sh | (link ? kLinkBit : 0);
     if (!link) run = i;
@@ -1186,27 +1198,57 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
   __syncwarp();
   griddep_launch_dependents();
 
-  // Per-sequence tables: length (0 when outside [1, max_seq_len]) and prefix sums
-  // of the blocks of work per unit.  Each thread scans PER consecutive sequences.
-  // They come from seq_lens and the prefix groups, which no kernel of this library
-  // writes, so they are built while the previous kernel in the stream may still be
-  // running (see griddep_wait below).
+  // The schedule is made of the lengths and prefix groups, while the previous kernel in the stream may still be
+  // running.  Should that kernel have written them, its writes are in order with these reads only behind
+  // griddep_wait: there they are read again, and where anything reads differently the schedule is made anew.
+  // (Neighbouring threads read neighbouring numbers: what all CTAs read at once comes from a few lines of L2.)
+  constexpr int PER = (kMaxSeqsPerLaunch + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
   const int S = p.num_seqs, U = p.units, PB = p.part_blocks;
   const bool shared = kMma && !kMod && p.shared, fused = !kMod && p.fused;
+  auto read_inputs = [&](DecodeInputs<PER>& in) {
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = tid + k * kDecodeWarps * 32;
+      in.len[k] = i < S ? ld_now(p.seq_lens + i) : 0;
+      in.group[k] = shared && i < S ? ld_now(p.prefix_group + i) : 0;
+      in.blocks[k] = shared && i < S ? ld_now(p.prefix_blocks + i) : 0;
+    }
+  };
   // the first block of a sequence of L tokens that its window reaches
   auto first_block = [&](int L) {
     if constexpr (kMod) return p.window > 0 ? max(0, L - p.window) / BS : 0;
     return 0;
   };
-  {
-    constexpr int PER = (kMaxSeqsPerLaunch + kDecodeWarps * 32 - 1) / (kDecodeWarps * 32);
+  // segment ids: one per (sequence, unit), or two with shared prefixes (the shared part, then the own part)
+  auto seg_id = [&](int s, int u, int part) { return shared ? 2 * (s * U + u) + part : s * U + u; };
+  // blocks of sequence s's shared segment (s a leader), else 0
+  auto shared_len = [&](int s) { return info_member(s_info[s]) == 0 ? info_off(s_lead[s]) : 0; };
+
+  const int W = gridDim.x * kDecodeWarps;
+  const int w = blockIdx.x * kDecodeWarps + warp;
+  // This warp's range of the T_all blocks of work: an equal share of their cost (blocks,
+  // shared blocks and segments weighted as kSegCost says).
+  long long T_all, start, end;
+  DecodeInputs<PER> in;
+  read_inputs(in);
+  for (bool waited = false;; waited = true) {
+    // Per-sequence tables: length (0 when outside [1, max_seq_len]) and prefix sums
+    // of the blocks of work per unit.  Each thread scans PER consecutive sequences.
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int i = tid + k * kDecodeWarps * 32;
+      if (i >= S) continue;
+      s_len[i] = in.len[k] < 1 || in.len[k] > p.max_seq_len ? 0 : in.len[k];
+      if (shared) {
+        s_lead[i] = in.group[k];
+        s_info[i] = in.blocks[k];
+      }
+    }
+    __syncthreads();
     int nb[PER], wt[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
-      const int i = tid * PER + k;
-      int L = i < S ? __ldg(p.seq_lens + i) : 0;
-      if (L < 1 || L > p.max_seq_len) L = 0;
-      if (i < S) s_len[i] = L;
+      const int i = tid * PER + k, L = i < S ? s_len[i] : 0;
       nb[k] = blocks_of<BS>(L) - first_block(L);
     }
     if (shared) {
@@ -1257,21 +1299,60 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
       s_wpre[S] = ow;
     }
     __syncthreads();
-  }
-  // segment ids: one per (sequence, unit), or two with shared prefixes (the shared part, then the own part)
-  auto seg_id = [&](int s, int u, int part) { return shared ? 2 * (s * U + u) + part : s * U + u; };
-  // blocks of sequence s's shared segment (s a leader), else 0
-  auto shared_len = [&](int s) { return info_member(s_info[s]) == 0 ? info_off(s_lead[s]) : 0; };
 
-  // Everything from here on may touch memory the previous kernel in the stream
-  // writes (the pools, the output, the workspace a previous call's merge still reads).
-  griddep_wait();
+    // the range
+    T_all = (long long)s_pre[S] * U;
+    const long long Tw = (long long)s_wpre[S] * U;
+    const bool small = kMod && Tw <= INT_MAX;  // 32-bit divisions (see locate)
+    auto div = [&](long long a, int b) -> long long {
+      return small ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+    };
+    // the first block whose cost starts at or after t
+    auto block_at = [&](long long t) -> long long {
+      if (t >= Tw) return T_all;
+      int lo = 0, hi = S - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((long long)s_wpre[mid] * U <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const int s = lo, wl = s_wpre[s + 1] - s_wpre[s], nbl = s_pre[s + 1] - s_pre[s];
+      const long long r = t - (long long)s_wpre[s] * U;
+      const int u = static_cast<int>(div(r, wl)), rr = static_cast<int>(r - (long long)u * wl);
+      // a unit's cost: [segment, shared blocks] (a leader with a shared part), segment, own blocks
+      const int B = shared ? shared_len(s) : 0;
+      const int wS = B > 0 ? kSegCost + kSharedCost * B : 0;
+      const int j = rr < wS ? max(0, rr - kSegCost + kSharedCost - 1) / kSharedCost
+                            : B + max(0, rr - wS - kSegCost + kOwnCost - 1) / kOwnCost;
+      return (long long)s_pre[s] * U + (long long)u * nbl + j;
+    };
+    const long long qt = div(Tw, W), rt = Tw - qt * W;
+    start = block_at(w * qt + div(w * rt, W));
+    end = block_at((w + 1) * qt + div((w + 1) * rt, W));
+    // Everything from here on may touch memory the previous kernel in the stream
+    // writes (the pools, the output, the workspace a previous call's merge still reads).
+    bool again = false;
+    DecodeInputs<PER> now = in;
+    if (!waited) {
+      griddep_wait();
+      read_inputs(now);
+      again = now.differs(in);
+    }
+    // (and every warp has its range: the side buffers may now receive copies)
+    if (!__syncthreads_or(again)) break;
+    in = now;
+  }
 
   // Sequences outside the contract: record the error, zero their rows, mark their
   // segments as needing no merge.  One CTA does it, and hands the cluster layout
   // to the merge kernel.
   if (blockIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      bad |= tid + k * kDecodeWarps * 32 < S && (in.len[k] < 1 || in.len[k] > p.max_seq_len);
+    bad = __syncthreads_or(bad);  // (a look at each sequence in turn takes ~100 clocks a sequence)
+    for (int s = 0; bad && s < S; ++s) {
       if (s_len[s] != 0) continue;
       if (tid == 0) set_error(p.err, kErrSeqLen);
       T* out = static_cast<T*>(p.out) + (long long)s * p.num_heads * D;
@@ -1284,9 +1365,6 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
         p.seq_info[S + s] = s_lead[s];
       }
   }
-
-  const int W = gridDim.x * kDecodeWarps;
-  const int w = blockIdx.x * kDecodeWarps + warp;
 
   // The fused step's pool writes: item i = (sequence, kv head) of the launch goes
   // to warp i mod W.  A batch of items is loaded before any of it is stored (the
@@ -1365,40 +1443,6 @@ __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     }
   };
 
-  // This warp's range of the T blocks of work: an equal share of their cost (blocks,
-  // shared blocks and segments weighted as kSegCost says).
-  const long long T_all = (long long)s_pre[S] * U;
-  long long start, end;
-  {
-    const long long Tw = (long long)s_wpre[S] * U;
-    const bool small = kMod && Tw <= INT_MAX;  // 32-bit divisions (see locate)
-    auto div = [&](long long a, int b) -> long long {
-      return small ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
-    };
-    // the first block whose cost starts at or after t
-    auto block_at = [&](long long t) -> long long {
-      if (t >= Tw) return T_all;
-      int lo = 0, hi = S - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((long long)s_wpre[mid] * U <= t) lo = mid;
-        else hi = mid - 1;
-      }
-      const int s = lo, wl = s_wpre[s + 1] - s_wpre[s], nbl = s_pre[s + 1] - s_pre[s];
-      const long long r = t - (long long)s_wpre[s] * U;
-      const int u = static_cast<int>(div(r, wl)), rr = static_cast<int>(r - (long long)u * wl);
-      // a unit's cost: [segment, shared blocks] (a leader with a shared part), segment, own blocks
-      const int B = shared ? shared_len(s) : 0;
-      const int wS = B > 0 ? kSegCost + kSharedCost * B : 0;
-      const int j = rr < wS ? max(0, rr - kSegCost + kSharedCost - 1) / kSharedCost
-                            : B + max(0, rr - wS - kSegCost + kOwnCost - 1) / kOwnCost;
-      return (long long)s_pre[s] * U + (long long)u * nbl + j;
-    };
-    const long long qt = div(Tw, W), rt = Tw - qt * W;
-    start = block_at(w * qt + div(w * rt, W));
-    end = block_at((w + 1) * qt + div((w + 1) * rt, W));
-    __syncthreads();  // every warp has its range: the side buffers may now receive copies
-  }
   const int len = static_cast<int>(end - start);
   if (len <= 0) {
     // This warp's slot may lie between the first and the last piece of the segment at `start`: it is marked as

@@ -106,13 +106,6 @@ __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_g
 template <int N>  // all but the last N groups of this lane's copies have landed
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The value in memory at this moment, whatever an earlier load of this kernel saw.
-__device__ __forceinline__ int ld_now(const int32_t* p) {
-  int v;
-  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ uint64_t ld_acquire(const uint64_t* p) {
   uint64_t v;
   asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");

@@ -35,13 +35,21 @@ __device__ __forceinline__ void set_error(unsigned* err, unsigned code) {
 // Every kernel of the library is launched so that it may become resident while
 // the previous kernel of the stream is still running.  Before it touches any
 // memory it waits for that kernel to finish and for its writes to be visible
-// (griddep_wait); as soon as it starts it lets the next kernel do the same
+// (griddep_wait; what the decode kernels read for their schedules before it they read
+// again behind it); as soon as it starts it lets the next kernel do the same
 // (griddep_launch_dependents).  A kernel never waits on a later one, so the
 // chain cannot deadlock.
 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The value in memory at this moment, whatever an earlier load of this kernel saw.
+__device__ __forceinline__ int ld_now(const int32_t* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
 template <typename... KArgs, typename... Args>
