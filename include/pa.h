@@ -448,8 +448,8 @@ PA_API pa_status pa_prefill_masked(void* out, const void* q, const void* k_cache
  * position p turns pair i of the first rotary_dim dims of each of its q and key heads,
  *     x' = amplitude * (x cos a - y sin a),  y' = amplitude * (x sin a + y cos a),  a = p * inv_freq[i],
  * the pair (x, y) being dims (i, i + rotary_dim / 2) for PA_ROPE_HALVES and (2 i, 2 i + 1) for
- * PA_ROPE_PAIRS; the other dims are copied.  Angles are exact to 2^-52 of themselves, whatever
- * the position; cosines, sines and products are fp32, and each element is rounded once
+ * PA_ROPE_PAIRS; the other dims are copied.  The angle of position p is off by at most
+ * |p| 2^-65 turns, whatever the frequency; cosines, sines and products are fp32, and each element is rounded once
  * (an FP8 code from the fp32 value).
  *
  * q, key, value  rows [num_tokens] of num_heads, num_kv_heads and num_kv_heads heads of head_size
@@ -459,7 +459,7 @@ PA_API pa_status pa_prefill_masked(void* out, const void* q, const void* k_cache
  *                row's elements), else it overlaps no input, from its first to its last row
  *                (PA_ERR_INVALID_ARG otherwise).  Every token's q is turned, padding tokens' too.
  * positions      int64 [num_tokens], any values
- * inv_freq       double [rotary_dim / 2] in device memory, finite: radians per position
+ * inv_freq       double [rotary_dim / 2] in device memory, below 2^32 in size: radians per position
  *                (pa_rope_frequencies computes them)
  * head_size 64 or 128; rotary_dim a multiple of 16 (PA_ERR_UNSUPPORTED otherwise); rows fp32,
  * fp16 or bf16.

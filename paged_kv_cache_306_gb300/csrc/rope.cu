@@ -10,8 +10,7 @@
 // The angle.  Positions are whole numbers, so the angle is taken in turns and fixed
 // point: with F_i = f_i / 2 pi as a 64-bit fraction of a turn, p F_i mod 2^64 is the
 // product's low word -- the reduction to one turn costs nothing and is exact for every
-// position, and the error is that of F_i alone, |p| 2^-65 turns (plus the rounding of f_i / 2 pi
-// beyond 2^-53 of it).  What is left after the nearest quarter turn lies within 1/8 turn, so as
+// position, and the error is that of F_i alone, which is rounded once: |p| 2^-65 turns, whatever f_i.  What is left after the nearest quarter turn lies within 1/8 turn, so as
 // fp32 it is off by at most 2^-28 turns, and sincospif finishes it.  (fp64 per token and pair
 // would be bound by this GPU's fp64 rate; f_i / 2 pi is computed in fp64 once per CTA.)
 //
@@ -46,7 +45,7 @@ constexpr int kRopeBatch = 2;  // units per thread in flight
 constexpr int kRopeValueRows = 4;               // rows of q that a row of v counts as (see launch_rope)
 constexpr int kRopeBusy = 7, kRopeMost = 9;     // units a thread
 
-// f / 2 pi as a 64-bit fraction of a turn (whole turns drop out).  The quotient is kept as an
+// f / 2 pi as a 64-bit fraction of a turn (whole turns drop out), to nearest.  The quotient is kept as an
 // unevaluated sum hi + lo: 1 / 2 pi to twice the precision of a double.
 __device__ __forceinline__ uint64_t turns_of(double f) {
   constexpr double kInv2Pi = 0x1.45f306dc9c883p-3;     // 1 / 2 pi, the nearest double
@@ -54,8 +53,9 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
   const double hi = f * kInv2Pi;
   const double lo = fma(f, kInv2Pi, -hi) + f * kInv2PiLo;
   const double frac = hi - floor(hi);  // [0, 1]; 1 only by rounding, and then it wraps to 0
-  const uint64_t a = frac >= 1.0 ? 0ull : __double2ull_rz(frac * 0x1p64);
-  return a + static_cast<uint64_t>(__double2ll_rn(lo * 0x1p64));
+  const double scaled = frac >= 1.0 ? 0.0 : frac * 0x1p64, whole = floor(scaled);
+  // (what hi has below 2^-64, as small frequencies do, is rounded together with lo)
+  return __double2ull_rz(whole) + static_cast<uint64_t>(__double2ll_rn(lo * 0x1p64 + (scaled - whole)));
 }
 
 // cos and sin of `turns` 2^-64 of a turn
