@@ -324,7 +324,7 @@ struct MmaMath {
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int h = 8 * n + 2 * t4 + hh;
-        slope_[kMod ? n : 0][hh] = slopes && h < nh ? __ldg(slopes + h) * kLog2e : 0.f;
+        slope_[kMod ? n : 0][hh] = slopes && h < nh ? slope_log2(__ldg(slopes + h)) : 0.f;
       }
   }
 
@@ -725,7 +725,7 @@ struct SimtMath {
     for (int k = 0; k < NGH * X; ++k) qv[k] = DType<T>::to_f32(qh[k]);
   }
 
-  __device__ __forceinline__ void load_slopes(const float* slopes, int) { slope_ = slopes ? __ldg(slopes) * kLog2e : 0.f; }
+  __device__ __forceinline__ void load_slopes(const float* slopes, int) { slope_ = slopes ? slope_log2(__ldg(slopes)) : 0.f; }
 
   __device__ __forceinline__ void set_columns(int) {}
 

@@ -125,6 +125,15 @@ template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t u)
   return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u));
 }
 
+// ---- biases --------------------------------------------------------------------------------
+
+// The bias of a head per position of distance, in log2 units: slope log2(e), limited to 2^95, so that with distances
+// below 2^31 no score overflows (a position's own bias, 0 times its slope, would not be a number, nor the difference of
+// two infinite scores).  A position more changes scores by more than any cap either way.
+__device__ __forceinline__ float slope_log2(float slope) {
+  return fminf(fmaxf(slope * 1.4426950408889634f, -0x1p95f), 0x1p95f);
+}
+
 // ---- tanh ------------------------------------------------------------------------------------
 
 // tanh(t) / t for |t| <= 1/2, u = t^2: a fit that is minimax in relative error (Lawson's iteration), off

@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int from = 0;
         float slope = 0.f;
         if (p.window > 0) from = max(0, pos - (p.window - 1));  // (from - k0c below would not fit an int otherwise)
-        if constexpr (kBias) slope = __ldg(p.slopes + U.kvh * G + (valid ? row % G : 0)) * kLog2e;
+        if constexpr (kBias) slope = slope_log2(__ldg(p.slopes + U.kvh * G + (valid ? row % G : 0)));
         float m = -INFINITY, l = 0.f;
         for (int c = 0; c < U.nchunks; ++c, ++cx) {
           // tcgen05.ld / st are warp-collective (.sync.aligned): every branch around them
