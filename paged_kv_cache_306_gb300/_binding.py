@@ -465,6 +465,7 @@ def _masked_tables(q, block_tables, seq_lens, alibi_slopes):
     import torch
     _need_here("block_tables", block_tables, torch.int32, 2)
     _need_here("seq_lens", seq_lens, torch.int32, 1)
+    _int32("max_blocks_per_seq", block_tables.shape[1])
     if block_tables.shape[0] != seq_lens.shape[0]:
         raise PAError(PA_ERR_INVALID_ARG, "block_tables and seq_lens must have one row per sequence")
     if alibi_slopes is not None:
@@ -598,6 +599,11 @@ def _rope_args(q_out, q, key, positions, inv_freq):
     return sq, sk
 
 
+def _rope_sizes(q, key, inv_freq):
+    return (_int32("num_heads", q.shape[1]), _int32("num_kv_heads", key.shape[1]), _int32("head_size", q.shape[2]),
+            _int32("rotary_dim", 2 * inv_freq.shape[0]))
+
+
 def pa_rope(q_out, key_out, q, key, positions, inv_freq, layout=ROPE_HALVES, amplitude=1.0, stream=None):
     """Rotary positions: q [T, H, D] and key [T, Hkv, D] (rows may lie apart, as views of one projection's)
     turned by positions (int64 [T]) times inv_freq (float64 [rotary dims / 2]) into q_out and key_out
@@ -613,8 +619,8 @@ def pa_rope(q_out, key_out, q, key, positions, inv_freq, layout=ROPE_HALVES, amp
     if key_out.shape != key.shape:
         raise PAError(PA_ERR_INVALID_ARG, "key_out and key differ in shape")
     T, H, D = q.shape
-    check(load().pa_rope(_ptr(q_out), _ptr(key_out), _ptr(q), _ptr(key), sq, sk, _ptr(positions), _ptr(inv_freq), T, H,
-                         key.shape[1], D, 2 * inv_freq.shape[0], _int32("layout", layout), float(amplitude), dtype_code(q.dtype),
+    check(load().pa_rope(_ptr(q_out), _ptr(key_out), _ptr(q), _ptr(key), sq, sk, _ptr(positions), _ptr(inv_freq), T,
+                         *_rope_sizes(q, key, inv_freq), _int32("layout", layout), float(amplitude), dtype_code(q.dtype),
                          _stream(stream)))
 
 
@@ -646,8 +652,9 @@ def pa_rope_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_ma
     if slot_mapping.shape[0] != T:
         raise PAError(PA_ERR_INVALID_ARG, "slot_mapping must have one entry per token")
     check(load().pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(key), _ptr(value), sq, sk, sv, _ptr(k_cache),
-                                   _ptr(v_cache), _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), T, H, hkv, D,
-                                   2 * inv_freq.shape[0], bs, nb, _int32("layout", layout), float(amplitude), dtype_code(q.dtype),
+                                   _ptr(v_cache), _ptr(positions), _ptr(slot_mapping), _ptr(inv_freq), T,
+                                   *_rope_sizes(q, key, inv_freq), _int32("block_size", bs), nb,
+                                   _int32("layout", layout), float(amplitude), dtype_code(q.dtype),
                                    dtype_code(k_cache.dtype), float(k_scale), float(v_scale), _stream(stream)))
 
 
