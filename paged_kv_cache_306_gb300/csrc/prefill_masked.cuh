@@ -598,26 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int form = 0;
           float mx = -INFINITY;
           if (seen) {
-            // Capped without a bias, where the warp's rows see the half whole: the tanh keeps the order of the
-            // scores, so the row's maximum is that of the raw ones, and the cap is taken within the exponentials'
-            // loop below, by the form that the scores' size allows (so that its multiply-adds run beside the
-            // exponentials).  Elsewhere, and where no form serves all of the scores, they are changed and hidden first,
-            // in TMEM.
-            bool change = kBias || __any_sync(0xffffffffu, lo > 0 || lim < kHalf - 1);
-            if (!change) {
-              float sv[kHalf];
-              ld64(t_h, sv);
-              mx = largest(sv) * sl2;  // (scale > 0 keeps the order)
-              if constexpr (kCap) {
-                const float size = fmaxf(mx, -smallest(sv));
-                const bool past = __any_sync(0xffffffffu, size > p.tanh_wide_to);
-                change = past && p.cap_log2 > kSmallCap;
-                form = past ? 3 : __any_sync(0xffffffffu, size > p.tanh_near_to) ? 2 : 1;
-                mx = cap_any(mx * p.scale_log2, p.cap_log2, p.cap_inv);
-              }
-            }
-            if (change) {
-              form = 0;
+            auto hide = [&]() {  // the scores changed and hidden, in TMEM, and their maximum
               mx = -INFINITY;
 #pragma unroll 1
               for (int k0 = 0; k0 < kHalf; k0 += kStep) {
@@ -637,6 +618,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx = fmaxf(mx, largest(sv) * sl2);
                 st32(t_h + k0, sv);
               }
+            };
+            // Capped without a bias, where the warp's rows see the half whole: the tanh keeps the order of the
+            // scores, so the row's maximum is that of the raw ones, and the cap is taken within the exponentials'
+            // loop below, by the form that the scores' size allows (so that its multiply-adds run beside the
+            // exponentials).  Elsewhere, and where no form serves all of the scores, they are changed first.
+            const bool whole = !kBias && !__any_sync(0xffffffffu, lo > 0 || lim < kHalf - 1);
+            float sv[kHalf];
+            if constexpr (kCap) {
+              bool change = !whole;
+              if (whole) {
+                ld64(t_h, sv);
+                mx = largest(sv);  // (scale > 0 keeps the order)
+                const float size = fmaxf(mx, -smallest(sv));
+                const bool past = __any_sync(0xffffffffu, size > p.tanh_wide_to);
+                change = past && p.cap_log2 > kSmallCap;
+                form = change ? 0 : past ? 3 : __any_sync(0xffffffffu, size > p.tanh_near_to) ? 2 : 1;
+                mx = cap_any(mx * p.scale_log2, p.cap_log2, p.cap_inv);
+              }
+              if (change) hide();
+            } else if (whole) {
+              ld64(t_h, sv);
+              mx = largest(sv) * sl2;  // (scale > 0 keeps the order)
+            } else {
+              hide();
             }
           }
           {
