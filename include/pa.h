@@ -45,12 +45,10 @@
  *     affected outputs are unspecified, and the first such error is recorded
  *     for pa_get_device_error().
  *   - Kernels are chained by programmatic dependent launch: a decode kernel may
- *     start while the previous kernel in the stream (another call of this
- *     library) finishes, and reads seq_lens and the prefix groups before it waits
- *     for that kernel; everything else it reads or writes it touches after.  A
- *     caller kernel that writes seq_lens or the prefix groups must not release
- *     its dependents early (griddepcontrol.launch_dependents) before those writes;
- *     an ordinary kernel never does.
+ *     start while the previous kernel in the stream finishes.  What it reads of
+ *     seq_lens and the prefix groups before it waits for that kernel is read again
+ *     behind the wait, and only the later values count; everything else it reads or
+ *     writes it touches after.  So any kernel may write a call's inputs right before it.
  *   - Thread safety: calls may be made from several host threads; the
  *     device-error word and the launch counter are shared per process.
  *   - The library looks up the device addresses of its own device-side objects
@@ -399,7 +397,7 @@ PA_API pa_status pa_prefill(void* out, const void* q, const void* k_cache, const
  *
  * softcap       0 (none), or in [2^-64, 2^64]
  * alibi_slopes  fp32 [num_heads], finite, 4-byte aligned; NULL: no bias.  The bias is
- *               computed in fp32.
+ *               computed in fp32, slopes past 2^94 in size as about 2^94.
  * window        positions the query sees, its own among them; 0: all
  *
  * Nothing before the window is read: block-table entries of blocks that end before it

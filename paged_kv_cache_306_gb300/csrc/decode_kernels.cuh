@@ -1081,8 +1081,9 @@ __device__ __forceinline__ void shared_layout(const DecodeParams& p, int* s_pre,
 // most two that do not hold their whole segment, its first and its last; the last one (or the only one) lies in the
 // warp's ring, whose copies have all been used by then, the other where caller partitions would keep
 // their running state (there are none).  s_piece[2 w], s_piece[2 w + 1]: the segments of warp w's pieces in the state
-// and in the ring, -1: none; s_piece[2 warps]: a warp's wait ran out, so that pieces are missing, and nothing is merged.  (A launch that small is all latency: one short sequence took 6.4 us with the merge as a
-// kernel of its own, 5.1 with it here.)
+// and in the ring, -1: none; s_piece[2 warps]: a warp's wait ran out, so that pieces are missing, and nothing is merged.
+// (A launch that small is all latency: one short sequence took 6.4 us with the merge as a kernel of its own, 5.1 with it
+// here; 4.8 now.)
 template <typename T, int D, bool kMma, int kRows>
 __device__ __forceinline__ void merge_here(const DecodeParams& p, const int* s_piece, const float* states, const unsigned char* rings,
                                            int ring_bytes, int warp, int warps, int lane) {
@@ -1145,9 +1146,10 @@ using DecodeArgs = std::conditional_t<kMod, DecodeMaskedParams, DecodeParams>;
 // kMod: capped or biased scores and windows (pa_decode_masked); no fused step, no shared
 // prefixes.  A window of w tokens leaves each sequence the blocks from (L - w) / BS on: they
 // are its work, and nothing before them is looked up or read.
-// What that costs: a capped score a reciprocal and an exponential more, hidden by the copies -- 64 sequences of
-// 512 .. 4096 tokens, 28/4 heads of 128 dims, fp16, cap 50, window 1024 (130 MB to read) take 30 us, a plain call over
-// 1024 tokens each 29; 4 x 32K .. 131K capped (1.46 GB) 226 us, 97% of a copy's rate.
+// What that costs: a capped score 8 multiplications and additions more (past half the cap a reciprocal and an
+// exponential too), hidden by the copies where a CTA has many -- 64 sequences of 512 .. 4096 tokens, 28/4 heads of 128
+// dims, fp16, window 1024 (130 MB to read) take 30.1 us, with cap 50 30.5, a plain call over 1024 tokens each 29.2;
+// 4 x 32K .. 131K capped (1.46 GB) 222 us, 98% of a copy's rate; 64 x 2048 from L2 50.5 us for the plain call's 49.2.
 template <typename T, typename TC, int D, int BS, int kMode, bool kMod>
 __global__ void __launch_bounds__(DecodeShape<TC, D, BS, kMode>::kWarps * 32, 1)
     decode_kernel(const DecodeArgs<kMod> p) {

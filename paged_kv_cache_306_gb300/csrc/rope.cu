@@ -10,9 +10,10 @@
 // The angle.  Positions are whole numbers, so the angle is taken in turns and fixed
 // point: with F_i = f_i / 2 pi as a 64-bit fraction of a turn, p F_i mod 2^64 is the
 // product's low word -- the reduction to one turn costs nothing and is exact for every
-// position, and the error is that of F_i alone, which is rounded once: |p| 2^-65 turns, whatever f_i.  What is left after the nearest quarter turn lies within 1/8 turn, so as
-// fp32 it is off by at most 2^-28 turns, and sincospif finishes it.  (fp64 per token and pair
-// would be bound by this GPU's fp64 rate; f_i / 2 pi is computed in fp64 once per CTA.)
+// position, and the error is that of F_i alone, which is rounded once: |p| 2^-65 turns, whatever f_i.
+// What is left after the nearest quarter turn lies within 1/8 turn, so as fp32 it is off by at most
+// 2^-28 turns, and sincospif finishes it.  (fp64 per token and pair would be bound by this GPU's fp64
+// rate; f_i / 2 pi is computed in fp64 once per CTA.)
 //
 // Work.  A unit is two 16-byte pieces of a row: the two halves' pieces of the same pairs,
 // or two neighbouring ones.  A CTA takes a tile of up to 16 tokens and some of their rows (q heads, then k heads,
@@ -25,8 +26,10 @@
 //
 // What bounds it: memory.  16384 tokens of 32 + 8 heads of 128 dims in bf16, 64 of them turned (336 MB): 53.8 us,
 // 6.2 TB/s, 93% of a copy's rate.  8192 tokens of 28 + 4 + 4 heads in fp16 into the pools (151 MB): 28 us, 5.4 TB/s;
-// what lies between is V, two bytes to each place.  One token: 2.5 us in a graph, latency: the launch, the frequencies,
-// a row.
+// what lies between is V, two bytes to each place.  fp32 rows: 16381 tokens of 32 + 8 heads (671 MB) 125.5 us, 5.3 TB/s;
+// 8192 of 28 + 4 + 4 into the pools (302 MB) 50 us, 6.0 TB/s.  FP8 pools: 1537 tokens of 32 + 8 + 8 heads (35 MB) 8.6 us
+// from L2, 11.1 from memory: V is 16 stores of a byte a unit.  One token: 2.2 us in a graph, latency: the launch, the
+// frequencies, a row.
 #include <stdint.h>
 
 #include <numeric>
