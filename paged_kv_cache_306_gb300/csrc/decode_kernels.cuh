@@ -1114,7 +1114,7 @@ __device__ __forceinline__ void merge_here(const DecodeParams& p, const int* s_p
     float top = m;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    const float w = m == -INFINITY ? 0.f : l * exp2f(m - top);
+    const float w = m == -INFINITY ? l : l * exp2f(m - top);
     float sum = w, acc[CPL] = {};
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
@@ -1794,7 +1794,8 @@ __global__ void __launch_bounds__(kMergeRows * 32, 2) decode_merge_kernel(const 
     float mc = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, o));
-    const float w = m == -INFINITY ? 0.f : l * exp2f(m - mc);
+    // (a piece without a score has l = 0; one whose scores are no numbers, an l that is none: it makes the row NaN too)
+    const float w = m == -INFINITY ? l : l * exp2f(m - mc);
     float lc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) lc += __shfl_xor_sync(0xffffffffu, lc, o);
@@ -1815,14 +1816,14 @@ __global__ void __launch_bounds__(kMergeRows * 32, 2) decode_merge_kernel(const 
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
-        if (i0 + i < n && wi > 0.f) {  // a slot no piece wrote in this launch holds anything (NaN too)
+        if (i0 + i < n && wi != 0.f) {  // a slot no piece wrote in this launch holds anything (NaN too)
           const float* v = reinterpret_cast<const float*>(&ov[i]);
 #pragma unroll
           for (int c = 0; c < CPL; ++c) oc[c] = fmaf(wi, v[c], oc[c]);
         }
       }
     }
-    if (lc > 0.f) {
+    if (lc != 0.f) {
       const float mn = fmaxf(RM, mc);
       const float fa = exp2f(RM - mn), fb = exp2f(mc - mn);
       RL = RL * fa + lc * fb;
@@ -1845,7 +1846,7 @@ __global__ void __launch_bounds__(kMergeRows * 32, 2) decode_merge_kernel(const 
 #pragma unroll
     for (int c = 0; c < CPL; ++c) RO[c] = 0.f;
     for (int j = 0; j < kMergeRows; ++j) {
-      if (!(s_l[j] > 0.f)) continue;
+      if (s_l[j] == 0.f) continue;
       const float mn = fmaxf(RM, s_m[j]);
       const float fa = exp2f(RM - mn), fb = exp2f(s_m[j] - mn);
       RL = RL * fa + s_l[j] * fb;
