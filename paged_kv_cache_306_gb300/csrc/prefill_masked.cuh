@@ -17,11 +17,12 @@
 //     beside the softmax's own one: 452 us for 16 chunks of 512 tokens behind 3584 (28 heads of 128 dims, fp16), which
 //     take 283 us uncapped; and it is off by a share of the cap, whatever the score.  So: the tanh keeps the scores'
 //     order, the row's maximum is the raw scores' one, and the cap becomes an odd polynomial in the raw score within the
-//     exponentials' loop, its multiply-adds (128 a clock and SM) beside the exponentials: 4 terms where all scores of the warp's half chunk lie within cap / 2 (358 us), 6 within
-//     cap (397 us), the exponential form past it (with a large cap for the scores that need it alone: cap_any,
-//     cap_small).  Their coefficients serve any cap (set_tanh): 358 us at caps of 500 and 10^6 too.  (Polynomials over
-//     all scores first, then the softmax: 403 us for the 4 terms; so now only where a mask cuts the half, or with a
-//     bias, after which the maximum is another one: 361 us biased, 488 us capped and biased.)
+//     exponentials' loop, its multiply-adds (128 a clock and SM) beside the exponentials: 4 terms where all scores of
+//     the warp's half chunk lie within cap / 2 (358 us), 6 within cap (397 us), the exponential form past it (with a
+//     large cap for the scores that need it alone: cap_any, cap_small).  The coefficients serve any cap (set_tanh): 358 us
+//     at caps of 500 and 10^6 too.  (Polynomials over all scores first, then the softmax: 403 us for the 4 terms; so now
+//     only where a mask cuts the half, or with a bias, after which the maximum is another one: 361 us biased, 488 us
+//     capped and biased.)
 //   * Two threads to a row, one for each half of a chunk's keys, which exchange their maxima; each reads
 //     its scores twice, for the maximum and for P, and keeps 32 in registers at a time.  A row's softmax is a
 //     step of the chain S, softmax, P V, S; halved, 16 chunks of 512 tokens with capped scores in a window of 1024 take
